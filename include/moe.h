@@ -422,6 +422,70 @@ int moe_time_next_launch(int32_t which, void* ev_begin, void* ev_end);
 int moe_read_probe(const void* buf, uint64_t bytes, uint32_t* sink, int32_t blocks, void* stream);
 
 
+/* ---- Operators beside the layer -------------------------------------------
+ * What joins the layer to the rest of a model: the norms, gate and residual
+ * scale around a block (moe_join_*), products grouped by expert on 16-bit
+ * weights with their gradients (moe_grouped_*), and the low-rank adapters of
+ * many requests beside a shared projection (moe_adapter_project). They follow
+ * the conventions above (device pointers, `stream`, error codes, nothing
+ * allocated, nothing kept) with their own shapes and these element types: */
+#define MOE_TYPE_BF16 0
+#define MOE_TYPE_FP16 1
+#define MOE_TYPE_F32 2   /* where a field says so */
+
+/* Bits that the device ORs into a call's optional status word (int32 on the
+ * device, set to 0 by the caller) when the data of an index array is invalid;
+ * the call stays inside its buffers in any case. */
+#define MOE_STATUS_BAD_OFFSETS 8   /* moe_grouped_*: offsets not ascending, or outside [0, rows] */
+#define MOE_STATUS_BAD_ADAPTER 16  /* moe_adapter_project: an index outside [-1, n_adapters)      */
+
+/* Joining a block to the residual stream. For each of m rows, with f32
+ * arithmetic from the loaded values to the one rounding of each output:
+ *   z  = b * rsqrt(mean(b^2) + eps) * w_post   (w_post NULL: z = b)
+ *   x' = x + scale * gate * z                  (gate NULL: 1)
+ *   y  = x' * rsqrt(mean(x'^2) + eps) * w_pre  (w_pre NULL: y is not made)
+ * b is the output of the block before, x' the residual stream after it, y the
+ * input of the next block. b NULL: no block yet, x' = x; y then is the norm of
+ * x, and x_out may be NULL. y uses x' before its rounding to the stream's type.
+ *   x, x_out   residual type [m][dim], rows `*_stride` elements apart
+ *   b, y       type [m][dim]
+ *   w_post, w_pre  type [dim]
+ *   gate       type [dim] (gate_rows 0), or [m][dim] with rows gate_stride apart
+ * x_out may be x, and y may be b, in place. Rows must not overlap. Any dim
+ * from 1 to MOE_JOIN_MAX_DIM and any element alignment; 1 <= m < 2^22. */
+#define MOE_JOIN_MAX_DIM 16384
+typedef struct moe_join {
+  int32_t dim;
+  int32_t type;          /* MOE_TYPE_BF16 or MOE_TYPE_FP16 */
+  int32_t residual_type; /* type, or MOE_TYPE_F32          */
+  int32_t gate_rows;     /* 1: a gate per row              */
+  float scale;           /* finite                         */
+  float eps;             /* > 0                            */
+  int64_t x_stride;      /* elements between rows, >= dim: x and dx            */
+  int64_t x_out_stride;  /* x_out and dx_out                                  */
+  int64_t b_stride;      /* b and db                                          */
+  int64_t gate_stride;   /* gate and dgate with gate_rows 1                   */
+  int64_t y_stride;      /* y and dy                                          */
+} moe_join;
+int moe_join_forward(const moe_join* j, const void* x, const void* b, const void* w_post, const void* gate,
+                     const void* w_pre, int64_t m, void* x_out, void* y, void* stream);
+
+/* The gradients of moe_join_forward. dy is y's gradient, dx_out the one that
+ * reaches x' from elsewhere (either may be NULL: zero; not both); x_out is the
+ * stream that the forward call wrote; b, w_post, gate, w_pre its inputs.
+ *   dx     residual type [m][dim]
+ *   db     type [m][dim], may be NULL
+ *   dw_post, dw_pre  f32 [dim], may be NULL: sums over the rows
+ *   dgate  f32 [dim] summed over the rows (gate_rows 0) or type [m][dim], may be NULL
+ * dx may be dx_out, and db may be b, in place. Every output is written whole (nothing is added to
+ * what was there). The sums over rows run in a fixed order: the same call
+ * gives the same bits. ws: moe_join_workspace_bytes(j, m) bytes, 256-byte
+ * aligned, uninitialised; not needed (NULL) where no sum over rows is asked for. */
+size_t moe_join_workspace_bytes(const moe_join* j, int64_t max_m);
+int moe_join_backward(const moe_join* j, const void* dy, const void* dx_out, const void* x_out, const void* b,
+                      const void* w_post, const void* gate, const void* w_pre, int64_t m, void* dx, void* db,
+                      float* dw_post, void* dgate, float* dw_pre, void* ws, size_t ws_bytes, void* stream);
+
 const char* moe_last_error(void);
 
 #ifdef __cplusplus

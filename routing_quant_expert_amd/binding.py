@@ -103,6 +103,10 @@ def lib():
         L.moe_cache_get_stats.argtypes = [_VP, ctypes.POINTER(CacheStats)]
         L.moe_cache_resident.argtypes = [_VP, ctypes.c_int32, _VP]
         L.moe_lru_simulate.argtypes = [ctypes.c_int32, ctypes.c_int64, _VP, _VP, ctypes.c_int32, _VP, _VP]
+        L.moe_join_forward.argtypes = [_VP] * 6 + [ctypes.c_int64, _VP, _VP, _VP]
+        L.moe_join_workspace_bytes.restype = ctypes.c_size_t
+        L.moe_join_workspace_bytes.argtypes = [_VP, ctypes.c_int64]
+        L.moe_join_backward.argtypes = [_VP] * 8 + [ctypes.c_int64] + [_VP] * 6 + [ctypes.c_size_t, _VP]
         L.moe_last_error.restype = ctypes.c_char_p
         _lib = L
     return _lib
@@ -320,3 +324,61 @@ def lru_simulate(n_slots: int, n_keys: int, batches):
     _check(lib().moe_lru_simulate(n_slots, n_keys, keys.ctypes.data, lens.ctypes.data, len(batches),
                                   slots.ctypes.data, miss.ctypes.data))
     return slots, miss
+
+
+# ---- operators beside the layer -------------------------------------------
+MOE_TYPE_BF16, MOE_TYPE_FP16, MOE_TYPE_F32 = 0, 1, 2
+MOE_STATUS_BAD_OFFSETS = 8
+MOE_STATUS_BAD_ADAPTER = 16
+MOE_JOIN_MAX_DIM = 16384
+
+
+def type_code(dtype) -> int:
+    """The MOE_TYPE_* code of a torch dtype (a code passes through)."""
+    if isinstance(dtype, int):
+        return dtype
+    code = {"torch.bfloat16": MOE_TYPE_BF16, "torch.float16": MOE_TYPE_FP16, "torch.float32": MOE_TYPE_F32}.get(
+        str(dtype))
+    if code is None:
+        raise MoeError(-1, f"element type must be bfloat16, float16 or float32 (got {dtype})")
+    return code
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+class Join(ctypes.Structure):
+    """moe_join: how a block joins a residual stream (norms after and before, gate, residual scale).
+    Strides default to contiguous rows of dim."""
+    _fields_ = [("dim", ctypes.c_int32), ("type", ctypes.c_int32), ("residual_type", ctypes.c_int32),
+                ("gate_rows", ctypes.c_int32), ("scale", ctypes.c_float), ("eps", ctypes.c_float),
+                ("x_stride", ctypes.c_int64), ("x_out_stride", ctypes.c_int64), ("b_stride", ctypes.c_int64),
+                ("gate_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64)]
+
+    def __init__(self, dim: int, dtype, residual=None, gate_rows: bool = False, scale: float = 1.0, eps: float = 1e-6,
+                 x_stride: int | None = None, x_out_stride: int | None = None, b_stride: int | None = None,
+                 gate_stride: int | None = None, y_stride: int | None = None):
+        t = type_code(dtype)
+        super().__init__(dim, t, t if residual is None else type_code(residual), int(gate_rows), scale, eps,
+                         *(dim if v is None else v for v in (x_stride, x_out_stride, b_stride, gate_stride, y_stride)))
+
+
+def join_forward(j: Join, x, block, w_post, gate, w_pre, x_out, y, stream=None):
+    """x_out = x + scale * gate * norm(block, w_post), y = norm(x_out, w_pre); block, w_post, gate, w_pre with y,
+    and (without a block) x_out may be None."""
+    _check(lib().moe_join_forward(ctypes.byref(j), _addr(x), _addr(block), _addr(w_post), _addr(gate), _addr(w_pre),
+                                  x.shape[0], _addr(x_out), _addr(y), _stream(stream)))
+
+
+def join_workspace_bytes(j: Join, max_m: int) -> int:
+    return int(lib().moe_join_workspace_bytes(ctypes.byref(j), max_m))
+
+
+def join_backward(j: Join, dy, dx_out, x_out, block, w_post, gate, w_pre, dx, dblock, dw_post, dgate, dw_pre, ws,
+                  stream=None):
+    """The gradients of join_forward: dx, dblock, dw_post, dgate, dw_pre (None where not wanted)."""
+    _check(lib().moe_join_backward(ctypes.byref(j), _addr(dy), _addr(dx_out), _addr(x_out), _addr(block),
+                                   _addr(w_post), _addr(gate), _addr(w_pre), dx.shape[0], _addr(dx), _addr(dblock),
+                                   _addr(dw_post), _addr(dgate), _addr(dw_pre), _addr(ws),
+                                   0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))

@@ -1,0 +1,73 @@
+// The 16-bit and f32 element types of the operators beside the layer: their
+// conversions, and loads and stores of up to 8 consecutive elements at any
+// element alignment (global accesses of gfx950 need no more).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/moe.h"
+
+namespace moe {
+
+typedef __bf16 bf16_t;
+typedef _Float16 fp16_t;
+
+template <typename T>
+struct elem_code;
+template <>
+struct elem_code<bf16_t> { static constexpr int value = MOE_TYPE_BF16; };
+template <>
+struct elem_code<fp16_t> { static constexpr int value = MOE_TYPE_FP16; };
+template <>
+struct elem_code<float> { static constexpr int value = MOE_TYPE_F32; };
+
+inline size_t elem_bytes(int type) { return type == MOE_TYPE_F32 ? 4 : 2; }
+
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef bf16_t bf16x8_t __attribute__((ext_vector_type(8)));
+typedef fp16_t fp16x8_t __attribute__((ext_vector_type(8)));
+
+// 8 consecutive elements in registers, as they are in memory.
+template <typename T>
+struct oct_of;
+template <>
+struct oct_of<bf16_t> { typedef bf16x8_t type; };
+template <>
+struct oct_of<fp16_t> { typedef fp16x8_t type; };
+template <>
+struct oct_of<float> { typedef f32x8 type; };
+template <typename T>
+using oct = typename oct_of<T>::type;
+
+template <typename V>
+__device__ __forceinline__ f32x8 to_f32(V v) { return __builtin_convertvector(v, f32x8); }
+
+// Elements p[0..7] of which the first n are there (n >= 8: all); the others are zero.
+template <typename T>
+__device__ __forceinline__ oct<T> load_oct(const T* p, int n) {
+  oct<T> o = {};
+  if (n >= 8) {
+    __builtin_memcpy(&o, p, 8 * sizeof(T));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (i < n) o[i] = p[i];
+  }
+  return o;
+}
+
+// The first n of f rounded to nearest even in T (infinities and NaN kept).
+template <typename T>
+__device__ __forceinline__ void store_oct(T* p, f32x8 f, int n) {
+  const oct<T> o = __builtin_convertvector(f, oct<T>);
+  if (n >= 8) {
+    __builtin_memcpy(p, &o, 8 * sizeof(T));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (i < n) p[i] = o[i];
+  }
+}
+
+}  // namespace moe

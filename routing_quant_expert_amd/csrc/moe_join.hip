@@ -1,0 +1,399 @@
+// Joining a block to the residual stream (moe_join_forward, moe_join_backward):
+// the norm after a block, its gate and residual scale, the residual add and
+// the norm before the next block as one pass over the rows, and its gradients.
+//
+//   z = b rb w_post, x' = x + s g z, y = x' rx w_pre,  r? = rsqrt(mean(.^2) + eps)
+// and backwards, with n = x' rx, dn = dy w_pre, nb = b rb, dz = s g dx:
+//   dx = dx_out + rx (dn - n mean(dn n)),  db = rb (dz w_post - nb mean(dz w_post nb)),
+//   dw_pre = sum dy n, dw_post = sum dz nb, dgate = s dx z.
+//
+// Bound by HBM: every operand is read once and every result written once, the
+// row stays in registers in between. A row belongs to TPR threads (one wave,
+// or a workgroup), thread t holding the chunks t, t + TPR, ... of 8 elements.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+
+#include "moe_element.h"
+#include "moe_host.h"
+#include "moe_wave.h"
+
+namespace moe {
+namespace {
+
+constexpr int kJoinThreads = 256;
+constexpr int64_t kJoinMaxRows = (int64_t)1 << 22;   // rows * 1024 threads stay below a launch's 2^32 threads
+
+struct JoinArgs {
+  int dim;
+  int gate_rows;
+  float scale, eps;
+  int64_t m;
+  int64_t x_stride, x_out_stride, b_stride, gate_stride, y_stride;
+};
+
+// Sums of N values over the TPR threads of a row, in every one of them. TPR =
+// 64: the wave's butterfly; more: the waves' sums meet in LDS (`buf` is used
+// by one call of the row; the next call takes the other buffer, so one barrier a call is enough).
+template <int TPR, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], float* buf) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = wave_sum_xor(v[i]);
+  if constexpr (TPR > 64) {
+    constexpr int W = TPR / 64;
+    const int wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) buf[i * W + wave] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float s = 0.0f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) s += buf[i * W + w];
+      v[i] = s;
+    }
+  }
+}
+
+__device__ __forceinline__ float sum_of_squares(f32x8 f) {
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s = fmaf(f[i], f[i], s);
+  return s;
+}
+
+__device__ __forceinline__ float dot8(f32x8 a, f32x8 b) {
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s = fmaf(a[i], b[i], s);
+  return s;
+}
+
+// (x_out may be x and y may be b: each thread has read what it overwrites.)
+template <typename T, typename RT, int TPR, int NC>
+__global__ __launch_bounds__(TPR < kJoinThreads ? kJoinThreads : TPR) void k_join(
+    JoinArgs a, const RT* x, const T* b, const T* __restrict__ w_post, const T* __restrict__ gate,
+    const T* __restrict__ w_pre, RT* x_out, T* y) {
+  constexpr int kRows = TPR < kJoinThreads ? kJoinThreads / TPR : 1;
+  __shared__ float buf[2][TPR / 64];
+  const int t = threadIdx.x % TPR;
+  const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
+  if (row >= a.m) return;   // whole waves; with TPR > 64 the whole workgroup
+  f32x8 xv[NC];
+  const float inv_dim = 1.0f / (float)a.dim;
+  oct<RT> xr[NC];
+  oct<T> br[NC];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int c = 8 * (t + TPR * i);
+    if (b) br[i] = load_oct(b + row * a.b_stride + c, a.dim - c);
+    xr[i] = load_oct(x + row * a.x_stride + c, a.dim - c);
+  }
+  if (b) {
+    float rb = 1.0f;
+    if (w_post) {
+      float s[1] = {0.0f};
+#pragma unroll
+      for (int i = 0; i < NC; ++i) s[0] += sum_of_squares(to_f32(br[i]));
+      row_sums<TPR>(s, buf[0]);
+      rb = 1.0f / sqrtf(s[0] * inv_dim + a.eps);
+    }
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = 8 * (t + TPR * i);
+      f32x8 z = to_f32(br[i]);
+      if (w_post) z = z * rb * to_f32(load_oct(w_post + c, a.dim - c));
+      if (gate) z = z * to_f32(load_oct(gate + (a.gate_rows ? row * a.gate_stride : 0) + c, a.dim - c));
+      xv[i] = to_f32(xr[i]) + a.scale * z;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) xv[i] = to_f32(xr[i]);
+  }
+  if (x_out) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = 8 * (t + TPR * i);
+      store_oct(x_out + row * a.x_out_stride + c, xv[i], a.dim - c);
+    }
+  }
+  if (!w_pre) return;
+  float s[1] = {0.0f};
+#pragma unroll
+  for (int i = 0; i < NC; ++i) s[0] += sum_of_squares(xv[i]);
+  row_sums<TPR>(s, buf[1]);
+  const float rx = 1.0f / sqrtf(s[0] * inv_dim + a.eps);
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int c = 8 * (t + TPR * i);
+    store_oct(y + row * a.y_stride + c, xv[i] * rx * to_f32(load_oct(w_pre + c, a.dim - c)), a.dim - c);
+  }
+}
+
+// The gradients: workgroup p takes the rows p, p + P, ... (P workgroups), so
+// that its threads keep the sums over rows of their columns in registers; they
+// are written as f32 partial sums [P][3][dim] that k_join_sums adds up.
+template <typename T, typename RT, int TPR, int NC>
+__global__ __launch_bounds__(TPR) void k_join_back(JoinArgs a, const T* __restrict__ dy, const RT* dxo,
+                                                   const RT* __restrict__ xo, const T* b,
+                                                   const T* __restrict__ w_post, const T* __restrict__ gate,
+                                                   const T* __restrict__ w_pre, RT* dx, T* db,
+                                                   T* __restrict__ dgate_rows,
+                                                   float* __restrict__ part, int sums) {
+  __shared__ float buf[2][3 * (TPR / 64)];
+  const int t = threadIdx.x;
+  const float inv_dim = 1.0f / (float)a.dim;
+  f32x8 s_pre[NC] = {}, s_post[NC] = {}, s_gate[NC] = {};
+  for (int64_t row = blockIdx.x; row < a.m; row += gridDim.x) {
+    f32x8 xv[NC], dn[NC], g[NC];
+    float s[3] = {0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = 8 * (t + TPR * i), left = a.dim - c;
+      if (dxo) g[i] = to_f32(load_oct(dxo + row * a.x_out_stride + c, left));
+      else g[i] = f32x8{};
+      if (dy) {
+        xv[i] = to_f32(load_oct(xo + row * a.x_out_stride + c, left));
+        dn[i] = to_f32(load_oct(dy + row * a.y_stride + c, left));
+        const f32x8 d = dn[i] * to_f32(load_oct(w_pre + c, left));
+        s[0] += sum_of_squares(xv[i]);
+        s[1] += dot8(d, xv[i]);
+      }
+      if (b && w_post) s[2] += sum_of_squares(to_f32(load_oct(b + row * a.b_stride + c, left)));
+    }
+    row_sums<TPR>(s, buf[0]);
+    const float rx = 1.0f / sqrtf(s[0] * inv_dim + a.eps);
+    const float c1 = s[1] * rx * rx * inv_dim;   // mean(dn n) rx: n mean(dn n) = x' c1
+    const float rb = b && w_post ? 1.0f / sqrtf(s[2] * inv_dim + a.eps) : 1.0f;
+    float q[1] = {0.0f};
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = 8 * (t + TPR * i), left = a.dim - c;
+      if (dy) {
+        s_pre[i] += dn[i] * (xv[i] * rx);
+        g[i] += rx * (dn[i] * to_f32(load_oct(w_pre + c, left)) - xv[i] * c1);
+      }
+      store_oct(dx + row * a.x_stride + c, g[i], left);
+      if (!b) continue;
+      const f32x8 nb = to_f32(load_oct(b + row * a.b_stride + c, left)) * rb;
+      f32x8 dz = g[i] * a.scale;
+      f32x8 z = nb;
+      f32x8 wp;
+      if (w_post) {
+        wp = to_f32(load_oct(w_post + c, left));
+        z = z * wp;
+      }
+      if (gate) {
+        const f32x8 dg = dz * z;
+        if (a.gate_rows) {
+          if (dgate_rows) store_oct(dgate_rows + row * a.gate_stride + c, dg, left);
+        } else {
+          s_gate[i] += dg;
+        }
+        dz = dz * to_f32(load_oct(gate + (a.gate_rows ? row * a.gate_stride : 0) + c, left));
+      }
+      if (w_post) {
+        s_post[i] += dz * nb;
+        dz = dz * wp;
+        q[0] += dot8(dz, nb);
+      }
+      g[i] = dz;
+    }
+    if (db) {
+      if (w_post) row_sums<TPR>(q, buf[1]);
+      const float c2 = q[0] * inv_dim;
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int c = 8 * (t + TPR * i), left = a.dim - c;
+        f32x8 d = g[i];
+        if (w_post) d = rb * (d - to_f32(load_oct(b + row * a.b_stride + c, left)) * (rb * c2));
+        store_oct(db + row * a.b_stride + c, d, left);
+      }
+    }
+    if (!(db && w_post) && TPR > 64) __syncthreads();   // buf[0] is written again by the next row
+  }
+  if (!sums) return;
+  float* out = part + (int64_t)blockIdx.x * 3 * a.dim;
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int c = 8 * (t + TPR * i), left = a.dim - c;
+    if (left <= 0) break;
+    store_oct(out + c, s_pre[i], left);
+    store_oct(out + a.dim + c, s_post[i], left);
+    store_oct(out + 2 * (int64_t)a.dim + c, s_gate[i], left);
+  }
+}
+
+// Column sums of the partial sums [parts][3 * dim], in a fixed order: 64
+// columns a workgroup, wave w adding the rows w, w + 4, ...
+__global__ __launch_bounds__(256) void k_join_sums(const float* __restrict__ part, int parts, int dim,
+                                                   float* __restrict__ dw_pre, float* __restrict__ dw_post,
+                                                   float* __restrict__ dgate) {
+  __shared__ float buf[4][64];
+  const int which = blockIdx.y;
+  float* out = which == 0 ? dw_pre : which == 1 ? dw_post : dgate;
+  if (!out) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int col = blockIdx.x * 64 + lane;
+  float s = 0.0f;
+  if (col < dim)
+    for (int p = wave; p < parts; p += 4) s += part[((int64_t)p * 3 + which) * dim + col];
+  buf[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && col < dim) out[col] = (buf[0][lane] + buf[1][lane]) + (buf[2][lane] + buf[3][lane]);
+}
+
+// Workgroups of the gradient kernel for m rows.
+int join_parts(int64_t m) { return (int)(m < 512 ? (m < 1 ? 1 : m) : 512); }
+
+int check_join(const moe_join* j, int64_t m) {
+  if (!j) return fail(MOE_EINVAL, "join is NULL%s%lld");
+  if (j->type != MOE_TYPE_BF16 && j->type != MOE_TYPE_FP16)
+    return fail(MOE_EINVAL, "join: type must be MOE_TYPE_BF16 or MOE_TYPE_FP16%s (%lld)", "", j->type);
+  if (j->residual_type != j->type && j->residual_type != MOE_TYPE_F32)
+    return fail(MOE_EINVAL, "join: residual_type must be type or MOE_TYPE_F32%s (%lld)", "", j->residual_type);
+  if (j->gate_rows != 0 && j->gate_rows != 1)
+    return fail(MOE_EINVAL, "join: gate_rows must be 0 or 1%s (%lld)", "", j->gate_rows);
+  if (!std::isfinite(j->scale) || !(j->eps > 0.0f) || !std::isfinite(j->eps))
+    return fail(MOE_EINVAL, "join: scale must be finite and eps finite and > 0%s%lld");
+  if (j->dim < 1) return fail(MOE_EINVAL, "join: dim must be >= 1%s (%lld)", "", j->dim);
+  if (j->dim > MOE_JOIN_MAX_DIM) return fail(MOE_EUNSUPPORTED, "join: dim above MOE_JOIN_MAX_DIM%s (%lld)", "", j->dim);
+  if (j->x_stride < j->dim || j->x_out_stride < j->dim || j->b_stride < j->dim || j->y_stride < j->dim ||
+      (j->gate_rows && j->gate_stride < j->dim))
+    return fail(MOE_EINVAL, "join: a row stride is below dim%s (%lld)", "", j->dim);
+  if (m < 1) return fail(MOE_EINVAL, "m must be >= 1%s (m %lld)", "", m);
+  if (m >= kJoinMaxRows) return fail(MOE_EUNSUPPORTED, "join: too many rows%s (m %lld)", "", m);
+  return MOE_OK;
+}
+
+// An element pointer is aligned to its element.
+bool off_element(const void* p, int type) { return (uintptr_t)p % elem_bytes(type) != 0; }
+
+JoinArgs join_args(const moe_join& j, int64_t m) {
+  return {j.dim, j.gate_rows, j.scale, j.eps, m, j.x_stride, j.x_out_stride, j.b_stride, j.gate_stride, j.y_stride};
+}
+
+template <typename T, typename RT, int TPR, int NC>
+void launch_join_as(const JoinArgs& a, const void* x, const void* b, const void* w_post, const void* gate,
+                    const void* w_pre, void* x_out, void* y, hipStream_t s) {
+  constexpr int kRows = TPR < kJoinThreads ? kJoinThreads / TPR : 1;
+  k_join<T, RT, TPR, NC><<<dim3((unsigned)((a.m + kRows - 1) / kRows)), dim3(kRows * TPR), 0, s>>>(
+      a, (const RT*)x, (const T*)b, (const T*)w_post, (const T*)gate, (const T*)w_pre, (RT*)x_out, (T*)y);
+}
+
+template <typename T, typename RT>
+void launch_join(const JoinArgs& a, const void* x, const void* b, const void* w_post, const void* gate,
+                 const void* w_pre, void* x_out, void* y, hipStream_t s) {
+  if (a.dim <= 512) launch_join_as<T, RT, 64, 1>(a, x, b, w_post, gate, w_pre, x_out, y, s);
+  else if (a.dim <= 1024) launch_join_as<T, RT, 64, 2>(a, x, b, w_post, gate, w_pre, x_out, y, s);
+  else if (a.dim <= 2048) launch_join_as<T, RT, 256, 1>(a, x, b, w_post, gate, w_pre, x_out, y, s);
+  else if (a.dim <= 4096) launch_join_as<T, RT, 256, 2>(a, x, b, w_post, gate, w_pre, x_out, y, s);
+  else if (a.dim <= 8192) launch_join_as<T, RT, 512, 2>(a, x, b, w_post, gate, w_pre, x_out, y, s);
+  else launch_join_as<T, RT, 1024, 2>(a, x, b, w_post, gate, w_pre, x_out, y, s);
+}
+
+template <typename T, typename RT, int TPR, int NC>
+void launch_back_as(const JoinArgs& a, const void* dy, const void* dxo, const void* xo, const void* b,
+                    const void* w_post, const void* gate, const void* w_pre, void* dx, void* db, void* dgate_rows,
+                    float* part, int sums, hipStream_t s) {
+  k_join_back<T, RT, TPR, NC><<<dim3(join_parts(a.m)), dim3(TPR), 0, s>>>(
+      a, (const T*)dy, (const RT*)dxo, (const RT*)xo, (const T*)b, (const T*)w_post, (const T*)gate, (const T*)w_pre,
+      (RT*)dx, (T*)db, (T*)dgate_rows, part, sums);
+}
+
+template <typename T, typename RT, typename... A>
+void launch_back(const JoinArgs& a, A... args) {
+  if (a.dim <= 512) launch_back_as<T, RT, 64, 1>(a, args...);
+  else if (a.dim <= 2048) launch_back_as<T, RT, 256, 1>(a, args...);
+  else if (a.dim <= 4096) launch_back_as<T, RT, 512, 1>(a, args...);
+  else if (a.dim <= 8192) launch_back_as<T, RT, 1024, 1>(a, args...);
+  else launch_back_as<T, RT, 1024, 2>(a, args...);
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+int moe_join_forward(const moe_join* j, const void* x, const void* b, const void* w_post, const void* gate,
+                     const void* w_pre, int64_t m, void* x_out, void* y, void* stream) {
+  if (int r = check_join(j, m)) return r;
+  if (!x) return fail(MOE_EINVAL, "join: x must be non-NULL%s%lld");
+  if (b && !x_out) return fail(MOE_EINVAL, "join: x_out must be non-NULL where there is a block output%s%lld");
+  if (!b && (w_post || gate)) return fail(MOE_EINVAL, "join: w_post and gate need a block output%s%lld");
+  if (!w_pre != !y) return fail(MOE_EINVAL, "join: w_pre and y go together%s%lld");
+  if (!x_out && !y) return fail(MOE_EINVAL, "join: nothing to write%s%lld");
+  for (const void* p : {b, w_post, gate, w_pre, (const void*)y})
+    if (off_element(p, j->type)) return fail(MOE_EINVAL, "join: a pointer is not aligned to its elements%s%lld");
+  for (const void* p : {x, (const void*)x_out})
+    if (off_element(p, j->residual_type)) return fail(MOE_EINVAL, "join: a pointer is not aligned to its elements%s%lld");
+  const JoinArgs a = join_args(*j, m);
+  const hipStream_t s = (hipStream_t)stream;
+  const bool f32 = j->residual_type == MOE_TYPE_F32;
+  if (j->type == MOE_TYPE_BF16)
+    f32 ? launch_join<bf16_t, float>(a, x, b, w_post, gate, w_pre, x_out, y, s)
+        : launch_join<bf16_t, bf16_t>(a, x, b, w_post, gate, w_pre, x_out, y, s);
+  else
+    f32 ? launch_join<fp16_t, float>(a, x, b, w_post, gate, w_pre, x_out, y, s)
+        : launch_join<fp16_t, fp16_t>(a, x, b, w_post, gate, w_pre, x_out, y, s);
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "join");
+}
+
+size_t moe_join_workspace_bytes(const moe_join* j, int64_t max_m) {
+  if (check_join(j, max_m)) return 0;
+  return ((size_t)join_parts(max_m) * 3 * j->dim * sizeof(float) + 255) & ~(size_t)255;
+}
+
+int moe_join_backward(const moe_join* j, const void* dy, const void* dx_out, const void* x_out, const void* b,
+                      const void* w_post, const void* gate, const void* w_pre, int64_t m, void* dx, void* db,
+                      float* dw_post, void* dgate, float* dw_pre, void* ws, size_t ws_bytes, void* stream) {
+  if (int r = check_join(j, m)) return r;
+  if (!dy && !dx_out) return fail(MOE_EINVAL, "join: dy or dx_out must be non-NULL%s%lld");
+  if (!dx) return fail(MOE_EINVAL, "join: dx must be non-NULL%s%lld");
+  if (dy && (!x_out || !w_pre)) return fail(MOE_EINVAL, "join: dy needs x_out and w_pre%s%lld");
+  if (!b && (w_post || gate || db)) return fail(MOE_EINVAL, "join: w_post, gate and db need a block output%s%lld");
+  if ((dw_pre && !dy) || (dw_post && !w_post) || (dgate && !gate))
+    return fail(MOE_EINVAL, "join: a gradient is asked for whose input is NULL%s%lld");
+  for (const void* p : {dy, b, w_post, gate, w_pre, (const void*)db})
+    if (off_element(p, j->type)) return fail(MOE_EINVAL, "join: a pointer is not aligned to its elements%s%lld");
+  for (const void* p : {dx_out, x_out, (const void*)dx})
+    if (off_element(p, j->residual_type)) return fail(MOE_EINVAL, "join: a pointer is not aligned to its elements%s%lld");
+  if (off_element(dgate, j->gate_rows ? j->type : MOE_TYPE_F32) || off_element(dw_post, MOE_TYPE_F32) ||
+      off_element(dw_pre, MOE_TYPE_F32))
+    return fail(MOE_EINVAL, "join: a pointer is not aligned to its elements%s%lld");
+  float* dgate_sum = j->gate_rows ? nullptr : (float*)dgate;
+  const int sums = dw_pre || dw_post || dgate_sum;
+  if (sums) {
+    if (!ws) return fail(MOE_EINVAL, "workspace is NULL%s%lld");
+    if ((uintptr_t)ws & 255) return fail(MOE_EINVAL, "workspace must be 256-byte aligned%s%lld");
+    const size_t need = moe_join_workspace_bytes(j, m);
+    if (ws_bytes < need) return fail(MOE_EWORKSPACE, "workspace too small%s: need %lld bytes", "", (long long)need);
+  }
+  const JoinArgs a = join_args(*j, m);
+  const hipStream_t s = (hipStream_t)stream;
+  const bool f32 = j->residual_type == MOE_TYPE_F32;
+  void* dgate_rows = j->gate_rows ? dgate : nullptr;
+  float* part = (float*)ws;
+  if (j->type == MOE_TYPE_BF16)
+    f32 ? launch_back<bf16_t, float>(a, dy, dx_out, x_out, b, w_post, gate, w_pre, dx, db, dgate_rows, part, sums, s)
+        : launch_back<bf16_t, bf16_t>(a, dy, dx_out, x_out, b, w_post, gate, w_pre, dx, db, dgate_rows, part, sums, s);
+  else
+    f32 ? launch_back<fp16_t, float>(a, dy, dx_out, x_out, b, w_post, gate, w_pre, dx, db, dgate_rows, part, sums, s)
+        : launch_back<fp16_t, fp16_t>(a, dy, dx_out, x_out, b, w_post, gate, w_pre, dx, db, dgate_rows, part, sums, s);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return hip_fail(e, "join_back");
+  if (sums) {
+    k_join_sums<<<dim3((j->dim + 63) / 64, 3), dim3(256), 0, s>>>(part, join_parts(m), j->dim, dw_pre, dw_post,
+                                                                  dgate_sum);
+    e = hipGetLastError();
+    if (e != hipSuccess) return hip_fail(e, "join_sums");
+  }
+  return MOE_OK;
+}
+
+}  // extern "C"

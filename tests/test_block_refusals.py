@@ -1,0 +1,109 @@
+"""The operators beside the layer refuse bad arguments before any launch (CPU)."""
+import ctypes
+
+import pytest
+
+import routing_quant_expert_amd as R
+
+EINVAL, EUNSUPPORTED, EWORKSPACE = -1, -2, -3
+
+
+class Fake:
+    """Stands in for a device tensor in calls that must fail validation."""
+
+    def __init__(self, addr=4096, rows=4, n=1 << 40):
+        self.addr, self.shape, self.n = addr, (rows, 64), n
+
+    def data_ptr(self):
+        return self.addr
+
+    def numel(self):
+        return self.n
+
+    def element_size(self):
+        return 1
+
+
+P = Fake()
+
+
+def refused(code, call):
+    with pytest.raises(R.MoeError) as ei:
+        call()
+    assert ei.value.code == code, str(ei.value)
+
+
+def join(**over):
+    j = R.Join(64, R.MOE_TYPE_BF16, residual=R.MOE_TYPE_F32)
+    for k, v in over.items():
+        setattr(j, k, v)
+    return j
+
+
+JOIN_BAD = [({"dim": 0}, EINVAL), ({"dim": -3}, EINVAL), ({"dim": R.MOE_JOIN_MAX_DIM + 1}, EUNSUPPORTED),
+            ({"type": 2}, EINVAL), ({"type": 7}, EINVAL), ({"residual_type": 1}, EINVAL), ({"gate_rows": 2}, EINVAL),
+            ({"scale": float("inf")}, EINVAL), ({"scale": float("nan")}, EINVAL), ({"eps": 0.0}, EINVAL),
+            ({"eps": -1e-6}, EINVAL), ({"eps": float("nan")}, EINVAL), ({"x_stride": 63}, EINVAL),
+            ({"x_out_stride": 63}, EINVAL), ({"b_stride": 63}, EINVAL), ({"y_stride": 63}, EINVAL),
+            ({"gate_rows": 1, "gate_stride": 63}, EINVAL)]
+
+
+@pytest.mark.parametrize("over,code", JOIN_BAD, ids=lambda v: str(v))
+def test_join_description(over, code):
+    j = join(**over)
+    if over.get("dim", 64) > 64:
+        for k in ("x_stride", "x_out_stride", "b_stride", "y_stride", "gate_stride"):
+            setattr(j, k, j.dim)
+    refused(code, lambda: R.join_forward(j, P, P, P, P, P, P, P, stream=0))
+    refused(code, lambda: R.join_backward(j, P, P, P, P, P, P, P, P, P, P, P, P, P, stream=0))
+    assert R.join_workspace_bytes(j, 4) == 0
+
+
+def test_join_arguments():
+    j = join()
+    odd, odd2 = Fake(4097), Fake(4098)
+    f = R.join_forward
+    for m, code in ((0, EINVAL), (1 << 22, EUNSUPPORTED)):
+        refused(code, lambda: f(j, Fake(rows=m), P, P, P, P, P, P, stream=0))
+        refused(code, lambda: R.join_backward(j, P, P, P, P, P, P, P, Fake(rows=m), P, P, P, P, P, stream=0))
+        assert R.join_workspace_bytes(j, m) == 0
+    assert R.join_workspace_bytes(j, (1 << 22) - 1) > 0
+    calls = [lambda: f(j, P, P, P, P, P, None, P, stream=0),        # a block and nowhere to write the stream
+             lambda: f(j, P, None, P, None, P, P, P, stream=0),     # a norm after no block
+             lambda: f(j, P, None, None, P, P, P, P, stream=0),     # a gate on no block
+             lambda: f(j, P, P, P, P, P, P, None, stream=0),        # w_pre without y
+             lambda: f(j, P, P, P, P, None, P, P, stream=0),        # y without w_pre
+             lambda: f(j, P, None, None, None, None, None, None, stream=0),
+             lambda: f(j, odd2, P, P, P, P, P, P, stream=0),        # an f32 stream on an address of 2 bytes
+             lambda: f(j, P, odd, P, P, P, P, P, stream=0),
+             lambda: f(j, P, P, P, P, P, P, odd, stream=0)]
+    b = R.join_backward
+    calls += [lambda: b(j, None, None, P, P, P, P, P, P, P, P, P, P, P, stream=0),   # no gradient comes in
+              lambda: b(j, P, P, None, P, P, P, P, P, P, P, P, P, P, stream=0),      # dy without the stream
+              lambda: b(j, P, P, P, P, P, P, None, P, P, P, P, P, P, stream=0),      # dy without w_pre
+              lambda: b(j, None, P, P, P, P, P, P, P, P, P, P, P, P, stream=0),      # dw_pre without dy
+              lambda: b(j, P, P, P, P, None, P, P, P, P, P, P, P, P, stream=0),      # dw_post without w_post
+              lambda: b(j, P, P, P, P, P, None, P, P, P, P, P, P, P, stream=0),      # dgate without a gate
+              lambda: b(j, P, P, P, None, None, None, P, P, P, None, None, P, P, stream=0),   # db without a block
+              lambda: b(j, P, P, P, P, P, P, P, P, P, P, P, P, None, stream=0),      # sums without a workspace
+              lambda: b(j, P, P, P, P, P, P, P, P, P, P, P, P, Fake(4096 + 128), stream=0),
+              lambda: b(j, P, P, P, P, P, P, P, P, odd, P, P, P, P, stream=0),
+              lambda: b(j, P, P, P, P, P, P, P, P, P, odd2, P, P, P, stream=0)]
+    for i, call in enumerate(calls):
+        with pytest.raises(R.MoeError) as ei:
+            call()
+        assert ei.value.code == EINVAL, i
+    small = Fake(n=R.join_workspace_bytes(j, 4) - 1)
+    refused(EWORKSPACE, lambda: b(j, P, P, P, P, P, P, P, P, P, P, P, P, small, stream=0))
+    L = R.lib()
+    assert L.moe_join_forward(None, 4096, 4096, None, None, None, 1, 4096, None, None) == EINVAL
+    assert L.moe_join_forward(ctypes.byref(j), None, 4096, None, None, None, 1, 4096, None, None) == EINVAL
+    assert L.moe_join_backward(ctypes.byref(j), 4096, None, 4096, None, None, None, 4096, 1, None, None, None, None,
+                               None, None, 0, None) == EINVAL
+
+
+def test_type_codes():
+    import torch
+    assert [R.type_code(t) for t in (torch.bfloat16, torch.float16, torch.float32)] == [0, 1, 2]
+    with pytest.raises(R.MoeError):
+        R.type_code(torch.float64)
