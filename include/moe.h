@@ -486,6 +486,39 @@ int moe_join_backward(const moe_join* j, const void* dy, const void* dx_out, con
                       const void* w_post, const void* gate, const void* w_pre, int64_t m, void* dx, void* db,
                       float* dw_post, void* dgate, float* dw_pre, void* ws, size_t ws_bytes, void* stream);
 
+/* Products grouped by expert: rows sorted by group, group g's rows
+ * offsets[g] .. offsets[g+1] (offsets: int32 [n_groups + 1] on the device,
+ * ascending inside [0, rows]; groups may be empty) with its own weight W[g],
+ * n x k. Products of 16-bit elements are summed in f32 and rounded once.
+ *   forward     y[r]  = W[g] x[r]
+ *   backward_x  dx[r] = W[g]^T dy[r]
+ *   backward_w  dW[g] = sum over the group's rows of dy[r] x[r]^T
+ *   x, dx  [rows][k]   y, dy  [rows][n]   w, dw  [n_groups][n][k]
+ * Inputs have `type`, the output `out_type`. Every output is written whole:
+ * rows of no group (before offsets[0], after offsets[n_groups]) and the dW of
+ * empty groups are 0. rows may be 0. Outputs must not overlap inputs. Any n,
+ * k >= 1, stride and element alignment; rows whose start is 16-byte aligned
+ * (and widths that are multiples of 8) take the faster path. The same call
+ * gives the same bits. status: MOE_STATUS_BAD_OFFSETS, may be NULL; outputs
+ * are unspecified then. */
+#define MOE_GROUPED_MAX_GROUPS 1024
+#define MOE_GROUPED_MAX_STRIDE (1 << 22)
+typedef struct moe_grouped {
+  int32_t n_groups, n, k;
+  int32_t type;            /* MOE_TYPE_BF16 or MOE_TYPE_FP16              */
+  int32_t out_type;        /* type, or MOE_TYPE_F32                       */
+  int64_t x_stride;        /* elements between rows: x and dx, >= k       */
+  int64_t y_stride;        /* y and dy, >= n                              */
+  int64_t w_stride;        /* rows of w and dw, >= k                      */
+  int64_t w_group_stride;  /* from one group's w (dw) to the next         */
+} moe_grouped;
+int moe_grouped_forward(const moe_grouped* g, const void* x, const void* w, const int32_t* offsets, int64_t rows,
+                        void* y, int32_t* status, void* stream);
+int moe_grouped_backward_x(const moe_grouped* g, const void* dy, const void* w, const int32_t* offsets, int64_t rows,
+                           void* dx, int32_t* status, void* stream);
+int moe_grouped_backward_w(const moe_grouped* g, const void* dy, const void* x, const int32_t* offsets, int64_t rows,
+                           void* dw, int32_t* status, void* stream);
+
 const char* moe_last_error(void);
 
 #ifdef __cplusplus

@@ -107,6 +107,8 @@ def lib():
         L.moe_join_workspace_bytes.restype = ctypes.c_size_t
         L.moe_join_workspace_bytes.argtypes = [_VP, ctypes.c_int64]
         L.moe_join_backward.argtypes = [_VP] * 8 + [ctypes.c_int64] + [_VP] * 6 + [ctypes.c_size_t, _VP]
+        for f in (L.moe_grouped_forward, L.moe_grouped_backward_x, L.moe_grouped_backward_w):
+            f.argtypes = [_VP] * 4 + [ctypes.c_int64] + [_VP] * 3
         L.moe_last_error.restype = ctypes.c_char_p
         _lib = L
     return _lib
@@ -331,6 +333,8 @@ MOE_TYPE_BF16, MOE_TYPE_FP16, MOE_TYPE_F32 = 0, 1, 2
 MOE_STATUS_BAD_OFFSETS = 8
 MOE_STATUS_BAD_ADAPTER = 16
 MOE_JOIN_MAX_DIM = 16384
+MOE_GROUPED_MAX_GROUPS = 1024
+MOE_GROUPED_MAX_STRIDE = 1 << 22
 
 
 def type_code(dtype) -> int:
@@ -382,3 +386,36 @@ def join_backward(j: Join, dy, dx_out, x_out, block, w_post, gate, w_pre, dx, db
                                    _addr(w_post), _addr(gate), _addr(w_pre), dx.shape[0], _addr(dx), _addr(dblock),
                                    _addr(dw_post), _addr(dgate), _addr(dw_pre), _addr(ws),
                                    0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
+
+
+class Grouped(ctypes.Structure):
+    """moe_grouped: products of rows sorted by group with one n x k weight per group.
+    Strides default to contiguous rows and weights."""
+    _fields_ = [("n_groups", ctypes.c_int32), ("n", ctypes.c_int32), ("k", ctypes.c_int32), ("type", ctypes.c_int32),
+                ("out_type", ctypes.c_int32), ("x_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64),
+                ("w_stride", ctypes.c_int64), ("w_group_stride", ctypes.c_int64)]
+
+    def __init__(self, n_groups: int, n: int, k: int, dtype, out=None, x_stride: int | None = None,
+                 y_stride: int | None = None, w_stride: int | None = None, w_group_stride: int | None = None):
+        t = type_code(dtype)
+        ws = k if w_stride is None else w_stride
+        super().__init__(n_groups, n, k, t, t if out is None else type_code(out), k if x_stride is None else x_stride,
+                         n if y_stride is None else y_stride, ws, n * ws if w_group_stride is None else w_group_stride)
+
+
+def grouped_forward(g: Grouped, x, w, offsets, y, status=None, stream=None):
+    """y[r] = w[group of r] @ x[r]; offsets: int32 [n_groups + 1] on the device."""
+    _check(lib().moe_grouped_forward(ctypes.byref(g), _addr(x), _addr(w), _addr(offsets), x.shape[0], _addr(y),
+                                     _addr(status), _stream(stream)))
+
+
+def grouped_backward_x(g: Grouped, dy, w, offsets, dx, status=None, stream=None):
+    """dx[r] = w[group of r]^T @ dy[r]."""
+    _check(lib().moe_grouped_backward_x(ctypes.byref(g), _addr(dy), _addr(w), _addr(offsets), dy.shape[0], _addr(dx),
+                                        _addr(status), _stream(stream)))
+
+
+def grouped_backward_w(g: Grouped, dy, x, offsets, dw, status=None, stream=None):
+    """dw[g] = the sum of dy[r] x[r]^T over the group's rows."""
+    _check(lib().moe_grouped_backward_w(ctypes.byref(g), _addr(dy), _addr(x), _addr(offsets), dy.shape[0], _addr(dw),
+                                        _addr(status), _stream(stream)))

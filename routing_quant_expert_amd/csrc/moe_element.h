@@ -49,10 +49,13 @@ __device__ __forceinline__ oct<T> load_oct(const T* p, int n) {
   oct<T> o = {};
   if (n >= 8) {
     __builtin_memcpy(&o, p, 8 * sizeof(T));
-  } else {
+  } else if (n > 0) {
+    // all seven loads at once (past the end: the last element again), not one after another behind branches
+    T v[7];
 #pragma unroll
-    for (int i = 0; i < 7; ++i)
-      if (i < n) o[i] = p[i];
+    for (int i = 0; i < 7; ++i) v[i] = p[i < n ? i : n - 1];
+#pragma unroll
+    for (int i = 0; i < 7; ++i) o[i] = i < n ? v[i] : (T)0.0f;
   }
   return o;
 }

@@ -1,0 +1,275 @@
+// Products grouped by expert (moe_grouped_*): rows sorted by group, group g's
+// rows offsets[g] .. offsets[g+1] against its own 16-bit weight W[g] (n x k).
+//
+//   forward  y[r]  = W[g(r)] x[r]                    P = W rows,    Q = x rows,  sum over k
+//   input    dx[r] = W[g(r)]^T dy[r]                 P = W columns, Q = dy rows, sum over n
+//   weight   dW[g] = sum over g's rows dy[r] x[r]^T  P = x columns, Q = dy columns
+//
+// The offsets stay on the device: the grid is an upper bound of the tiles (a
+// group adds at most one partial tile), every wave finds its tile from the
+// offsets by two wave-wide prefix sums, and workgroups past the last tile end
+// at once.
+#include <hip/hip_runtime.h>
+
+#include "moe_gemm.h"
+#include "moe_host.h"
+
+namespace moe {
+namespace {
+
+constexpr int kSuper = 8;   // row tiles that share a weight tile before the next weight tile
+
+struct GroupedArgs {
+  const int32_t* offsets;
+  int32_t* status;
+  int groups, rows;
+  int n, k;
+  int f32;   // outputs in f32
+  int64_t x_stride, y_stride, w_stride, w_group;
+};
+
+// Rows are cut at the edges 0, offsets[0..groups], rows: entry e = g + 1 is
+// group g, the first and last entries are the rows of no group. Edges are
+// clamped to [0, rows], so that no offsets lead outside the buffers.
+__device__ __forceinline__ int edge(const GroupedArgs& a, int e) {
+  if (e <= 0) return 0;
+  if (e > a.groups + 1) return a.rows;
+  return min(max(a.offsets[e - 1], 0), a.rows);
+}
+
+__device__ __forceinline__ int wave_scan(int v, int lane) {
+#pragma unroll
+  for (int s = 1; s < 64; s *= 2) {
+    const int o = __shfl_up(v, s);
+    if (lane >= s) v += o;
+  }
+  return v;
+}
+
+struct Tile {
+  int group;        // groups or -1: the rows of no group
+  int row, rows;    // first row and rows of the tile (0: no tile)
+  int p;            // tile along the output's columns
+};
+
+// The tile of this workgroup: `np` column tiles for every BQ rows of an entry.
+// Lane l sums the tiles of the entries U l .. U l + U - 1; the wave's prefix
+// sums give the lane, and the prefix sums of that lane's entries the entry.
+template <int BQ>
+__device__ __forceinline__ Tile find_tile(const GroupedArgs& a, int np) {
+  const int lane = threadIdx.x & 63, entries = a.groups + 2, U = (entries + 63) / 64;
+  auto tiles = [](int lo, int hi) { return hi > lo ? (hi - lo + BQ - 1) / BQ : 0; };
+  int sum = 0;
+  int lo = edge(a, lane * U);
+  for (int u = 0; u < U; ++u) {
+    const int e = lane * U + u;
+    if (e >= entries) break;
+    const int hi = edge(a, e + 1);
+    sum += tiles(lo, hi);
+    lo = hi;
+  }
+  const int incl = wave_scan(sum, lane);
+  const int64_t total = (int64_t)__shfl(incl, 63) * np;
+  const int64_t place = xcd_order(blockIdx.x, total);
+  if (place >= total) return {0, 0, 0, 0};
+  const int t = (int)(place / np);
+  const uint64_t lanes = __ballot(incl > t);
+  if (!lanes) return {0, 0, 0, 0};   // (counts of offsets that do not ascend may wrap)
+  const int sel = __builtin_ctzll(lanes);
+  const int before = __shfl(incl - sum, sel);
+  const int e = sel * U + lane;
+  const bool mine = lane < U && e < entries;
+  const int elo = mine ? edge(a, e) : 0, ehi = mine ? edge(a, e + 1) : 0;
+  const int cnt = tiles(elo, ehi);
+  const int incl2 = before + wave_scan(cnt, lane);
+  const uint64_t hits = __ballot(incl2 > t);
+  if (!hits) return {0, 0, 0, 0};
+  const int s = __builtin_ctzll(hits);
+  const int first = __shfl(incl2 - cnt, s), n_rt = __shfl(cnt, s);
+  const int glo = __shfl(elo, s), ghi = __shfl(ehi, s);
+  // inside the entry: kSuper row tiles after one another, then the next column tile
+  const int64_t l = place - (int64_t)first * np;
+  const int sup = (int)(l / (kSuper * np)), in = (int)(l - (int64_t)sup * kSuper * np);
+  const int wide = min(kSuper, n_rt - kSuper * sup);
+  const int rt = wide > 0 ? kSuper * sup + in % wide : -1;
+  if (rt < 0 || rt >= n_rt) return {0, 0, 0, 0};
+  return {sel * U + s - 1, glo + rt * BQ, min(BQ, ghi - (glo + rt * BQ)), in / wide};
+}
+
+// The first workgroup reports offsets that do not ascend or leave [0, rows].
+__device__ __forceinline__ void report(const GroupedArgs& a) {
+  if (!a.status || blockIdx.x) return;
+  bool bad = false;
+  for (int g = threadIdx.x; g < a.groups; g += blockDim.x) {
+    const int lo = a.offsets[g], hi = a.offsets[g + 1];
+    bad = bad || lo < 0 || hi < lo || hi > a.rows;
+  }
+  if (bad) atomicOr(a.status, MOE_STATUS_BAD_OFFSETS);
+}
+
+// Forward (WCOL false): in = x, out = y. Input gradient (WCOL true): in = dy, out = dx.
+template <typename T, bool WCOL, typename G>
+__global__ __launch_bounds__(G::NT) void k_grouped(GroupedArgs a, const T* __restrict__ in, const T* __restrict__ w,
+                                                   void* __restrict__ out) {
+  extern __shared__ __align__(16) uint8_t lds[];
+  report(a);
+  const int width = WCOL ? a.k : a.n, red = WCOL ? a.n : a.k;
+  Tile t = find_tile<G::kQ>(a, (width + G::kP - 1) / G::kP);
+  // (the same in every lane: into scalar registers)
+  t.group = __builtin_amdgcn_readfirstlane(t.group);
+  t.row = __builtin_amdgcn_readfirstlane(t.row);
+  t.rows = __builtin_amdgcn_readfirstlane(t.rows);
+  t.p = __builtin_amdgcn_readfirstlane(t.p);
+  if (t.rows <= 0) return;
+  const bool none = t.group < 0 || t.group >= a.groups;
+  const int p0 = t.p * G::kP;
+  const int64_t in_stride = WCOL ? a.y_stride : a.x_stride, out_stride = WCOL ? a.x_stride : a.y_stride;
+  const Operand<T> P = {w + (none ? 0 : t.group) * a.w_group + (WCOL ? p0 : p0 * a.w_stride), a.w_stride, WCOL ? width - p0 : min(G::kP, width - p0)};
+  const Operand<T> Q = {in + t.row * in_stride, in_stride, t.rows};
+  typename G::Acc acc = {};
+  G::run(P, Q, none ? 0 : red, lds, acc);
+  uint8_t* o = (uint8_t*)out + (t.row * out_stride + p0) * (a.f32 ? 4 : 2);
+  G::store(acc, o, a.f32, out_stride, width - p0, t.rows);
+}
+
+template <typename T, typename G>
+__global__ __launch_bounds__(G::NT) void k_grouped_dw(GroupedArgs a, const T* __restrict__ dy, const T* __restrict__ x,
+                                                      void* __restrict__ dw) {
+  extern __shared__ __align__(16) uint8_t lds[];
+  report(a);
+  const int np = (a.k + G::kP - 1) / G::kP, nq = (a.n + G::kQ - 1) / G::kQ;
+  const int64_t total = (int64_t)np * nq * a.groups, place = xcd_order(blockIdx.x, total);
+  if (place >= total) return;
+  const int g = (int)(place / (np * nq)), in = (int)(place % (np * nq));
+  const int p0 = in / nq * G::kP, q0 = in % nq * G::kQ;
+  const int lo = edge(a, g + 1), hi = max(lo, edge(a, g + 2));
+  const Operand<T> P = {x + lo * a.x_stride + p0, a.x_stride, a.k - p0};
+  const Operand<T> Q = {dy + lo * a.y_stride + q0, a.y_stride, a.n - q0};
+  typename G::Acc acc = {};
+  G::run(P, Q, hi - lo, lds, acc);
+  uint8_t* o = (uint8_t*)dw + (g * a.w_group + q0 * a.w_stride + p0) * (a.f32 ? 4 : 2);
+  G::store(acc, o, a.f32, a.w_stride, a.k - p0, a.n - q0);
+}
+
+enum Way { kForward, kInput, kWeight };
+
+int check_grouped(const moe_grouped* g, int64_t rows) {
+  if (!g) return fail(MOE_EINVAL, "grouped is NULL%s%lld");
+  if (g->type != MOE_TYPE_BF16 && g->type != MOE_TYPE_FP16)
+    return fail(MOE_EINVAL, "grouped: type must be MOE_TYPE_BF16 or MOE_TYPE_FP16%s (%lld)", "", g->type);
+  if (g->out_type != g->type && g->out_type != MOE_TYPE_F32)
+    return fail(MOE_EINVAL, "grouped: out_type must be type or MOE_TYPE_F32%s (%lld)", "", g->out_type);
+  if (g->n_groups < 1) return fail(MOE_EINVAL, "grouped: n_groups must be >= 1%s (%lld)", "", g->n_groups);
+  if (g->n_groups > MOE_GROUPED_MAX_GROUPS)
+    return fail(MOE_EUNSUPPORTED, "grouped: n_groups above MOE_GROUPED_MAX_GROUPS%s (%lld)", "", g->n_groups);
+  if (g->n < 1 || g->k < 1) return fail(MOE_EINVAL, "grouped: n and k must be >= 1%s%lld");
+  if (g->x_stride < g->k || g->y_stride < g->n || g->w_stride < g->k)
+    return fail(MOE_EINVAL, "grouped: a row stride is below its row%s%lld");
+  if (g->w_group_stride < (int64_t)(g->n - 1) * g->w_stride + g->k)
+    return fail(MOE_EINVAL, "grouped: w_group_stride is below one weight%s (%lld)", "", g->w_group_stride);
+  if (g->x_stride > MOE_GROUPED_MAX_STRIDE || g->y_stride > MOE_GROUPED_MAX_STRIDE ||
+      g->w_stride > MOE_GROUPED_MAX_STRIDE)
+    return fail(MOE_EUNSUPPORTED, "grouped: a row stride above MOE_GROUPED_MAX_STRIDE%s%lld");
+  if (rows < 0) return fail(MOE_EINVAL, "grouped: rows must be >= 0%s (%lld)", "", rows);
+  if (rows > INT32_MAX) return fail(MOE_EUNSUPPORTED, "grouped: rows above 2^31 - 1%s (%lld)", "", rows);
+  return MOE_OK;
+}
+
+GroupedArgs grouped_args(const moe_grouped& g, const int32_t* offsets, int64_t rows, int32_t* status) {
+  return {offsets, status, g.n_groups, (int)rows, g.n, g.k, g.out_type == MOE_TYPE_F32,
+          g.x_stride, g.y_stride, g.w_stride, g.w_group_stride};
+}
+
+// Rows that can be brought into LDS 16 bytes at a time.
+bool rows16(const void* p, int64_t stride) { return ((uintptr_t)p & 15) == 0 && stride % 8 == 0; }
+
+// (`tiles` workgroups, rounded up to whole rounds of the XCDs as xcd_order needs them)
+template <auto Kernel, typename... A>
+int launch(int64_t tiles, int threads, int lds, hipStream_t s, A... args) {
+  const int64_t blocks = (tiles + 7) / 8 * 8;
+  if (blocks * threads >= (int64_t)1 << 32)
+    return fail(MOE_EUNSUPPORTED, "grouped: too many tiles for one launch%s (%lld)", "", blocks);
+  static const hipError_t attr = hipFuncSetAttribute((const void*)Kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (attr != hipSuccess) return hip_fail(attr, "grouped");
+  Kernel<<<dim3((unsigned)blocks), dim3(threads), lds, s>>>(args...);
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "grouped");
+}
+
+template <typename T, bool WCOL, typename G>
+int launch_rows(const GroupedArgs& a, const void* in, const void* w, void* out, hipStream_t s) {
+  const int width = WCOL ? a.k : a.n;
+  const int64_t some = a.groups + 2 < a.rows ? a.groups + 2 : a.rows;   // entries that can have rows
+  const int64_t row_tiles = (a.rows + (G::kQ - 1) * some) / G::kQ;
+  return launch<k_grouped<T, WCOL, G>>(row_tiles * ((width + G::kP - 1) / G::kP), G::NT, G::kLds, s, a, (const T*)in,
+                                       (const T*)w, out);
+}
+
+template <typename T, bool WCOL, bool DMA>
+int launch_rows_as(const GroupedArgs& a, const void* in, const void* w, void* out, hipStream_t s) {
+  const int64_t mean = a.rows / a.groups;
+  if (mean < 16) return launch_rows<T, WCOL, Gemm<T, WCOL, false, 128, 16, 4, 1, 4, DMA>>(a, in, w, out, s);
+  if (mean < 64) return launch_rows<T, WCOL, Gemm<T, WCOL, false, 128, 64, 2, 2, 3, DMA>>(a, in, w, out, s);
+  return launch_rows<T, WCOL, Gemm<T, WCOL, false, 128, 128, 2, 2, 2, DMA>>(a, in, w, out, s);
+}
+
+template <typename T, typename G>
+int launch_dw(const GroupedArgs& a, const void* dy, const void* x, void* dw, hipStream_t s) {
+  const int64_t tiles = (int64_t)((a.k + G::kP - 1) / G::kP) * ((a.n + G::kQ - 1) / G::kQ) * a.groups;
+  return launch<k_grouped_dw<T, G>>(tiles, G::NT, G::kLds, s, a, (const T*)dy, (const T*)x, dw);
+}
+
+template <typename T>
+int launch_way(Way way, const GroupedArgs& a, const void* in, const void* w, void* out, hipStream_t s) {
+  if (way == kForward)
+    return rows16(in, a.x_stride) && rows16(w, a.w_stride) && a.w_group % 8 == 0
+               ? launch_rows_as<T, false, true>(a, in, w, out, s)
+               : launch_rows_as<T, false, false>(a, in, w, out, s);
+  if (way == kInput)
+    return rows16(in, a.y_stride) && rows16(w, a.w_stride) && a.w_group % 8 == 0 && a.k % 8 == 0
+               ? launch_rows_as<T, true, true>(a, in, w, out, s)
+               : launch_rows_as<T, true, false>(a, in, w, out, s);
+  return rows16(in, a.y_stride) && rows16(w, a.x_stride) && a.n % 8 == 0 && a.k % 8 == 0
+             ? launch_dw<T, Gemm<T, true, true, 128, 128, 2, 2, 2, true>>(a, in, w, out, s)
+             : launch_dw<T, Gemm<T, true, true, 128, 128, 2, 2, 2, false>>(a, in, w, out, s);
+}
+
+int grouped(Way way, const moe_grouped* g, const void* in, const void* w, const int32_t* offsets, int64_t rows,
+            void* out, int32_t* status, void* stream) {
+  if (int r = check_grouped(g, rows)) return r;
+  if (!offsets) return fail(MOE_EINVAL, "grouped: offsets must be non-NULL%s%lld");
+  if (way != kWeight && rows == 0) return MOE_OK;   // nothing to write
+  if ((rows && !in) || ((rows || way != kWeight) && !w) || !out)
+    return fail(MOE_EINVAL, "grouped: operands and output must be non-NULL%s%lld");
+  const size_t es = elem_bytes(g->out_type);
+  if ((uintptr_t)in % 2 || (uintptr_t)w % 2 || (uintptr_t)out % es || (uintptr_t)offsets % 4 || (uintptr_t)status % 4)
+    return fail(MOE_EINVAL, "grouped: a pointer is not aligned to its elements%s%lld");
+  const GroupedArgs a = grouped_args(*g, offsets, rows, status);
+  const hipStream_t s = (hipStream_t)stream;
+  return g->type == MOE_TYPE_BF16 ? launch_way<bf16_t>(way, a, in, w, out, s)
+                                  : launch_way<fp16_t>(way, a, in, w, out, s);
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+int moe_grouped_forward(const moe_grouped* g, const void* x, const void* w, const int32_t* offsets, int64_t rows,
+                        void* y, int32_t* status, void* stream) {
+  return grouped(kForward, g, x, w, offsets, rows, y, status, stream);
+}
+
+int moe_grouped_backward_x(const moe_grouped* g, const void* dy, const void* w, const int32_t* offsets, int64_t rows,
+                           void* dx, int32_t* status, void* stream) {
+  return grouped(kInput, g, dy, w, offsets, rows, dx, status, stream);
+}
+
+int moe_grouped_backward_w(const moe_grouped* g, const void* dy, const void* x, const int32_t* offsets, int64_t rows,
+                           void* dw, int32_t* status, void* stream) {
+  return grouped(kWeight, g, dy, x, offsets, rows, dw, status, stream);
+}
+
+}  // extern "C"

@@ -107,3 +107,48 @@ def test_type_codes():
     assert [R.type_code(t) for t in (torch.bfloat16, torch.float16, torch.float32)] == [0, 1, 2]
     with pytest.raises(R.MoeError):
         R.type_code(torch.float64)
+
+
+def grouped(**over):
+    g = R.Grouped(4, 64, 32, R.MOE_TYPE_FP16, out=R.MOE_TYPE_F32)
+    for k, v in over.items():
+        setattr(g, k, v)
+    return g
+
+
+GROUPED_CALLS = [R.grouped_forward, R.grouped_backward_x, R.grouped_backward_w]
+GROUPED_BAD = [({"n_groups": 0}, EINVAL), ({"n_groups": R.MOE_GROUPED_MAX_GROUPS + 1}, EUNSUPPORTED), ({"n": 0}, EINVAL),
+               ({"k": -1}, EINVAL), ({"type": 2}, EINVAL), ({"out_type": 0}, EINVAL), ({"out_type": 3}, EINVAL),
+               ({"x_stride": 31}, EINVAL), ({"y_stride": 63}, EINVAL), ({"w_stride": 31}, EINVAL),
+               ({"w_group_stride": 63 * 32 + 31}, EINVAL), ({"x_stride": R.MOE_GROUPED_MAX_STRIDE + 1}, EUNSUPPORTED),
+               ({"y_stride": R.MOE_GROUPED_MAX_STRIDE + 1}, EUNSUPPORTED),
+               ({"w_stride": R.MOE_GROUPED_MAX_STRIDE + 1, "w_group_stride": 1 << 40}, EUNSUPPORTED)]
+
+
+@pytest.mark.parametrize("over,code", GROUPED_BAD, ids=lambda v: str(v))
+def test_grouped_description(over, code):
+    for f in GROUPED_CALLS:
+        refused(code, lambda: f(grouped(**over), P, P, P, P, stream=0))
+
+
+def test_grouped_arguments():
+    g = grouped()
+    odd, odd2 = Fake(4097), Fake(4098)
+    for f in GROUPED_CALLS:
+        for i, a in enumerate(([None] * 4, [odd, P, P, P], [P, odd, P, P], [P, P, odd2, P], [P, P, None, P],
+                               [P, P, P, None], [P, P, P, odd2], [P, None, P, P])):
+            if a[0] is None:
+                a[0] = Fake(0)
+            refused(EINVAL, lambda: f(g, *a, stream=0))
+        refused(EINVAL, lambda: f(g, P, P, P, P, status=odd2, stream=0))
+        refused(EUNSUPPORTED, lambda: f(g, Fake(rows=1 << 31), P, P, P, stream=0))
+        # more tiles than a launch can have
+        if f is not R.grouped_backward_w:
+            refused(EUNSUPPORTED, lambda: f(grouped(n=1 << 20, k=1 << 20, x_stride=1 << 20, y_stride=1 << 20, w_stride=1 << 20,
+                                                    w_group_stride=1 << 40), Fake(rows=(1 << 31) - 1), P, P, P, stream=0))
+    L = R.lib()
+    assert L.moe_grouped_forward(None, 4096, 4096, 4096, 1, 4096, None, None) == EINVAL
+    assert L.moe_grouped_forward(ctypes.byref(g), 4096, 4096, 4096, -1, 4096, None, None) == EINVAL
+    # nothing to write: no pointers needed
+    assert L.moe_grouped_forward(ctypes.byref(g), None, None, 4096, 0, None, None, None) == 0
+    assert L.moe_grouped_forward(ctypes.byref(g), None, None, None, 0, None, None, None) == EINVAL
