@@ -519,6 +519,37 @@ int moe_grouped_backward_x(const moe_grouped* g, const void* dy, const void* w, 
 int moe_grouped_backward_w(const moe_grouped* g, const void* dy, const void* x, const int32_t* offsets, int64_t rows,
                            void* dw, int32_t* status, void* stream);
 
+/* A shared projection with one low-rank adapter per token:
+ *   out[t] = W x[t] + factor[a] B[a] (A[a] x[t]),  a = index[t]; a = -1: W x[t].
+ * Products of 16-bit elements, f32 sums, one rounding at the end (A x is not
+ * rounded to 16 bits in between).
+ *   x      type [m][k]       w    type [n][k]      out  out_type [m][n]
+ *   index  int32 [m] on the device: adapters in any order, each -1 or below n_adapters
+ * Adapters of a smaller rank are filled up with zeros. Outputs must not
+ * overlap inputs. Any n, k >= 1, stride and element alignment; 16-byte aligned
+ * rows take the faster path. The same call gives the same bits. ws:
+ * moe_adapter_workspace_bytes(p, m) bytes, 256-byte aligned, uninitialised; a
+ * workspace for max_m serves every m up to it. status:
+ * MOE_STATUS_BAD_ADAPTER, may be NULL; a token of an invalid index is
+ * projected without an adapter. 1 <= m <= MOE_ADAPTER_MAX_TOKENS. */
+#define MOE_ADAPTER_MAX_ADAPTERS 1024
+#define MOE_ADAPTER_MAX_RANK 1024
+#define MOE_ADAPTER_MAX_TOKENS (1 << 20)
+typedef struct moe_adapters {
+  int32_t n_adapters, rank, n, k;
+  int32_t type;            /* MOE_TYPE_BF16 or MOE_TYPE_FP16              */
+  int32_t out_type;        /* type, or MOE_TYPE_F32                       */
+  const void* a;           /* type [n_adapters][rank][k]                  */
+  const void* b;           /* type [n_adapters][n][rank]                  */
+  const float* factor;     /* f32 [n_adapters], NULL: 1                   */
+  int64_t x_stride, w_stride, out_stride;   /* elements between rows, at most MOE_GROUPED_MAX_STRIDE */
+  int64_t a_stride, a_group_stride;         /* rows of A; from one adapter's A to the next           */
+  int64_t b_stride, b_group_stride;
+} moe_adapters;
+size_t moe_adapter_workspace_bytes(const moe_adapters* p, int64_t max_m);
+int moe_adapter_project(const moe_adapters* p, const void* x, const void* w, const int32_t* index, int64_t m,
+                        void* out, void* ws, size_t ws_bytes, int32_t* status, void* stream);
+
 const char* moe_last_error(void);
 
 #ifdef __cplusplus

@@ -109,6 +109,9 @@ def lib():
         L.moe_join_backward.argtypes = [_VP] * 8 + [ctypes.c_int64] + [_VP] * 6 + [ctypes.c_size_t, _VP]
         for f in (L.moe_grouped_forward, L.moe_grouped_backward_x, L.moe_grouped_backward_w):
             f.argtypes = [_VP] * 4 + [ctypes.c_int64] + [_VP] * 3
+        L.moe_adapter_workspace_bytes.restype = ctypes.c_size_t
+        L.moe_adapter_workspace_bytes.argtypes = [_VP, ctypes.c_int64]
+        L.moe_adapter_project.argtypes = [_VP] * 4 + [ctypes.c_int64, _VP, _VP, ctypes.c_size_t, _VP, _VP]
         L.moe_last_error.restype = ctypes.c_char_p
         _lib = L
     return _lib
@@ -335,6 +338,9 @@ MOE_STATUS_BAD_ADAPTER = 16
 MOE_JOIN_MAX_DIM = 16384
 MOE_GROUPED_MAX_GROUPS = 1024
 MOE_GROUPED_MAX_STRIDE = 1 << 22
+MOE_ADAPTER_MAX_ADAPTERS = 1024
+MOE_ADAPTER_MAX_RANK = 1024
+MOE_ADAPTER_MAX_TOKENS = 1 << 20
 
 
 def type_code(dtype) -> int:
@@ -419,3 +425,41 @@ def grouped_backward_w(g: Grouped, dy, x, offsets, dw, status=None, stream=None)
     """dw[g] = the sum of dy[r] x[r]^T over the group's rows."""
     _check(lib().moe_grouped_backward_w(ctypes.byref(g), _addr(dy), _addr(x), _addr(offsets), dy.shape[0], _addr(dw),
                                         _addr(status), _stream(stream)))
+
+
+class Adapters(ctypes.Structure):
+    """moe_adapters: the low-rank adapters a [n_adapters, rank, k] and b [n_adapters, n, rank] (device tensors, kept
+    here) beside a shared n x k projection; factor f32 [n_adapters] or None. Strides default to contiguous rows."""
+    _fields_ = [("n_adapters", ctypes.c_int32), ("rank", ctypes.c_int32), ("n", ctypes.c_int32), ("k", ctypes.c_int32),
+                ("type", ctypes.c_int32), ("out_type", ctypes.c_int32), ("a", _VP), ("b", _VP), ("factor", _VP),
+                ("x_stride", ctypes.c_int64), ("w_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64),
+                ("a_stride", ctypes.c_int64), ("a_group_stride", ctypes.c_int64), ("b_stride", ctypes.c_int64),
+                ("b_group_stride", ctypes.c_int64)]
+
+    def __init__(self, a, b, factor=None, out=None, x_stride: int | None = None, w_stride: int | None = None,
+                 out_stride: int | None = None):
+        count, rank, k = a.shape
+        n = b.shape[1]
+        if tuple(b.shape) != (count, n, rank) or a.dtype != b.dtype:
+            raise MoeError(-1, f"adapters: a {tuple(a.shape)} {a.dtype} and b {tuple(b.shape)} {b.dtype} do not fit")
+        if (k > 1 and a.stride(2) != 1) or (rank > 1 and b.stride(2) != 1):
+            raise MoeError(-1, "adapters: the rows of a and b must be contiguous")
+        if factor is not None and (type_code(factor.dtype) != MOE_TYPE_F32 or tuple(factor.shape) != (count,) or
+                                   not factor.is_contiguous()):
+            raise MoeError(-1, "adapters: factor must be contiguous f32 [n_adapters]")
+        t = type_code(a.dtype)
+        super().__init__(count, rank, n, k, t, t if out is None else type_code(out), _addr(a), _addr(b), _addr(factor),
+                         k if x_stride is None else x_stride, k if w_stride is None else w_stride,
+                         n if out_stride is None else out_stride, a.stride(1), a.stride(0), b.stride(1), b.stride(0))
+        self._kept = (a, b, factor)
+
+
+def adapter_workspace_bytes(p: Adapters, max_m: int) -> int:
+    return int(lib().moe_adapter_workspace_bytes(ctypes.byref(p), max_m))
+
+
+def adapter_project(p: Adapters, x, w, index, out, ws, status=None, stream=None):
+    """out[t] = w @ x[t] + factor[a] * b[a] @ (a[a] @ x[t]) with a = index[t] (-1: w @ x[t] alone)."""
+    _check(lib().moe_adapter_project(ctypes.byref(p), _addr(x), _addr(w), _addr(index), x.shape[0], _addr(out),
+                                     _addr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _addr(status),
+                                     _stream(stream)))

@@ -16,7 +16,10 @@
 // holds four neighbouring outputs of one row.
 #pragma once
 
+#include <type_traits>
+
 #include "moe_element.h"
+#include "moe_internal.h"
 #include "moe_kquant.h"
 
 namespace moe {
@@ -36,16 +39,19 @@ __device__ __forceinline__ f32x4 mfma16(fp16x8_t a, fp16x8_t b, f32x4 c) {
 }
 
 // An operand of one tile: `base` at its first row (column) and r = 0, `count`
-// rows (columns) there, `ld` elements from one row to the next (COL: from one r to the next).
+// rows (columns) there, `ld` elements from one row to the next (COL: from one
+// r to the next). Gathered rows: row i of the tile is row rows[i] of base (below 0: any row, its outputs are not stored).
 template <typename T>
 struct Operand {
   const T* base;
   int64_t ld;
   int count;
+  const int32_t* rows;
 };
 
-template <typename T, bool COL, int R, int NT>
+template <typename T, bool COL, int R, int NT, bool GATHER = false>
 struct TileOf {
+  typedef std::conditional_t<GATHER, int64_t, uint32_t> Off;   // a tile's elements stay within 2^32 of its base
   static constexpr int kBytes = R * kStep * 2;
   static constexpr int kChunks = R * kStep / 8;
   static constexpr int kPer = kChunks >= NT ? kChunks / NT : 1;   // chunks a thread brings in
@@ -67,19 +73,27 @@ struct TileOf {
   }
 
   // Element offsets of the thread's chunks of a full step from the operand's
-  // base. Rows (columns) past the operand's repeat its last: they make outputs that are not stored.
-  __device__ static __forceinline__ void offsets(const Operand<T>& o, uint32_t (&off)[kPer]) {
+  // base. Rows past the operand's (and for DMA columns) repeat its last: they
+  // make outputs that are not stored.
+  template <bool DMA>
+  __device__ static __forceinline__ void offsets(const Operand<T>& o, Off (&off)[kPer]) {
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       int r, own;
       place(position(k), r, own);
-      own = min(own, COL ? o.count - 8 : o.count - 1);
-      off[k] = COL ? (uint32_t)r * (uint32_t)o.ld + own : (uint32_t)own * (uint32_t)o.ld + r;
+      if (COL) {
+        if (DMA) own = min(own, o.count - 8);
+        off[k] = (Off)r * (Off)o.ld + own;
+      } else {
+        own = min(own, o.count - 1);
+        if constexpr (GATHER) own = max(o.rows[own], 0);
+        off[k] = (Off)own * (Off)o.ld + r;
+      }
     }
   }
   __device__ static __forceinline__ int64_t step_stride(const Operand<T>& o) { return COL ? kStep * o.ld : kStep; }
 
-  __device__ static __forceinline__ void dma(const T* at, const uint32_t (&off)[kPer], uint8_t* tile) {
+  __device__ static __forceinline__ void dma(const T* at, const Off (&off)[kPer], uint8_t* tile) {
     uint8_t* first = tile + 16 * 64 * __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) % (kChunks < NT ? kChunks / 64 : NT / 64));
 #pragma unroll
     for (int k = 0; k < kPer; ++k)
@@ -88,24 +102,19 @@ struct TileOf {
   }
 
   // The same through registers, at any alignment: r past `left` and columns
-  // past the operand's are zero (rows past the operand's: zero, or its last row).
-  __device__ static __forceinline__ void load(const Operand<T>& o, const T* at, int left, oct<T> (&v)[kPer]) {
+  // past the operand's are zero.
+  __device__ static __forceinline__ void load(const Operand<T>& o, const T* at, const Off (&off)[kPer], int left,
+                                              oct<T> (&v)[kPer]) {
     if (left >= kStep && (!COL || o.count >= R)) {
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        int r, own;
-        place(position(k), r, own);
-        if (!COL) own = min(own, o.count - 1);
-        __builtin_memcpy(&v[k], at + (COL ? (uint32_t)r * (uint32_t)o.ld + own : (uint32_t)own * (uint32_t)o.ld + r), 16);
-      }
+      for (int k = 0; k < kPer; ++k) __builtin_memcpy(&v[k], at + off[k], 16);
       return;
     }
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       int r, own;
       place(position(k), r, own);
-      if (COL) v[k] = load_oct(at + (int64_t)r * o.ld + own, r < left ? o.count - own : 0);
-      else v[k] = load_oct(at + (int64_t)own * o.ld + r, own < o.count ? left - r : 0);
+      v[k] = load_oct(at + off[k], COL ? (r < left ? o.count - own : 0) : left - r);
     }
   }
   __device__ static __forceinline__ void store(const oct<T> (&v)[kPer], uint8_t* tile) {
@@ -147,11 +156,11 @@ __device__ __forceinline__ void wait_steps(int steps) {
 
 // WP x WQ waves of BP/WP x BQ/WQ outputs each; ST slots of one step in LDS.
 // DMA: 16-byte aligned rows, brought into LDS directly; otherwise through registers, any alignment.
-template <typename T, bool PCOL, bool QCOL, int BP, int BQ, int WP, int WQ, int ST, bool DMA>
+template <typename T, bool PCOL, bool QCOL, int BP, int BQ, int WP, int WQ, int ST, bool DMA, bool GATHER = false>
 struct Gemm {
   static constexpr int NT = 64 * WP * WQ;
   typedef TileOf<T, PCOL, BP, NT> PT;
-  typedef TileOf<T, QCOL, BQ, NT> QT;
+  typedef TileOf<T, QCOL, BQ, NT, GATHER> QT;
   static constexpr int kSlots = DMA ? ST : 2;
   static constexpr int kSlot = PT::kBytes + QT::kBytes;
   static constexpr int kLds = kSlots * kSlot;
@@ -178,16 +187,36 @@ struct Gemm {
     }
   }
 
+  // One step of the products of tile rows q whose bit is set in `some` (bit j: the j-th 16 rows of the tile).
+  __device__ static __forceinline__ void compute_some(const uint8_t* ptile, const uint8_t* qtile, uint32_t some, Acc& acc) {
+    const int lane = threadIdx.x & 63, p0 = wave_p(), q0 = wave_q();
+    some >>= __builtin_amdgcn_readfirstlane(q0 / 16);
+#pragma unroll
+    for (int kk = 0; kk < kStep / 32; ++kk) {
+      oct<T> pv[NP];
+#pragma unroll
+      for (int i = 0; i < NP; ++i) pv[i] = PT::operand(ptile, p0 + 16 * i, kk, lane);
+#pragma unroll
+      for (int j = 0; j < NQ; ++j) {
+        if (!(some >> j & 1)) continue;
+        const oct<T> qv = QT::operand(qtile, q0 + 16 * j, kk, lane);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) acc[i][j] = mfma16(pv[i], qv, acc[i][j]);
+      }
+    }
+  }
+
   // Adds the sum over r < red. LDS is free for other use after a barrier.
   __device__ static __forceinline__ void run(const Operand<T>& p, const Operand<T>& q, int red, uint8_t* lds,
                                              Acc& acc) {
     const int64_t ps = PT::step_stride(p), qs = QT::step_stride(q);
+    typename PT::Off po[PT::kPer];
+    typename QT::Off qo[QT::kPer];
+    PT::template offsets<DMA>(p, po);
+    QT::template offsets<DMA>(q, qo);
     if constexpr (DMA) {
       const int nk = red / kStep, tail = red % kStep;
       constexpr int kPer = PT::kPer + QT::kPer;
-      uint32_t po[PT::kPer], qo[QT::kPer];
-      PT::offsets(p, po);
-      QT::offsets(q, qo);
       const T *pat = p.base, *qat = q.base;
       auto issue = [&](uint8_t* slot) {
         PT::dma(pat, po, slot);
@@ -202,8 +231,8 @@ struct Gemm {
       uint8_t *get = lds, *put = end - kSlot;
       if (tail) {   // the last, partial step first, in the slot that the ring needs last
         oct<T> pv[PT::kPer], qv[QT::kPer];
-        PT::load(p, p.base + nk * ps, tail, pv);
-        QT::load(q, q.base + nk * qs, tail, qv);
+        PT::load(p, p.base + nk * ps, po, tail, pv);
+        QT::load(q, q.base + nk * qs, qo, tail, qv);
         PT::store(pv, put);
         QT::store(qv, put + PT::kBytes);
         lds_barrier();
@@ -223,8 +252,8 @@ struct Gemm {
       oct<T> pv[PT::kPer], qv[QT::kPer];
       const T *pat = p.base, *qat = q.base;
       auto load = [&](int s) {
-        PT::load(p, pat, red - s * kStep, pv);
-        QT::load(q, qat, red - s * kStep, qv);
+        PT::load(p, pat, po, red - s * kStep, pv);
+        QT::load(q, qat, qo, red - s * kStep, qv);
         pat += ps;
         qat += qs;
       };
@@ -247,13 +276,15 @@ struct Gemm {
     }
   }
 
-  // Writes the tile's first `pn` x `qn` outputs at `out` (type f32 or T), rows `ld` apart.
-  __device__ static __forceinline__ void store(const Acc& acc, void* out, bool f32, int64_t ld, int pn, int qn) {
+  // Writes the tile's first `pn` outputs of each row at `out` (type f32 or T),
+  // rows `ld` apart; row(q) is the place of tile row q (below 0: not stored).
+  template <typename Row>
+  __device__ static __forceinline__ void store(const Acc& acc, void* out, bool f32, int64_t ld, int pn, Row&& row) {
     const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int j = 0; j < NQ; ++j) {
-      const int q = wave_q() + 16 * j + (lane & 15);
-      if (q >= qn) continue;
+      const int64_t q = row(wave_q() + 16 * j + (lane & 15));
+      if (q < 0) continue;
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         const int p = wave_p() + 16 * i + 4 * (lane >> 4);
@@ -284,6 +315,45 @@ struct Gemm {
 __device__ __forceinline__ int64_t xcd_order(int64_t b, int64_t n) {
   const int64_t per = (n + 7) / 8;
   return b / 8 < per ? (b % 8) * per + b / 8 : n;
+}
+
+// Place l of an order over n_rt row tiles x np column tiles: 8 row tiles that
+// share a column tile after one another, then the next column tile.
+__device__ __forceinline__ void tile_at(int64_t l, int n_rt, int np, int& rt, int& pt) {
+  constexpr int kSuper = 8;
+  const int sup = (int)(l / (kSuper * np)), in = (int)(l - (int64_t)sup * kSuper * np);
+  const int wide = max(min(kSuper, n_rt - kSuper * sup), 1);
+  rt = kSuper * sup + in % wide;
+  pt = in / wide;
+}
+
+// The wave's inclusive prefix sums.
+__device__ __forceinline__ int wave_scan(int v, int lane) {
+#pragma unroll
+  for (int s = 1; s < 64; s *= 2) {
+    const int o = __shfl_up(v, s);
+    if (lane >= s) v += o;
+  }
+  return v;
+}
+
+// Rows that can be brought into LDS 16 bytes at a time.
+inline bool rows16(const void* p, int64_t stride) { return ((uintptr_t)p & 15) == 0 && stride % 8 == 0; }
+
+// `blocks` workgroups of Kernel with `lds` bytes of dynamic LDS.
+template <auto Kernel, typename... A>
+int launch_tiles(const char* what, dim3 blocks, int threads, int lds, hipStream_t s, A... args) {
+  static const hipError_t attr = hipFuncSetAttribute((const void*)Kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (attr != hipSuccess) return hip_fail(attr, what);
+  Kernel<<<blocks, dim3(threads), lds, s>>>(args...);
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess ? MOE_OK : hip_fail(e, what);
+}
+
+// Workgroups for `tiles` tiles placed by xcd_order (whole rounds of the XCDs), or 0 where one launch cannot have them.
+inline int64_t tile_blocks(int64_t tiles, int threads) {
+  const int64_t blocks = (tiles + 7) / 8 * 8;
+  return blocks * threads < (int64_t)1 << 32 ? blocks : 0;
 }
 
 }  // namespace moe

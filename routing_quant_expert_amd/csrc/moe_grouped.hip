@@ -17,8 +17,6 @@
 namespace moe {
 namespace {
 
-constexpr int kSuper = 8;   // row tiles that share a weight tile before the next weight tile
-
 struct GroupedArgs {
   const int32_t* offsets;
   int32_t* status;
@@ -35,15 +33,6 @@ __device__ __forceinline__ int edge(const GroupedArgs& a, int e) {
   if (e <= 0) return 0;
   if (e > a.groups + 1) return a.rows;
   return min(max(a.offsets[e - 1], 0), a.rows);
-}
-
-__device__ __forceinline__ int wave_scan(int v, int lane) {
-#pragma unroll
-  for (int s = 1; s < 64; s *= 2) {
-    const int o = __shfl_up(v, s);
-    if (lane >= s) v += o;
-  }
-  return v;
 }
 
 struct Tile {
@@ -87,13 +76,10 @@ __device__ __forceinline__ Tile find_tile(const GroupedArgs& a, int np) {
   const int s = __builtin_ctzll(hits);
   const int first = __shfl(incl2 - cnt, s), n_rt = __shfl(cnt, s);
   const int glo = __shfl(elo, s), ghi = __shfl(ehi, s);
-  // inside the entry: kSuper row tiles after one another, then the next column tile
-  const int64_t l = place - (int64_t)first * np;
-  const int sup = (int)(l / (kSuper * np)), in = (int)(l - (int64_t)sup * kSuper * np);
-  const int wide = min(kSuper, n_rt - kSuper * sup);
-  const int rt = wide > 0 ? kSuper * sup + in % wide : -1;
+  int rt, pt;
+  tile_at(place - (int64_t)first * np, n_rt, np, rt, pt);
   if (rt < 0 || rt >= n_rt) return {0, 0, 0, 0};
-  return {sel * U + s - 1, glo + rt * BQ, min(BQ, ghi - (glo + rt * BQ)), in / wide};
+  return {sel * U + s - 1, glo + rt * BQ, min(BQ, ghi - (glo + rt * BQ)), pt};
 }
 
 // The first workgroup reports offsets that do not ascend or leave [0, rows].
@@ -124,12 +110,12 @@ __global__ __launch_bounds__(G::NT) void k_grouped(GroupedArgs a, const T* __res
   const bool none = t.group < 0 || t.group >= a.groups;
   const int p0 = t.p * G::kP;
   const int64_t in_stride = WCOL ? a.y_stride : a.x_stride, out_stride = WCOL ? a.x_stride : a.y_stride;
-  const Operand<T> P = {w + (none ? 0 : t.group) * a.w_group + (WCOL ? p0 : p0 * a.w_stride), a.w_stride, WCOL ? width - p0 : min(G::kP, width - p0)};
-  const Operand<T> Q = {in + t.row * in_stride, in_stride, t.rows};
+  const Operand<T> P = {w + (none ? 0 : t.group) * a.w_group + (WCOL ? p0 : p0 * a.w_stride), a.w_stride, WCOL ? width - p0 : min(G::kP, width - p0), nullptr};
+  const Operand<T> Q = {in + t.row * in_stride, in_stride, t.rows, nullptr};
   typename G::Acc acc = {};
   G::run(P, Q, none ? 0 : red, lds, acc);
   uint8_t* o = (uint8_t*)out + (t.row * out_stride + p0) * (a.f32 ? 4 : 2);
-  G::store(acc, o, a.f32, out_stride, width - p0, t.rows);
+  G::store(acc, o, a.f32, out_stride, width - p0, [&](int q) { return q < t.rows ? q : -1; });
 }
 
 template <typename T, typename G>
@@ -143,12 +129,12 @@ __global__ __launch_bounds__(G::NT) void k_grouped_dw(GroupedArgs a, const T* __
   const int g = (int)(place / (np * nq)), in = (int)(place % (np * nq));
   const int p0 = in / nq * G::kP, q0 = in % nq * G::kQ;
   const int lo = edge(a, g + 1), hi = max(lo, edge(a, g + 2));
-  const Operand<T> P = {x + lo * a.x_stride + p0, a.x_stride, a.k - p0};
-  const Operand<T> Q = {dy + lo * a.y_stride + q0, a.y_stride, a.n - q0};
+  const Operand<T> P = {x + lo * a.x_stride + p0, a.x_stride, a.k - p0, nullptr};
+  const Operand<T> Q = {dy + lo * a.y_stride + q0, a.y_stride, a.n - q0, nullptr};
   typename G::Acc acc = {};
   G::run(P, Q, hi - lo, lds, acc);
   uint8_t* o = (uint8_t*)dw + (g * a.w_group + q0 * a.w_stride + p0) * (a.f32 ? 4 : 2);
-  G::store(acc, o, a.f32, a.w_stride, a.k - p0, a.n - q0);
+  G::store(acc, o, a.f32, a.w_stride, a.k - p0, [&](int q) { return q0 + q < a.n ? q : -1; });
 }
 
 enum Way { kForward, kInput, kWeight };
@@ -180,20 +166,11 @@ GroupedArgs grouped_args(const moe_grouped& g, const int32_t* offsets, int64_t r
           g.x_stride, g.y_stride, g.w_stride, g.w_group_stride};
 }
 
-// Rows that can be brought into LDS 16 bytes at a time.
-bool rows16(const void* p, int64_t stride) { return ((uintptr_t)p & 15) == 0 && stride % 8 == 0; }
-
-// (`tiles` workgroups, rounded up to whole rounds of the XCDs as xcd_order needs them)
-template <auto Kernel, typename... A>
-int launch(int64_t tiles, int threads, int lds, hipStream_t s, A... args) {
-  const int64_t blocks = (tiles + 7) / 8 * 8;
-  if (blocks * threads >= (int64_t)1 << 32)
-    return fail(MOE_EUNSUPPORTED, "grouped: too many tiles for one launch%s (%lld)", "", blocks);
-  static const hipError_t attr = hipFuncSetAttribute((const void*)Kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-  if (attr != hipSuccess) return hip_fail(attr, "grouped");
-  Kernel<<<dim3((unsigned)blocks), dim3(threads), lds, s>>>(args...);
-  const hipError_t e = hipGetLastError();
-  return e == hipSuccess ? MOE_OK : hip_fail(e, "grouped");
+template <auto Kernel, typename G, typename... A>
+int launch(int64_t tiles, hipStream_t s, A... args) {
+  const int64_t blocks = tile_blocks(tiles, G::NT);
+  if (!blocks) return fail(MOE_EUNSUPPORTED, "grouped: too many tiles for one launch%s (%lld)", "", tiles);
+  return launch_tiles<Kernel>("grouped", dim3((unsigned)blocks), G::NT, G::kLds, s, args...);
 }
 
 template <typename T, bool WCOL, typename G>
@@ -201,7 +178,7 @@ int launch_rows(const GroupedArgs& a, const void* in, const void* w, void* out, 
   const int width = WCOL ? a.k : a.n;
   const int64_t some = a.groups + 2 < a.rows ? a.groups + 2 : a.rows;   // entries that can have rows
   const int64_t row_tiles = (a.rows + (G::kQ - 1) * some) / G::kQ;
-  return launch<k_grouped<T, WCOL, G>>(row_tiles * ((width + G::kP - 1) / G::kP), G::NT, G::kLds, s, a, (const T*)in,
+  return launch<k_grouped<T, WCOL, G>, G>(row_tiles * ((width + G::kP - 1) / G::kP), s, a, (const T*)in,
                                        (const T*)w, out);
 }
 
@@ -216,7 +193,7 @@ int launch_rows_as(const GroupedArgs& a, const void* in, const void* w, void* ou
 template <typename T, typename G>
 int launch_dw(const GroupedArgs& a, const void* dy, const void* x, void* dw, hipStream_t s) {
   const int64_t tiles = (int64_t)((a.k + G::kP - 1) / G::kP) * ((a.n + G::kQ - 1) / G::kQ) * a.groups;
-  return launch<k_grouped_dw<T, G>>(tiles, G::NT, G::kLds, s, a, (const T*)dy, (const T*)x, dw);
+  return launch<k_grouped_dw<T, G>, G>(tiles, s, a, (const T*)dy, (const T*)x, dw);
 }
 
 template <typename T>

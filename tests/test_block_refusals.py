@@ -152,3 +152,62 @@ def test_grouped_arguments():
     # nothing to write: no pointers needed
     assert L.moe_grouped_forward(ctypes.byref(g), None, None, 4096, 0, None, None, None) == 0
     assert L.moe_grouped_forward(ctypes.byref(g), None, None, None, 0, None, None, None) == EINVAL
+
+
+def adapters(**over):
+    import torch
+    p = R.Adapters(torch.zeros(3, 8, 32, dtype=torch.bfloat16), torch.zeros(3, 64, 8, dtype=torch.bfloat16), out=torch.float32)
+    for k, v in over.items():
+        setattr(p, k, v)
+    return p
+
+
+BIG = R.MOE_GROUPED_MAX_STRIDE + 1
+ADAPTER_BAD = [({"n_adapters": 0}, EINVAL), ({"rank": 0}, EINVAL), ({"n": 0}, EINVAL), ({"k": 0}, EINVAL),
+               ({"n_adapters": R.MOE_ADAPTER_MAX_ADAPTERS + 1}, EUNSUPPORTED),
+               ({"rank": R.MOE_ADAPTER_MAX_RANK + 1}, EUNSUPPORTED), ({"type": 2}, EINVAL), ({"out_type": 1}, EINVAL),
+               ({"x_stride": 31}, EINVAL), ({"w_stride": 31}, EINVAL), ({"a_stride": 31}, EINVAL),
+               ({"b_stride": 7}, EINVAL), ({"out_stride": 63}, EINVAL), ({"a_group_stride": 8 * 32 - 1}, EINVAL),
+               ({"b_group_stride": 64 * 8 - 1}, EINVAL), ({"a": None}, EINVAL), ({"b": None}, EINVAL),
+               ({"a": 4097}, EINVAL), ({"b": 4097}, EINVAL), ({"factor": 4098}, EINVAL)]
+ADAPTER_BAD += [({k: BIG, "a_group_stride": 1 << 40, "b_group_stride": 1 << 40}, EUNSUPPORTED)
+                for k in ("x_stride", "w_stride", "out_stride", "a_stride", "b_stride")]
+
+
+@pytest.mark.parametrize("over,code", ADAPTER_BAD, ids=lambda v: str(v))
+def test_adapter_description(over, code):
+    p = adapters(**over)
+    refused(code, lambda: R.adapter_project(p, P, P, P, P, P, stream=0))
+    assert R.adapter_workspace_bytes(p, 4) == 0
+
+
+def test_adapter_arguments():
+    import torch
+    p = adapters()
+    odd, odd2 = Fake(4097), Fake(4098)
+    f = R.adapter_project
+    for a in ([Fake(0), P, P, P], [P, None, P, P], [P, P, None, P], [P, P, P, None], [odd, P, P, P], [P, odd, P, P],
+              [P, P, odd2, P], [P, P, P, odd2]):
+        refused(EINVAL, lambda: f(p, *a, P, stream=0))
+    refused(EINVAL, lambda: f(p, P, P, P, P, P, status=odd2, stream=0))
+    refused(EINVAL, lambda: f(p, P, P, P, P, None, stream=0))
+    refused(EINVAL, lambda: f(p, P, P, P, P, Fake(4096 + 128), stream=0))
+    for m in (1, 64, 65, 1000, R.MOE_ADAPTER_MAX_TOKENS):
+        need = R.adapter_workspace_bytes(p, m)
+        assert need > 0 and need % 256 == 0
+        if m != 64:
+            continue
+        refused(EWORKSPACE, lambda: f(p, Fake(rows=m), P, P, P, Fake(n=need - 1), stream=0))
+    sizes = [R.adapter_workspace_bytes(p, m) for m in (1, 10, 64, 65, 200, 5000)]
+    assert sizes == sorted(sizes)
+    refused(EINVAL, lambda: f(p, Fake(rows=0), P, P, P, P, stream=0))
+    refused(EUNSUPPORTED, lambda: f(p, Fake(rows=R.MOE_ADAPTER_MAX_TOKENS + 1), P, P, P, P, stream=0))
+    L = R.lib()
+    assert L.moe_adapter_project(None, 4096, 4096, 4096, 1, 4096, 4096, 1 << 30, None, None) == EINVAL
+    a, b = torch.zeros(3, 8, 32, dtype=torch.bfloat16), torch.zeros(3, 64, 8, dtype=torch.bfloat16)
+    for call in (lambda: R.Adapters(a, b[:2]), lambda: R.Adapters(a, b.half()), lambda: R.Adapters(a, b[:, :, :7]),
+                 lambda: R.Adapters(a.transpose(1, 2).contiguous().transpose(1, 2), b),
+                 lambda: R.Adapters(a, b, torch.zeros(3, dtype=torch.float16)),
+                 lambda: R.Adapters(a, b, torch.zeros(4)), lambda: R.Adapters(a, b, torch.zeros(6)[::2]),
+                 lambda: R.Adapters(a.double(), b.double())):
+        refused(EINVAL, call)
