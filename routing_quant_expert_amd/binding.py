@@ -128,9 +128,10 @@ def _ptr(t):
 
 def _stream(stream):
     if stream is None:
+        # the current device's current stream, without the Stream object that torch.cuda.current_stream() makes (3 us)
         import torch
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-    return ctypes.c_void_p(stream if isinstance(stream, int) else stream.cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def cfg_from_shape(shape) -> Cfg:

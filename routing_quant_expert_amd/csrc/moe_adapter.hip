@@ -1,21 +1,23 @@
 // A shared projection with one low-rank adapter per token (moe_adapter_project):
 //   out[t] = W x[t] + factor[a] B[a] (A[a] x[t]),  a = index[t] (-1: W x[t] alone).
 //
-// Few tokens (m <= 64): the call reads every weight once, so the long sums over
-// k are cut into slices, enough for all CUs to read at once (k_adapter_part: W
-// and the A of the adapters in use, f32 partial sums), and a second launch adds
-// them up with the short products by B (k_adapter_sum, all in f32).
+// Few tokens (or few tiles): the call reads every weight once, so the long
+// sums over k are cut into slices, enough for all CUs to read at once
+// (k_adapter_part: W and the A of the adapters in use, f32 partial sums), and a
+// second launch adds them up with the short products by B (k_adapter_sum, all in f32).
 //
-// More tokens: they are sorted by adapter (k_adapter_sort), every adapter's
-// tokens filled up to whole 16-row slots, u = factor A x is made once per slot
-// in f32 (k_adapter_low), and the tiles of the projection run over the sorted
-// slots (k_adapter_main): after its sum over k a tile goes on with u and B as
-// further terms of the same sums, adapter by adapter, only in the 16-row slots
-// of that adapter: no other token's values meet its weights. u enters those
-// products as two 16-bit terms, its rounded value and the rounded rest (three
-// where a bf16 product makes an f32 output), so that it is exact to 2^-16 of
-// itself at least (2^-24 for f32 outputs of either type, 2^-22 for fp16).
+// More tokens: they are sorted by adapter (k_adapter_sort), u = factor A x is
+// made in f32 by 16 tokens of one adapter (k_adapter_low), and the tiles of
+// the projection run over the sorted tokens (k_adapter_main): after its sum
+// over k a tile goes on with the products of u and B, adapter by adapter, and
+// adds them to the outputs of that adapter's tokens alone: no other token's
+// values meet its weights. u enters those products as two 16-bit terms, its
+// rounded value and the rounded rest (three where a bf16 product makes an f32
+// output), so that it is exact to 2^-16 of itself at least (2^-24 for f32
+// outputs of either type, 2^-22 for fp16).
 #include <hip/hip_runtime.h>
+
+#include <algorithm>
 
 #include "moe_gemm.h"
 #include "moe_host.h"
@@ -23,8 +25,8 @@
 namespace moe {
 namespace {
 
-constexpr int kFewTokens = 64;        // a wave's lanes hold one token each in k_adapter_part
-constexpr int kSlotTile = 128;        // the sorted slots are padded to the largest tile
+constexpr int kTokenTile = 64;   // a wave's lanes hold one token each in k_adapter_part
+constexpr int kRowTile = 128;    // the sorted tokens are padded to the largest tile
 
 struct AdapterArgs {
   int adapters, rank, n, k;
@@ -49,14 +51,22 @@ __device__ __forceinline__ float factor_of(const AdapterArgs& a, int i) { return
 
 // ---- few tokens -----------------------------------------------------------
 
-// Slices of the sum over k: `count` of `len` (a multiple of a step).
+// Whether m tokens take the sliced sums: 64 tokens, or so few tiles of 64 x 64
+// that most CUs would have none.
+bool few_tokens(int n, int64_t m) {
+  return m <= kTokenTile || (m <= 512 && (m + 63) / 64 * ((n + 63) / 64) <= 128);
+}
+
+// Slices of the sum over k: `count` of `len` (a multiple of a step). Two
+// workgroups a CU for the projection's own tiles where tokens are few (one
+// token of 2048 x 4096: all of W is asked for at once), one where the partial sums themselves are much to move.
 struct Slices {
   int count, len;
 };
-Slices slices_of(int n, int k) {
-  const int tiles = (n + 63) / 64, most = (k + 255) / 256;
-  int count = (384 + tiles - 1) / tiles;
-  count = count < most ? count : most;
+Slices slices_of(int n, int k, int64_t m) {
+  const int64_t tiles = (int64_t)((n + 63) / 64) * ((m + kTokenTile - 1) / kTokenTile);
+  const int64_t most = (k + 255) / 256, want = ((m <= 16 ? 512 : 256) + tiles - 1) / tiles;
+  const int count = (int)(want < most ? want : most);
   const int len = ((k + count - 1) / count + kStep - 1) / kStep * kStep;
   return {(k + len - 1) / len, len};
 }
@@ -64,15 +74,15 @@ Slices slices_of(int n, int k) {
 // Tile `t` of a slice: the W tiles, then each adapter's A tiles; partial sums
 // [slice][m][n] of W x and [slice][m][rank] of A x (of a token's own adapter).
 template <typename T, typename G>
-__global__ __launch_bounds__(G::NT) void k_adapter_part(AdapterArgs a, Slices sl, const T* __restrict__ x,
+__global__ __launch_bounds__(G::NT, 2) void k_adapter_part(AdapterArgs a, Slices sl, const T* __restrict__ x,
                                                         const T* __restrict__ w, const T* __restrict__ wa,
                                                         float* __restrict__ part, float* __restrict__ upart) {
   extern __shared__ __align__(16) uint8_t lds[];
   const int lane = threadIdx.x & 63;
   const int wt = (a.n + G::kP - 1) / G::kP, rt = (a.rank + G::kP - 1) / G::kP;
-  const int slice = blockIdx.y, tile = blockIdx.x;
-  const int mine = lane < a.m ? adapter_of(a, lane) : -1;
-  if (a.status && tile == 0 && slice == 0 && threadIdx.x < 64 && lane < a.m && bad_index(a, lane))
+  const int slice = blockIdx.y, tile = blockIdx.x, t0 = blockIdx.z * kTokenTile, tokens = min(a.m - t0, kTokenTile);
+  const int mine = lane < tokens ? adapter_of(a, t0 + lane) : -1;
+  if (a.status && tile == 0 && slice == 0 && threadIdx.x < 64 && lane < tokens && bad_index(a, t0 + lane))
     atomicOr(a.status, MOE_STATUS_BAD_ADAPTER);
   const bool base = tile < wt;
   const int adapter = base ? -1 : (tile - wt) / rt;
@@ -81,139 +91,192 @@ __global__ __launch_bounds__(G::NT) void k_adapter_part(AdapterArgs a, Slices sl
   const int p0 = (base ? tile : (tile - wt) % rt) * G::kP, width = base ? a.n : a.rank;
   const int k0 = slice * sl.len, red = min(sl.len, a.k - k0);
   const Operand<T> P = {base ? w + p0 * a.w_stride + k0 : wa + adapter * a.a_group + p0 * a.a_stride + k0,
-                        base ? a.w_stride : a.a_stride, min(G::kP, width - p0), nullptr};
-  const Operand<T> Q = {x + k0, a.x_stride, a.m, nullptr};
+                        base ? a.w_stride : a.a_stride, min(G::kP, width - p0), nullptr, a.k >= 8};
+  const Operand<T> Q = {x + t0 * a.x_stride + k0, a.x_stride, tokens, nullptr, a.k >= 8};
   typename G::Acc acc = {};
   G::run(P, Q, red, lds, acc);
-  float* out = (base ? part : upart) + (int64_t)slice * a.m * width + p0;
-  G::store(acc, out, true, width, width - p0,
-           [&](int q) { return q < a.m && (base || (users >> q & 1)) ? q : -1; });
+  float* out = (base ? part : upart) + ((int64_t)slice * a.m + t0) * width + p0;
+  G::store(acc, out, true, false, width, width - p0,
+           [&](int q) { return q < tokens && (base || (users >> q & 1)) ? q : -1; });
 }
 
+// 256 columns of one token: the slices' sums, in order, then the rank terms.
 template <typename T, typename U>
 __global__ __launch_bounds__(256) void k_adapter_sum(AdapterArgs a, int slices, const T* __restrict__ wb,
                                                      const float* __restrict__ part, const float* __restrict__ upart,
                                                      U* __restrict__ out) {
   __shared__ float u[MOE_ADAPTER_MAX_RANK];
-  const int t = blockIdx.y, c = blockIdx.x * 256 + threadIdx.x;
+  const int t = blockIdx.y, c = blockIdx.x * 256 + threadIdx.x, col = min(c, a.n - 1);
   const int mine = adapter_of(a, t);
+  auto total = [&](const float* from, int width) {
+    from += (int64_t)t * width;
+    float s = 0.0f;
+#pragma unroll 8
+    for (int i = 0; i < slices; ++i) s += from[(int64_t)i * a.m * width];
+    return s;
+  };
+  float s = total(part + col, a.n);
   if (mine >= 0) {
-    for (int j = threadIdx.x; j < a.rank; j += 256) {
-      float s = 0.0f;
-      for (int i = 0; i < slices; ++i) s += upart[((int64_t)i * a.m + t) * a.rank + j];
-      u[j] = factor_of(a, mine) * s;
-    }
+    for (int j = threadIdx.x; j < a.rank; j += 256) u[j] = factor_of(a, mine) * total(upart + j, a.rank);
   }
   __syncthreads();
-  if (c >= a.n) return;
-  float s = 0.0f;
-  for (int i = 0; i < slices; ++i) s += part[((int64_t)i * a.m + t) * a.n + c];
   if (mine >= 0) {
-    const T* b = wb + mine * a.b_group + c * a.b_stride;
+    const T* b = wb + mine * a.b_group + col * a.b_stride;
+#pragma unroll 2
     for (int j = 0; j < a.rank; j += 8) {
-      const f32x8 v = to_f32(load_oct(b + j, a.rank - j));
+      const f32x8 v = to_f32(load_oct(b + j, a.rank - j, a.rank >= 8));
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (j + i < a.rank) s = fmaf(u[j + i], v[i], s);
     }
   }
-  out[t * a.out_stride + c] = (U)s;
+  if (c < a.n) out[t * a.out_stride + c] = (U)s;
 }
 
 // ---- more tokens ----------------------------------------------------------
 
-// The sorted slots: tokens without an adapter, then adapter by adapter, each
-// filled up to 16 slots with empty ones (token -1), the whole up to a tile.
+// The tokens in the order of their adapters (those without one first), filled
+// up to a tile with rows of no token; and the same rows again adapter by
+// adapter in slots, each adapter's filled up to 16 (row -1).
 struct Sorted {
-  int32_t* slots;   // [1] their number, a multiple of 16
-  int32_t* token;   // [most]
-  int32_t* owner;   // [most / 16] adapter of 16 slots, or -1
-  float* u;         // [most][rank_pad]: factor A x
+  int32_t* token;   // [padded] or -1
+  int32_t* owner;   // [padded] the row's adapter, or -1
+  int32_t* slots;   // [1] number of slots, a multiple of 16
+  int32_t* row;     // [most slots] sorted row, or -1
+  int32_t* user;    // [most slots / 16] adapter of 16 slots
+  float* u;         // [padded][rank_pad]: factor A x
   int rank_pad;
 };
 
+int64_t padded_rows(int64_t m) { return (m + kRowTile - 1) / kRowTile * kRowTile; }
 int64_t most_slots(int64_t m, int adapters) {
-  const int64_t used = adapters + 1 < m ? adapters + 1 : m;
-  return (m + 15 * used + kSlotTile - 1) / kSlotTile * kSlotTile;
+  const int64_t used = adapters < m ? adapters : m;
+  return (m + 15 * used) / 16 * 16;
 }
 int rank_pad(int rank) { return (rank + kStep - 1) / kStep * kStep; }
 
-// One workgroup: counts, starts and places. The places of an adapter's tokens
-// among its own slots depend on the order of the atomics; a token's outputs do not depend on its place.
-__global__ __launch_bounds__(1024) void k_adapter_sort(AdapterArgs a, Sorted so) {
-  __shared__ int count[MOE_ADAPTER_MAX_ADAPTERS + 1], start[MOE_ADAPTER_MAX_ADAPTERS + 2];
-  const int tid = threadIdx.x, buckets = a.adapters + 1;
+// One workgroup: counts, starts and places (of bucket 0, the tokens without an
+// adapter, then bucket by bucket). The order of an adapter's tokens depends
+// on the order of the atomics; a token's outputs do not depend on its place.
+__global__ __launch_bounds__(1024) void k_adapter_sort(AdapterArgs a, Sorted so, int padded) {
+  __shared__ int count[MOE_ADAPTER_MAX_ADAPTERS + 1], start[MOE_ADAPTER_MAX_ADAPTERS + 1], slot[MOE_ADAPTER_MAX_ADAPTERS + 1];
+  const int tid = threadIdx.x, lane = tid & 63, buckets = a.adapters + 1;
   for (int b = tid; b < buckets; b += 1024) count[b] = 0;
   __syncthreads();
+  // Counts the lanes that are there in their buckets (by one lane where all have the same): the lane's place in its own.
+  auto add = [&](bool there, int b) -> int {
+    const uint64_t lanes = __ballot(there);
+    if (!lanes) return 0;
+    const int leader = __builtin_ctzll(lanes), first = __shfl(b, leader);
+    if (lanes != __ballot(there && b == first)) return there ? atomicAdd(&count[b], 1) : 0;
+    int at = 0;
+    if (lane == leader) at = atomicAdd(&count[b], __popcll(lanes));
+    return __shfl(at, leader) + (int)__popcll(lanes & ((1ull << lane) - 1));
+  };
+  constexpr int kHeld = 4;   // tokens whose bucket and place a thread keeps
+  int held[kHeld], place[kHeld];
   bool bad = false;
-  for (int t = tid; t < a.m; t += 1024) {
-    atomicAdd(&count[adapter_of(a, t) + 1], 1);
-    bad = bad || bad_index(a, t);
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int t = tid + 1024 * i;
+    held[i] = t < a.m ? adapter_of(a, t) + 1 : 0;
+    bad = bad || (t < a.m && bad_index(a, t));
+  }
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) place[i] = add(tid + 1024 * i < a.m, held[i]);
+  if (a.m > 1024 * kHeld) __syncthreads();   // the held tokens take the first places
+  for (int t0 = 1024 * kHeld; t0 < a.m; t0 += 1024) {
+    const int t = t0 + tid;
+    add(t < a.m, t < a.m ? adapter_of(a, t) + 1 : 0);
+    bad = bad || (t < a.m && bad_index(a, t));
   }
   if (a.status && bad) atomicOr(a.status, MOE_STATUS_BAD_ADAPTER);
   __syncthreads();
   if (tid < 64) {
-    int sum = 0;
+    int rows = 0, slots = 0;
     for (int b0 = 0; b0 < buckets; b0 += 64) {
-      const int v = b0 + tid < buckets ? (count[b0 + tid] + 15) / 16 * 16 : 0;
-      const int incl = wave_scan(v, tid);
-      if (b0 + tid < buckets) start[b0 + tid] = sum + incl - v;
-      sum += __shfl(incl, 63);
+      const int b = b0 + tid, v = b < buckets ? count[b] : 0, w = b > 0 ? (v + 15) / 16 * 16 : 0;
+      const int rows_to = wave_scan(v, tid), slots_to = wave_scan(w, tid);
+      if (b < buckets) {
+        start[b] = rows + rows_to - v;
+        slot[b] = slots + slots_to - w;
+      }
+      rows += __shfl(rows_to, 63);
+      slots += __shfl(slots_to, 63);
     }
-    if (tid == 0) start[buckets] = sum;
+    if (tid == 0) *so.slots = slots;
   }
   __syncthreads();
-  const int total = start[buckets], padded = (total + kSlotTile - 1) / kSlotTile * kSlotTile;
-  for (int b = tid; b < buckets; b += 1024)
-    for (int i = start[b] + count[b]; i < start[b + 1]; ++i) so.token[i] = -1;
-  for (int i = total + tid; i < padded; i += 1024) so.token[i] = -1;
-  for (int s = tid; s < padded / 16; s += 1024) {
-    int lo = 0, hi = buckets;   // the last bucket that starts at or before the 16 slots
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (start[mid] <= 16 * s) lo = mid;
-      else hi = mid;
-    }
-    so.owner[s] = 16 * s < total ? lo - 1 : -1;
+  for (int i = a.m + tid; i < padded; i += 1024) {
+    so.token[i] = -1;
+    so.owner[i] = -1;
   }
-  if (tid == 0) *so.slots = total;
+  for (int b = 1 + tid; b < buckets; b += 1024) {
+    const int v = count[b], end = (v + 15) / 16 * 16;
+    for (int i = v; i < end; ++i) so.row[slot[b] + i] = -1;
+    for (int i = 0; i < end; i += 16) so.user[(slot[b] + i) / 16] = b - 1;
+  }
+  auto put = [&](int t, int b, int at) {
+    const int row = start[b] + at;
+    so.token[row] = t;
+    so.owner[row] = b - 1;
+    if (b > 0) so.row[slot[b] + at] = row;
+  };
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    if (tid + 1024 * i < a.m) put(tid + 1024 * i, held[i], place[i]);
+  if (a.m <= 1024 * kHeld) return;
+  // the others' places: counted again, from the held tokens' numbers up
   __syncthreads();
-  for (int t = tid; t < a.m; t += 1024) {
-    const int b = adapter_of(a, t) + 1;
-    so.token[start[b] + atomicSub(&count[b], 1) - 1] = t;
+  for (int b = tid; b < buckets; b += 1024) count[b] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) add(true, held[i]);
+  __syncthreads();
+  for (int t0 = 1024 * kHeld; t0 < a.m; t0 += 1024) {
+    const int t = t0 + tid, b = t < a.m ? adapter_of(a, t) + 1 : 0;
+    const int at = add(t < a.m, b);
+    if (t < a.m) put(t, b, at);
   }
 }
 
-// u of 16 slots and 64 ranks: the four waves take every fourth 32 of k, their sums meet in LDS.
+// u of 16 slots and 64 ranks: the eight waves take every eighth 32 of k, their sums meet in LDS.
+constexpr int kLowWaves = 8;
 template <typename T, int NA>
-__global__ __launch_bounds__(256) void k_adapter_low(AdapterArgs a, Sorted so, const T* __restrict__ x,
-                                                     const T* __restrict__ wa) {
-  __shared__ float red[4][16][NA * 16 + 1];
+__global__ __launch_bounds__(64 * kLowWaves) void k_adapter_low(AdapterArgs a, Sorted so, const T* __restrict__ x,
+                                                                const T* __restrict__ wa) {
+  __shared__ float red[kLowWaves][16][NA * 16 + 1];
   const int s = blockIdx.x, r0 = blockIdx.y * kStep;
   if (16 * s >= *so.slots) return;
-  const int mine = so.owner[s];
-  if (mine < 0) return;
+  const int mine = so.user[s];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row = lane & 15, part = 8 * (lane >> 4);
-  const T* xr = x + max(so.token[16 * s + row], 0) * a.x_stride + part;
+  const T* xr = x + max(so.token[max(so.row[16 * s + row], 0)], 0) * a.x_stride + part;
   const T* ar[NA];
 #pragma unroll
   for (int i = 0; i < NA; ++i)
     ar[i] = wa + mine * a.a_group + min(r0 + 16 * i + row, a.rank - 1) * a.a_stride + part;
   f32x4 acc[NA] = {};
   int k = 32 * wave;
-#pragma unroll 4
-  for (; k + 32 <= a.k; k += 128) {
-    oct<T> xv, av[NA];
-    __builtin_memcpy(&xv, xr + k, 16);
+  auto some = [&](auto count) {   // `count` of the wave's 32 k, all loads at once
+    oct<T> xv[count], av[count][NA];
 #pragma unroll
-    for (int i = 0; i < NA; ++i) __builtin_memcpy(&av[i], ar[i] + k, 16);
+    for (int n = 0; n < count; ++n) {
+      __builtin_memcpy(&xv[n], xr + k + 32 * kLowWaves * n, 16);
 #pragma unroll
-    for (int i = 0; i < NA; ++i) acc[i] = mfma16(av[i], xv, acc[i]);
-  }
+      for (int i = 0; i < NA; ++i) __builtin_memcpy(&av[n][i], ar[i] + k + 32 * kLowWaves * n, 16);
+    }
+#pragma unroll
+    for (int n = 0; n < count; ++n)
+#pragma unroll
+      for (int i = 0; i < NA; ++i) acc[i] = mfma16(av[n][i], xv[n], acc[i]);
+    k += 32 * kLowWaves * count;
+  };
+  while (k + 3 * 32 * kLowWaves + 32 <= a.k) some(std::integral_constant<int, 4>());
+  while (k + 32 <= a.k) some(std::integral_constant<int, 1>());
   if (k < a.k) {
-    const oct<T> xv = load_oct(xr + k, a.k - k - part);
+    const oct<T> xv = load_oct(xr + k, a.k - k - part, a.k >= 8);
 #pragma unroll
-    for (int i = 0; i < NA; ++i) acc[i] = mfma16(load_oct(ar[i] + k, a.k - k - part), xv, acc[i]);
+    for (int i = 0; i < NA; ++i) acc[i] = mfma16(load_oct(ar[i] + k, a.k - k - part, a.k >= 8), xv, acc[i]);
   }
 #pragma unroll
   for (int i = 0; i < NA; ++i)
@@ -221,20 +284,24 @@ __global__ __launch_bounds__(256) void k_adapter_low(AdapterArgs a, Sorted so, c
     for (int r = 0; r < 4; ++r) red[wave][row][16 * i + 4 * (lane >> 4) + r] = acc[i][r];
   __syncthreads();
   const float f = factor_of(a, mine);
-  for (int i = threadIdx.x; i < 16 * kStep; i += 256) {
-    const int slot = i / kStep, j = i % kStep;
+  for (int i = threadIdx.x; i < 16 * kStep; i += 64 * kLowWaves) {
+    const int slot = i / kStep, j = i % kStep, to = so.row[16 * s + slot];
+    if (to < 0) continue;
     float v = 0.0f;
-    if (j < NA * 16 && r0 + j < a.rank)
-      v = f * ((red[0][slot][j] + red[1][slot][j]) + (red[2][slot][j] + red[3][slot][j]));
-    so.u[(int64_t)(16 * s + slot) * so.rank_pad + r0 + j] = v;
+    if (j < NA * 16 && r0 + j < a.rank) {
+#pragma unroll
+      for (int w = 0; w < kLowWaves; ++w) v += red[w][slot][j];
+      v *= f;
+    }
+    so.u[(int64_t)to * so.rank_pad + r0 + j] = v;
   }
 }
 
-// u of a tile's slots and 64 ranks as `PIECES` 16-bit tiles whose sum it is.
+// u of a tile's rows and 64 ranks as `PIECES` 16-bit tiles whose sum it is.
 // fp16: a row whose largest value would pass the type's range is scaled by a
-// power of two (row_scale), and its sums beside it.
+// power of two (row_scale), and its products back.
 template <typename T, typename G, int PIECES>
-__device__ __forceinline__ void stage_u(const Sorted& so, int slot0, int r0, uint8_t* tiles, float* row_scale) {
+__device__ __forceinline__ void stage_u(const Sorted& so, int row0, int r0, uint8_t* tiles, float* row_scale) {
   typedef typename G::QT QT;
 #pragma unroll
   for (int k = 0; k < QT::kPer; ++k) {
@@ -242,7 +309,7 @@ __device__ __forceinline__ void stage_u(const Sorted& so, int slot0, int r0, uin
     int r, row;
     QT::place(i, r, row);
     f32x8 v = {};
-    if (so.owner[(slot0 + row) / 16] >= 0) v = load_oct(so.u + (int64_t)(slot0 + row) * so.rank_pad + r0 + r, 8);
+    if (so.owner[row0 + row] >= 0) v = load_oct(so.u + (int64_t)(row0 + row) * so.rank_pad + r0 + r, 8, true);
     if constexpr (std::is_same_v<T, fp16_t>) {
       float most = 0.0f;
 #pragma unroll
@@ -266,56 +333,47 @@ __device__ __forceinline__ void stage_u(const Sorted& so, int slot0, int r0, uin
 }
 
 template <typename T, typename G, int PIECES>
-__global__ __launch_bounds__(G::NT) void k_adapter_main(AdapterArgs a, Sorted so, const T* __restrict__ x,
-                                                        const T* __restrict__ w, const T* __restrict__ wb,
-                                                        void* __restrict__ out) {
+__global__ __launch_bounds__(G::NT, 2) void k_adapter_main(AdapterArgs a, Sorted so, const T* __restrict__ x,
+                                                           const T* __restrict__ w, const T* __restrict__ wb,
+                                                           void* __restrict__ out) {
   extern __shared__ __align__(16) uint8_t lds[];
   __shared__ float row_scale[G::kQ];
   static_assert(G::PT::kBytes + PIECES * G::QT::kBytes <= G::kLds, "the tiles of u and B fit the ring's LDS");
-  const int np = (a.n + G::kP - 1) / G::kP, nq = (*so.slots + G::kQ - 1) / G::kQ;
+  const int np = (a.n + G::kP - 1) / G::kP, nq = (a.m + G::kQ - 1) / G::kQ;
   const int64_t total = (int64_t)np * nq, place = xcd_order(blockIdx.x, total);
   if (place >= total) return;
   int qt, pt;
   tile_at(place, nq, np, qt, pt);
-  const int p0 = pt * G::kP, slot0 = qt * G::kQ;
-  const Operand<T> P = {w + p0 * a.w_stride, a.w_stride, min(G::kP, a.n - p0), nullptr};
-  const Operand<T> Q = {x, a.x_stride, G::kQ, so.token + slot0};
+  const int p0 = pt * G::kP, row0 = qt * G::kQ, lane = threadIdx.x & 63;
+  const Operand<T> P = {w + p0 * a.w_stride, a.w_stride, min(G::kP, a.n - p0), nullptr, a.k >= 8};
+  const Operand<T> Q = {x, a.x_stride, G::kQ, so.token + row0, a.k >= 8};
   typename G::Acc acc = {};
   G::run(P, Q, a.k, lds, acc);
 
-  int owner[G::kQ / 16], any = -1;
+  constexpr int kOwners = (G::kQ + 63) / 64;
+  int owner[kOwners];   // of row 64 i + lane of the tile: ascending, but for rows of no token at the end
 #pragma unroll
-  for (int j = 0; j < G::kQ / 16; ++j) {
-    owner[j] = __builtin_amdgcn_readfirstlane(so.owner[slot0 / 16 + j]);
-    any = max(any, owner[j]);
-  }
-  for (int r0 = 0; any >= 0 && r0 < a.rank; r0 += kStep) {
+  for (int i = 0; i < kOwners; ++i) owner[i] = so.owner[row0 + 64 * i + lane];
+  int mine[G::NQ];      // of the rows whose outputs this lane holds
+#pragma unroll
+  for (int j = 0; j < G::NQ; ++j) mine[j] = so.owner[row0 + G::wave_q() + 16 * j + (lane & 15)];
+  // the first adapter of the tile above `done`, or -1
+  auto after = [&](int done) {
+    int next = -1;
+#pragma unroll
+    for (int i = kOwners - 1; i >= 0; --i) {
+      const uint64_t rows = __ballot(owner[i] > done);
+      if (rows) next = __builtin_amdgcn_readlane(owner[i], __builtin_ctzll(rows));
+    }
+    return next;
+  };
+  const int first = after(-1);
+  for (int r0 = 0; first >= 0 && r0 < a.rank; r0 += kStep) {
     uint8_t* const ut = lds + G::PT::kBytes;
     lds_barrier();
-    stage_u<T, G, PIECES>(so, slot0, r0, ut, row_scale);
-    bool scaled = false;
-    if constexpr (std::is_same_v<T, fp16_t>) {
-      lds_barrier();
-#pragma unroll
-      for (int j = 0; j < G::NQ; ++j) {
-        const float s = row_scale[G::wave_q() + 16 * j + (threadIdx.x & 15)];
-        if (__ballot(s != 1.0f)) {
-          scaled = true;
-#pragma unroll
-          for (int i = 0; i < G::NP; ++i) acc[i][j] = acc[i][j] * s;
-        }
-      }
-    }
-    for (int done = -1;;) {   // the adapters of the tile, ascending
-      int next = INT32_MAX;
-#pragma unroll
-      for (int j = 0; j < G::kQ / 16; ++j)
-        if (owner[j] > done) next = min(next, owner[j]);
-      if (next == INT32_MAX) break;
-      uint32_t some = 0;
-#pragma unroll
-      for (int j = 0; j < G::kQ / 16; ++j) some |= owner[j] == next ? 1u << j : 0u;
-      const Operand<T> B = {wb + next * a.b_group + p0 * a.b_stride + r0, a.b_stride, min(G::kP, a.n - p0), nullptr};
+    stage_u<T, G, PIECES>(so, row0, r0, ut, row_scale);
+    for (int next = first; next >= 0; next = after(next)) {
+      const Operand<T> B = {wb + next * a.b_group + p0 * a.b_stride + r0, a.b_stride, min(G::kP, a.n - p0), nullptr, a.rank >= 8};
       typename G::PT::Off off[G::PT::kPer];
       oct<T> v[G::PT::kPer];
       G::PT::template offsets<false>(B, off);
@@ -323,23 +381,21 @@ __global__ __launch_bounds__(G::NT) void k_adapter_main(AdapterArgs a, Sorted so
       G::PT::store(v, lds);
       lds_barrier();
 #pragma unroll
-      for (int p = 0; p < PIECES; ++p) G::compute_some(lds, ut + p * G::QT::kBytes, some, acc);
-      lds_barrier();
-      done = next;
-    }
-    if constexpr (std::is_same_v<T, fp16_t>) {
-      if (scaled) {
+      for (int j = 0; j < G::NQ; ++j) {
+        if (!__ballot(mine[j] == next)) continue;
+        f32x4 low[G::NP] = {};
+        G::template multiply_row<PIECES>(lds, ut, j, low);
+        float back = 1.0f;
+        if constexpr (std::is_same_v<T, fp16_t>) back = 1.0f / row_scale[G::wave_q() + 16 * j + (lane & 15)];
 #pragma unroll
-        for (int j = 0; j < G::NQ; ++j) {
-          const float s = 1.0f / row_scale[G::wave_q() + 16 * j + (threadIdx.x & 15)];
-#pragma unroll
-          for (int i = 0; i < G::NP; ++i) acc[i][j] = acc[i][j] * s;
-        }
+        for (int i = 0; i < G::NP; ++i)
+          if (mine[j] == next) acc[i][j] = acc[i][j] + low[i] * back;
       }
+      lds_barrier();
     }
   }
   uint8_t* o = (uint8_t*)out + (int64_t)p0 * (a.f32 ? 4 : 2);
-  G::store(acc, o, a.f32, a.out_stride, a.n - p0, [&](int q) { return so.token[slot0 + q]; });
+  G::store(acc, o, a.f32, false, a.out_stride, a.n - p0, [&](int q) { return so.token[row0 + q]; });
 }
 
 int check_adapters(const moe_adapters* p, int64_t m) {
@@ -369,22 +425,24 @@ int check_adapters(const moe_adapters* p, int64_t m) {
 
 size_t round256(size_t v) { return (v + 255) & ~(size_t)255; }
 
-// Bytes of the parts of the workspace: few tokens: the partial sums; more: slots, tokens, owners, u.
+// Bytes of the parts of the workspace: few tokens: the partial sums; more: the sorted rows and u.
 struct AdapterWs {
-  size_t part, upart, slots, token, owner, u, total;
+  size_t part, upart, owner, slots, row, user, u, total;
 };
 AdapterWs adapter_ws(const moe_adapters& p, int64_t m) {
   AdapterWs w = {};
-  if (m <= kFewTokens) {
-    const Slices s = slices_of(p.n, p.k);
+  if (few_tokens(p.n, m)) {
+    const Slices s = slices_of(p.n, p.k, m);
     w.upart = round256((size_t)s.count * m * p.n * 4);
     w.total = w.upart + round256((size_t)s.count * m * p.rank * 4);
   } else {
-    const size_t most = (size_t)most_slots(m, p.n_adapters);
-    w.token = 256;
-    w.owner = w.token + round256(most * 4);
-    w.u = w.owner + round256(most / 16 * 4);
-    w.total = w.u + round256(most * rank_pad(p.rank) * 4);
+    const size_t rows = (size_t)padded_rows(m), slots = (size_t)most_slots(m, p.n_adapters);
+    w.owner = rows * 4;
+    w.slots = 2 * w.owner;
+    w.row = w.slots + 256;
+    w.user = w.row + round256(slots * 4);
+    w.u = w.user + round256(slots / 16 * 4);
+    w.total = w.u + rows * rank_pad(p.rank) * 4;
   }
   return w;
 }
@@ -392,16 +450,16 @@ AdapterWs adapter_ws(const moe_adapters& p, int64_t m) {
 template <typename T, bool DMA, int BQ>
 int launch_part(const AdapterArgs& a, Slices sl, const T* x, const T* w, const T* wa, float* part, float* upart,
                 hipStream_t s) {
-  typedef Gemm<T, false, false, 64, BQ, 4, 1, 6, DMA> G;
+  typedef Gemm<T, false, false, 64, BQ, 4, 1, 4, DMA> G;
   const int64_t tiles = (a.n + 63) / 64 + (int64_t)a.adapters * ((a.rank + 63) / 64);
-  return launch_tiles<k_adapter_part<T, G>>("adapters", dim3((unsigned)tiles, sl.count), G::NT, G::kLds, s, a, sl, x, w,
-                                            wa, part, upart);
+  return launch_tiles<k_adapter_part<T, G>>("adapters", dim3((unsigned)tiles, sl.count, (a.m + kTokenTile - 1) / kTokenTile),
+                                            G::NT, G::kLds, s, a, sl, x, w, wa, part, upart);
 }
 
 template <typename T, bool DMA>
 int launch_few(const AdapterArgs& a, const T* x, const T* w, const T* wa, const T* wb, void* out, uint8_t* ws,
                const AdapterWs& l, hipStream_t s) {
-  const Slices sl = slices_of(a.n, a.k);
+  const Slices sl = slices_of(a.n, a.k, a.m);
   float *part = (float*)(ws + l.part), *upart = (float*)(ws + l.upart);
   const int r = a.m <= 16   ? launch_part<T, DMA, 16>(a, sl, x, w, wa, part, upart, s)
                 : a.m <= 32 ? launch_part<T, DMA, 32>(a, sl, x, w, wa, part, upart, s)
@@ -414,35 +472,40 @@ int launch_few(const AdapterArgs& a, const T* x, const T* w, const T* wa, const 
   return e == hipSuccess ? MOE_OK : hip_fail(e, "adapters");
 }
 
-template <typename T, typename G, int PIECES>
+template <typename T, typename G>
 int launch_main(const AdapterArgs& a, const Sorted& so, const T* x, const T* w, const T* wb, void* out, hipStream_t s) {
-  const int64_t tiles = most_slots(a.m, a.adapters) / G::kQ * ((a.n + G::kP - 1) / G::kP);
+  const int64_t tiles = (int64_t)((a.m + G::kQ - 1) / G::kQ) * ((a.n + G::kP - 1) / G::kP);
   const int64_t blocks = tile_blocks(tiles, G::NT);
   if (!blocks) return fail(MOE_EUNSUPPORTED, "adapters: too many tiles for one launch%s (%lld)", "", tiles);
-  return launch_tiles<k_adapter_main<T, G, PIECES>>("adapters", dim3((unsigned)blocks), G::NT, G::kLds, s, a, so, x, w,
-                                                    wb, out);
+  const dim3 grid((unsigned)blocks);
+  if constexpr (std::is_same_v<T, bf16_t>) {
+    if (a.f32) return launch_tiles<k_adapter_main<T, G, 3>>("adapters", grid, G::NT, G::kLds, s, a, so, x, w, wb, out);
+  }
+  return launch_tiles<k_adapter_main<T, G, 2>>("adapters", grid, G::NT, G::kLds, s, a, so, x, w, wb, out);
 }
 
 template <typename T, bool DMA>
 int launch_many(const AdapterArgs& a, const T* x, const T* w, const T* wa, const T* wb, void* out, uint8_t* ws,
                 const AdapterWs& l, hipStream_t s) {
-  const Sorted so = {(int32_t*)ws, (int32_t*)(ws + l.token), (int32_t*)(ws + l.owner), (float*)(ws + l.u),
-                     rank_pad(a.rank)};
-  k_adapter_sort<<<dim3(1), dim3(1024), 0, s>>>(a, so);
+  const Sorted so = {(int32_t*)ws, (int32_t*)(ws + l.owner), (int32_t*)(ws + l.slots), (int32_t*)(ws + l.row),
+                     (int32_t*)(ws + l.user), (float*)(ws + l.u), rank_pad(a.rank)};
+  k_adapter_sort<<<dim3(1), dim3(1024), 0, s>>>(a, so, (int)padded_rows(a.m));
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return hip_fail(e, "adapters");
-  const dim3 grid((unsigned)(most_slots(a.m, a.adapters) / 16), (a.rank + kStep - 1) / kStep);
-  if (a.rank <= 16) k_adapter_low<T, 1><<<grid, dim3(256), 0, s>>>(a, so, x, wa);
-  else if (a.rank <= 32) k_adapter_low<T, 2><<<grid, dim3(256), 0, s>>>(a, so, x, wa);
-  else k_adapter_low<T, 4><<<grid, dim3(256), 0, s>>>(a, so, x, wa);
+  const dim3 grid((unsigned)(most_slots(a.m, a.adapters) / 16), (a.rank + kStep - 1) / kStep), threads(64 * kLowWaves);
+  if (a.rank <= 16) k_adapter_low<T, 1><<<grid, threads, 0, s>>>(a, so, x, wa);
+  else if (a.rank <= 32) k_adapter_low<T, 2><<<grid, threads, 0, s>>>(a, so, x, wa);
+  else k_adapter_low<T, 4><<<grid, threads, 0, s>>>(a, so, x, wa);
   e = hipGetLastError();
   if (e != hipSuccess) return hip_fail(e, "adapters");
-  typedef Gemm<T, false, false, 64, 64, 2, 2, 4, DMA, true> Small;
-  typedef Gemm<T, false, false, 128, 128, 2, 2, 2, DMA, true> Large;
-  const bool small = a.m <= 512;
-  if (std::is_same_v<T, bf16_t> && a.f32)
-    return small ? launch_main<T, Small, 3>(a, so, x, w, wb, out, s) : launch_main<T, Large, 3>(a, so, x, w, wb, out, s);
-  return small ? launch_main<T, Small, 2>(a, so, x, w, wb, out, s) : launch_main<T, Large, 2>(a, so, x, w, wb, out, s);
+  const int64_t rows = (a.m + 127) / 128;
+  if (rows * ((a.n + 127) / 128) < 256)
+    return launch_main<T, Gemm<T, false, false, 64, 64, 2, 2, 4, DMA, true>>(a, so, x, w, wb, out, s);
+  if constexpr (DMA) {
+    if (rows * ((a.n + 255) / 256) >= 768 && a.k >= 1024)
+      return launch_main<T, Gemm<T, false, false, 256, 128, 4, 2, 3, DMA, true>>(a, so, x, w, wb, out, s);
+  }
+  return launch_main<T, Gemm<T, false, false, 128, 128, 2, 2, 2, DMA, true>>(a, so, x, w, wb, out, s);
 }
 
 template <typename T>
@@ -451,7 +514,7 @@ int launch_adapters(const moe_adapters& p, const AdapterArgs& a, const void* x, 
   const AdapterWs l = adapter_ws(p, a.m);
   const T *xt = (const T*)x, *wt = (const T*)w, *wa = (const T*)p.a, *wb = (const T*)p.b;
   const bool dma = rows16(x, a.x_stride) && rows16(w, a.w_stride);
-  if (a.m > kFewTokens)
+  if (!few_tokens(a.n, a.m))
     return dma ? launch_many<T, true>(a, xt, wt, wa, wb, out, ws, l, s)
                : launch_many<T, false>(a, xt, wt, wa, wb, out, ws, l, s);
   return dma && rows16(p.a, a.a_stride) && a.a_group % 8 == 0
@@ -468,9 +531,10 @@ extern "C" {
 
 size_t moe_adapter_workspace_bytes(const moe_adapters* p, int64_t max_m) {
   if (check_adapters(p, max_m)) return 0;
-  const size_t few = adapter_ws(*p, max_m < kFewTokens ? max_m : kFewTokens).total;
-  const size_t all = adapter_ws(*p, max_m).total;
-  return few > all ? few : all;
+  // (the number of slices falls where m grows)
+  size_t most = adapter_ws(*p, max_m).total;
+  for (int64_t m = 1; m < max_m && few_tokens(p->n, m); ++m) most = std::max(most, adapter_ws(*p, m).total);
+  return most;
 }
 
 int moe_adapter_project(const moe_adapters* p, const void* x, const void* w, const int32_t* index, int64_t m,

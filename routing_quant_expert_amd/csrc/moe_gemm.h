@@ -40,18 +40,20 @@ __device__ __forceinline__ f32x4 mfma16(fp16x8_t a, fp16x8_t b, f32x4 c) {
 
 // An operand of one tile: `base` at its first row (column) and r = 0, `count`
 // rows (columns) there, `ld` elements from one row to the next (COL: from one
-// r to the next). Gathered rows: row i of the tile is row rows[i] of base (below 0: any row, its outputs are not stored).
+// r to the next). `room`: the stored rows that this tile is part of (COL: the
+// tile's r lie along several) have 8 elements or more. Gathered rows: row i of the tile is row rows[i] of base (below 0: any row, its outputs are not stored).
 template <typename T>
 struct Operand {
   const T* base;
   int64_t ld;
   int count;
   const int32_t* rows;
+  bool room;
 };
 
 template <typename T, bool COL, int R, int NT, bool GATHER = false>
 struct TileOf {
-  typedef std::conditional_t<GATHER, int64_t, uint32_t> Off;   // a tile's elements stay within 2^32 of its base
+  typedef std::conditional_t<GATHER, int64_t, uint32_t> Off;   // a tile's elements stay within 2^31 of its base
   static constexpr int kBytes = R * kStep * 2;
   static constexpr int kChunks = R * kStep / 8;
   static constexpr int kPer = kChunks >= NT ? kChunks / NT : 1;   // chunks a thread brings in
@@ -59,7 +61,11 @@ struct TileOf {
   static_assert(kChunks % NT == 0 || NT % kChunks == 0, "chunks over threads");
   static_assert(!COL || R >= 64, "the swizzle of a column tile needs 8 chunks a row");
 
-  __device__ static __forceinline__ int swizzle(int row) { return COL ? 2 * (row & 3) : row & 7; }
+  // A transposing read takes four rows of 32 bytes for each quarter of the wave, the quarters 8 rows apart.
+  // Rows of 256 bytes and more all start at LDS bank 0: 8 swizzles keep the 8 rows of half a wave apart (4 where a row has 8 chunks only).
+  __device__ static __forceinline__ int swizzle(int row) {
+    return !COL ? row & 7 : kRowChunks >= 16 ? 2 * ((row & 3) | (row >> 1 & 4)) : 2 * (row & 3);
+  }
 
   // Chunk position i of the tile: r (within the step) and own index of its first element.
   __device__ static __forceinline__ void place(int i, int& r, int& own) {
@@ -93,13 +99,25 @@ struct TileOf {
   }
   __device__ static __forceinline__ int64_t step_stride(const Operand<T>& o) { return COL ? kStep * o.ld : kStep; }
 
-  __device__ static __forceinline__ void dma(const T* at, const Off (&off)[kPer], uint8_t* tile) {
-    uint8_t* first = tile + 16 * 64 * __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) % (kChunks < NT ? kChunks / 64 : NT / 64));
+  // `at` is the same in every lane. The compiler does not see these writes of
+  // LDS: it would wait for all of them before any later LDS read. The waits
+  // are the caller's. (m0 is declared as changed; nothing else in these kernels holds a value there.)
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+  __device__ static __forceinline__ void dma(const T* at, const Off (&off)[kPer], uint32_t tile) {
+    const uint32_t first = tile + 16 * 64 * __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) % (kChunks < NT ? kChunks / 64 : NT / 64));
 #pragma unroll
-    for (int k = 0; k < kPer; ++k)
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(at + off[k]),
-                                       (__attribute__((address_space(3))) void*)(first + 16 * NT * k), 16, 0, 0);
+    for (int k = 0; k < kPer; ++k) {
+      if constexpr (GATHER)
+        asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+                     : : "v"(at + off[k]), "s"(first + 16 * NT * k) : "memory", "m0");
+      else
+        asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+                     : : "v"(2 * off[k]), "s"(at), "s"(first + 16 * NT * k) : "memory", "m0");
+    }
   }
+
+#pragma clang diagnostic pop
 
   // The same through registers, at any alignment: r past `left` and columns
   // past the operand's are zero.
@@ -114,7 +132,7 @@ struct TileOf {
     for (int k = 0; k < kPer; ++k) {
       int r, own;
       place(position(k), r, own);
-      v[k] = load_oct(at + off[k], COL ? (r < left ? o.count - own : 0) : left - r);
+      v[k] = load_oct(at + off[k], COL ? (r < left ? o.count - own : 0) : left - r, o.room);
     }
   }
   __device__ static __forceinline__ void store(const oct<T> (&v)[kPer], uint8_t* tile) {
@@ -126,11 +144,11 @@ struct TileOf {
   __device__ static __forceinline__ oct<T> operand(const uint8_t* tile, int own, int kk, int lane) {
     if constexpr (!COL) {
       const int row = own + (lane & 15);
-      return *reinterpret_cast<const oct<T>*>(tile + 16 * (row * kRowChunks + ((4 * kk + (lane >> 4)) ^ (row & 7))));
+      return *reinterpret_cast<const oct<T>*>(tile + 16 * (row * kRowChunks + ((4 * kk + (lane >> 4)) ^ swizzle(row))));
     } else {
       const int r = 32 * kk + 8 * (lane >> 4) + ((lane & 15) >> 2), col = own + 4 * (lane & 3);
       const uint8_t* p = tile + 16 * (r * kRowChunks + ((col >> 3) ^ swizzle(r))) + 2 * (col & 7);
-      // r and r + 4 have the same swizzle
+      // (r and r + 4 have the same swizzle)
       struct { s16x4 lo, hi; } v;
       v.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_tr_t)p);
       v.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_tr_t)(p + 4 * 16 * kRowChunks));
@@ -143,6 +161,17 @@ struct TileOf {
 __device__ __forceinline__ void lds_barrier() {
   wait_lgkm0();
   block_sync_lds();
+}
+
+// The same pointer in every lane, as a scalar.
+template <typename T>
+__device__ __forceinline__ const T* uniform(const T* p) {
+  const uint64_t v = (uint64_t)p;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  return (const T*)((uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ uint32_t lds_offset(const uint8_t* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)p;
 }
 
 // Waits until at most N * `steps` of this wave's loads are in flight (steps <= MAX).
@@ -171,37 +200,57 @@ struct Gemm {
   __device__ static __forceinline__ int wave_p() { return (threadIdx.x >> 6) % WP * (BP / WP); }
   __device__ static __forceinline__ int wave_q() { return (threadIdx.x >> 6) / WP * (BQ / WQ); }
 
-  __device__ static __forceinline__ void compute(const uint8_t* slot, Acc& acc) {
+  // The MFMA operands of 32 r, and their products.
+  struct Half {
+    oct<T> p[NP], q[NQ];
+  };
+  __device__ static __forceinline__ void read(const uint8_t* slot, int kk, Half& h) {
     const int lane = threadIdx.x & 63, p0 = wave_p(), q0 = wave_q();
 #pragma unroll
+    for (int j = 0; j < NQ; ++j) h.q[j] = QT::operand(slot + PT::kBytes, q0 + 16 * j, kk, lane);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) h.p[i] = PT::operand(slot, p0 + 16 * i, kk, lane);
+  }
+  __device__ static __forceinline__ void multiply(const Half& h, Acc& acc) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i)
+#pragma unroll
+      for (int j = 0; j < NQ; ++j) acc[i][j] = mfma16(h.p[i], h.q[j], acc[i][j]);
+  }
+  // Places the reads of one half step evenly among the first products of the half before.
+  __device__ static __forceinline__ void interleave() {
+    constexpr int kReads = NP * (PCOL ? 2 : 1) + NQ * (QCOL ? 2 : 1), kProducts = NP * NQ;
+    constexpr int kEach = (2 * kReads + kProducts - 1) / kProducts;
+#pragma unroll
+    for (int i = 0; i < kProducts; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x100, kEach, 0);   // LDS reads
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);       // a product
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  __device__ static __forceinline__ void compute(const uint8_t* slot, Acc& acc) {
+    Half h;
+#pragma unroll
     for (int kk = 0; kk < kStep / 32; ++kk) {
-      oct<T> pv[NP], qv[NQ];
-#pragma unroll
-      for (int j = 0; j < NQ; ++j) qv[j] = QT::operand(slot + PT::kBytes, q0 + 16 * j, kk, lane);
-#pragma unroll
-      for (int i = 0; i < NP; ++i) pv[i] = PT::operand(slot, p0 + 16 * i, kk, lane);
-#pragma unroll
-      for (int i = 0; i < NP; ++i)
-#pragma unroll
-        for (int j = 0; j < NQ; ++j) acc[i][j] = mfma16(pv[i], qv[j], acc[i][j]);
+      read(slot, kk, h);
+      multiply(h, acc);
     }
   }
 
-  // One step of the products of tile rows q whose bit is set in `some` (bit j: the j-th 16 rows of the tile).
-  __device__ static __forceinline__ void compute_some(const uint8_t* ptile, const uint8_t* qtile, uint32_t some, Acc& acc) {
+  // One step of the products of the wave's j-th 16 tile rows q, whose operand is the sum of `PIECES` tiles.
+  template <int PIECES>
+  __device__ static __forceinline__ void multiply_row(const uint8_t* ptile, const uint8_t* qtiles, int j, f32x4 (&acc)[NP]) {
     const int lane = threadIdx.x & 63, p0 = wave_p(), q0 = wave_q();
-    some >>= __builtin_amdgcn_readfirstlane(q0 / 16);
 #pragma unroll
     for (int kk = 0; kk < kStep / 32; ++kk) {
       oct<T> pv[NP];
 #pragma unroll
       for (int i = 0; i < NP; ++i) pv[i] = PT::operand(ptile, p0 + 16 * i, kk, lane);
 #pragma unroll
-      for (int j = 0; j < NQ; ++j) {
-        if (!(some >> j & 1)) continue;
-        const oct<T> qv = QT::operand(qtile, q0 + 16 * j, kk, lane);
+      for (int n = 0; n < PIECES; ++n) {
+        const oct<T> qv = QT::operand(qtiles + n * QT::kBytes, q0 + 16 * j, kk, lane);
 #pragma unroll
-        for (int i = 0; i < NP; ++i) acc[i][j] = mfma16(pv[i], qv, acc[i][j]);
+        for (int i = 0; i < NP; ++i) acc[i] = mfma16(pv[i], qv, acc[i]);
       }
     }
   }
@@ -217,10 +266,11 @@ struct Gemm {
     if constexpr (DMA) {
       const int nk = red / kStep, tail = red % kStep;
       constexpr int kPer = PT::kPer + QT::kPer;
-      const T *pat = p.base, *qat = q.base;
-      auto issue = [&](uint8_t* slot) {
-        PT::dma(pat, po, slot);
-        QT::dma(qat, qo, slot + PT::kBytes);
+      const T *pat = uniform(p.base), *qat = uniform(q.base);
+      auto issue = [&](const uint8_t* slot) {
+        const uint32_t at = lds_offset(slot);
+        PT::dma(pat, po, at);
+        QT::dma(qat, qo, at + PT::kBytes);
         pat += ps;
         qat += qs;
       };
@@ -228,8 +278,8 @@ struct Gemm {
 #pragma unroll
       for (int s = 0; s < ST - 1; ++s)
         if (s < nk) issue(lds + s * kSlot);
-      uint8_t *get = lds, *put = end - kSlot;
       if (tail) {   // the last, partial step first, in the slot that the ring needs last
+        uint8_t* const put = end - kSlot;
         oct<T> pv[PT::kPer], qv[QT::kPer];
         PT::load(p, p.base + nk * ps, po, tail, pv);
         QT::load(q, q.base + nk * qs, qo, tail, qv);
@@ -237,16 +287,46 @@ struct Gemm {
         QT::store(qv, put + PT::kBytes);
         lds_barrier();
         compute(put, acc);
+        lds_barrier();
+      }
+      if (nk == 0) return;
+      if (ST - 1 < nk) issue(end - kSlot);
+      // The operands of one half step are read while the products of the half
+      // before run; a slot is free, and filled with the step ST later, as soon as every wave has read its second half.
+      Half h0, h1;
+      wait_steps<kPer, ST - 1>(nk - 1);
+      lds_barrier();
+      read(lds, 0, h0);
+      const uint8_t* get = lds;
+      int s = 0;
+#pragma unroll 1
+      for (; s < nk - ST; ++s) {
+        read(get, 1, h1);
+        multiply(h0, acc);
+        interleave();
+        wait_vmcnt<kPer * (ST - 2)>();   // step s + 1 is in; later ones may be in flight
+        lds_barrier();                   // for every wave; and all have read step s
+        issue(get);
+        get = get + kSlot == end ? lds : get + kSlot;
+        read(get, 0, h0);
+        multiply(h1, acc);
+        interleave();
       }
 #pragma unroll 1
-      for (int s = 0; s < nk; ++s) {
-        wait_steps<kPer, ST - 2>(nk - 1 - s);   // step s is in; later ones may be in flight
-        lds_barrier();                          // for every wave; and all are done with step s - 1
-        if (s + ST - 1 < nk) issue(put);
-        compute(get, acc);
+      for (; s < nk - 1; ++s) {
+        read(get, 1, h1);
+        multiply(h0, acc);
+        interleave();
+        wait_steps<kPer, ST - 2>(nk - 2 - s);
+        lds_barrier();
         get = get + kSlot == end ? lds : get + kSlot;
-        put = put + kSlot == end ? lds : put + kSlot;
+        read(get, 0, h0);
+        multiply(h1, acc);
+        interleave();
       }
+      read(get, 1, h1);
+      multiply(h0, acc);
+      multiply(h1, acc);
     } else {
       const int nk = (red + kStep - 1) / kStep;
       oct<T> pv[PT::kPer], qv[QT::kPer];
@@ -278,29 +358,42 @@ struct Gemm {
 
   // Writes the tile's first `pn` outputs of each row at `out` (type f32 or T),
   // rows `ld` apart; row(q) is the place of tile row q (below 0: not stored).
+  // `stream`: past the caches (the non-temporal bit), where the whole output is larger than they are.
   template <typename Row>
-  __device__ static __forceinline__ void store(const Acc& acc, void* out, bool f32, int64_t ld, int pn, Row&& row) {
+  __device__ static __forceinline__ void store(const Acc& acc, void* out, bool f32, bool stream, int64_t ld, int pn,
+                                               Row&& row) {
+    if (f32) store_to(acc, (float*)out, stream, ld, pn, row);
+    else store_to(acc, (T*)out, stream, ld, pn, row);
+  }
+  template <typename U, typename Row>
+  __device__ static __forceinline__ void store_to(const Acc& acc, U* out, bool stream, int64_t ld, int pn, Row& row) {
+    if (pn < BP) store_as<false, false>(acc, out, ld, pn, row);
+    else if (stream) store_as<true, true>(acc, out, ld, pn, row);
+    else store_as<true, false>(acc, out, ld, pn, row);
+  }
+  template <bool FULL, bool STREAM, typename U, typename Row>
+  __device__ static __forceinline__ void store_as(const Acc& acc, U* out, int64_t ld, int pn, Row& row) {
     const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int j = 0; j < NQ; ++j) {
       const int64_t q = row(wave_q() + 16 * j + (lane & 15));
       if (q < 0) continue;
+      const int p = wave_p() + 4 * (lane >> 4);
+      U* at = out + q * ld + p;
 #pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        const int p = wave_p() + 16 * i + 4 * (lane >> 4);
-        if (f32) store_quad((float*)out + q * ld + p, acc[i][j], pn - p);
-        else store_quad((T*)out + q * ld + p, acc[i][j], pn - p);
-      }
+      for (int i = 0; i < NP; ++i) store_quad<STREAM>(at + 16 * i, acc[i][j], FULL ? 4 : pn - p - 16 * i);
     }
   }
 
   // The first n of four outputs, rounded to nearest even in U.
-  template <typename U>
+  template <bool STREAM, typename U>
   __device__ static __forceinline__ void store_quad(U* at, f32x4 f, int n) {
     typedef U quad __attribute__((ext_vector_type(4)));
+    typedef quad quad_at __attribute__((aligned(sizeof(U))));   // any element alignment
     const quad v = __builtin_convertvector(f, quad);
     if (n >= 4) {
-      __builtin_memcpy(at, &v, sizeof(v));
+      if (STREAM) __builtin_nontemporal_store(v, (quad_at*)at);
+      else *(quad_at*)at = v;
     } else {
 #pragma unroll
       for (int i = 0; i < 3; ++i)

@@ -22,7 +22,8 @@ struct GroupedArgs {
   int32_t* status;
   int groups, rows;
   int n, k;
-  int f32;   // outputs in f32
+  int f32;      // outputs in f32
+  int stream;   // outputs past the caches
   int64_t x_stride, y_stride, w_stride, w_group;
 };
 
@@ -95,7 +96,7 @@ __device__ __forceinline__ void report(const GroupedArgs& a) {
 
 // Forward (WCOL false): in = x, out = y. Input gradient (WCOL true): in = dy, out = dx.
 template <typename T, bool WCOL, typename G>
-__global__ __launch_bounds__(G::NT) void k_grouped(GroupedArgs a, const T* __restrict__ in, const T* __restrict__ w,
+__global__ __launch_bounds__(G::NT, 2) void k_grouped(GroupedArgs a, const T* __restrict__ in, const T* __restrict__ w,
                                                    void* __restrict__ out) {
   extern __shared__ __align__(16) uint8_t lds[];
   report(a);
@@ -110,16 +111,17 @@ __global__ __launch_bounds__(G::NT) void k_grouped(GroupedArgs a, const T* __res
   const bool none = t.group < 0 || t.group >= a.groups;
   const int p0 = t.p * G::kP;
   const int64_t in_stride = WCOL ? a.y_stride : a.x_stride, out_stride = WCOL ? a.x_stride : a.y_stride;
-  const Operand<T> P = {w + (none ? 0 : t.group) * a.w_group + (WCOL ? p0 : p0 * a.w_stride), a.w_stride, WCOL ? width - p0 : min(G::kP, width - p0), nullptr};
-  const Operand<T> Q = {in + t.row * in_stride, in_stride, t.rows, nullptr};
+  const Operand<T> P = {w + (none ? 0 : t.group) * a.w_group + (WCOL ? p0 : p0 * a.w_stride), a.w_stride, WCOL ? width - p0 : min(G::kP, width - p0), nullptr,
+                        a.k >= 8};
+  const Operand<T> Q = {in + t.row * in_stride, in_stride, t.rows, nullptr, red >= 8};
   typename G::Acc acc = {};
   G::run(P, Q, none ? 0 : red, lds, acc);
   uint8_t* o = (uint8_t*)out + (t.row * out_stride + p0) * (a.f32 ? 4 : 2);
-  G::store(acc, o, a.f32, out_stride, width - p0, [&](int q) { return q < t.rows ? q : -1; });
+  G::store(acc, o, a.f32, a.stream, out_stride, width - p0, [&](int q) { return q < t.rows ? q : -1; });
 }
 
 template <typename T, typename G>
-__global__ __launch_bounds__(G::NT) void k_grouped_dw(GroupedArgs a, const T* __restrict__ dy, const T* __restrict__ x,
+__global__ __launch_bounds__(G::NT, 2) void k_grouped_dw(GroupedArgs a, const T* __restrict__ dy, const T* __restrict__ x,
                                                       void* __restrict__ dw) {
   extern __shared__ __align__(16) uint8_t lds[];
   report(a);
@@ -127,14 +129,16 @@ __global__ __launch_bounds__(G::NT) void k_grouped_dw(GroupedArgs a, const T* __
   const int64_t total = (int64_t)np * nq * a.groups, place = xcd_order(blockIdx.x, total);
   if (place >= total) return;
   const int g = (int)(place / (np * nq)), in = (int)(place % (np * nq));
-  const int p0 = in / nq * G::kP, q0 = in % nq * G::kQ;
+  int qt, pt;
+  tile_at(in, nq, np, qt, pt);
+  const int p0 = pt * G::kP, q0 = qt * G::kQ;
   const int lo = edge(a, g + 1), hi = max(lo, edge(a, g + 2));
-  const Operand<T> P = {x + lo * a.x_stride + p0, a.x_stride, a.k - p0, nullptr};
-  const Operand<T> Q = {dy + lo * a.y_stride + q0, a.y_stride, a.n - q0, nullptr};
+  const Operand<T> P = {x + lo * a.x_stride + p0, a.x_stride, a.k - p0, nullptr, a.k >= 8};
+  const Operand<T> Q = {dy + lo * a.y_stride + q0, a.y_stride, a.n - q0, nullptr, a.n >= 8};
   typename G::Acc acc = {};
   G::run(P, Q, hi - lo, lds, acc);
   uint8_t* o = (uint8_t*)dw + (g * a.w_group + q0 * a.w_stride + p0) * (a.f32 ? 4 : 2);
-  G::store(acc, o, a.f32, a.w_stride, a.k - p0, [&](int q) { return q0 + q < a.n ? q : -1; });
+  G::store(acc, o, a.f32, a.stream, a.w_stride, a.k - p0, [&](int q) { return q0 + q < a.n ? q : -1; });
 }
 
 enum Way { kForward, kInput, kWeight };
@@ -161,8 +165,17 @@ int check_grouped(const moe_grouped* g, int64_t rows) {
   return MOE_OK;
 }
 
-GroupedArgs grouped_args(const moe_grouped& g, const int32_t* offsets, int64_t rows, int32_t* status) {
-  return {offsets, status, g.n_groups, (int)rows, g.n, g.k, g.out_type == MOE_TYPE_F32,
+// f32 outputs of 64 MiB and more, twice what the L2s hold, are written past
+// the caches: they would push the operands out that neighbouring tiles share.
+// The weight gradient of 16384 rows over 32 groups of 4096 x 2048 (1.07 GB):
+// 466 us against 575. (16-bit outputs are the same either way.)
+bool past_caches(const moe_grouped& g, Way way, int64_t rows) {
+  const double count = way == kWeight ? (double)g.n_groups * g.n * g.k : (double)rows * (way == kForward ? g.n : g.k);
+  return g.out_type == MOE_TYPE_F32 && 4 * count >= (double)(64 << 20);
+}
+
+GroupedArgs grouped_args(const moe_grouped& g, Way way, const int32_t* offsets, int64_t rows, int32_t* status) {
+  return {offsets, status, g.n_groups, (int)rows, g.n, g.k, g.out_type == MOE_TYPE_F32, past_caches(g, way, rows),
           g.x_stride, g.y_stride, g.w_stride, g.w_group_stride};
 }
 
@@ -173,20 +186,39 @@ int launch(int64_t tiles, hipStream_t s, A... args) {
   return launch_tiles<Kernel>("grouped", dim3((unsigned)blocks), G::NT, G::kLds, s, args...);
 }
 
+// At most so many row tiles of q rows: a group adds at most one partial tile.
+int64_t row_tiles(const GroupedArgs& a, int q) {
+  const int64_t some = a.groups + 2 < a.rows ? a.groups + 2 : a.rows;   // entries that can have rows
+  return (a.rows + (q - 1) * some) / q;
+}
+
 template <typename T, bool WCOL, typename G>
 int launch_rows(const GroupedArgs& a, const void* in, const void* w, void* out, hipStream_t s) {
   const int width = WCOL ? a.k : a.n;
-  const int64_t some = a.groups + 2 < a.rows ? a.groups + 2 : a.rows;   // entries that can have rows
-  const int64_t row_tiles = (a.rows + (G::kQ - 1) * some) / G::kQ;
-  return launch<k_grouped<T, WCOL, G>, G>(row_tiles * ((width + G::kP - 1) / G::kP), s, a, (const T*)in,
-                                       (const T*)w, out);
+  return launch<k_grouped<T, WCOL, G>, G>(row_tiles(a, G::kQ) * ((width + G::kP - 1) / G::kP), s, a, (const T*)in,
+                                          (const T*)w, out);
 }
 
 template <typename T, bool WCOL, bool DMA>
 int launch_rows_as(const GroupedArgs& a, const void* in, const void* w, void* out, hipStream_t s) {
   const int64_t mean = a.rows / a.groups;
+  const int width = WCOL ? a.k : a.n;
   if (mean < 16) return launch_rows<T, WCOL, Gemm<T, WCOL, false, 128, 16, 4, 1, 4, DMA>>(a, in, w, out, s);
-  if (mean < 64) return launch_rows<T, WCOL, Gemm<T, WCOL, false, 128, 64, 2, 2, 3, DMA>>(a, in, w, out, s);
+  // Few tiles: smaller ones, so that more CUs share the work. 100 rows of one group of 2048 x 2048: 10.5 us in
+  // tiles of 16 rows, 15 of 64, 20 of 128; 1200 rows over 4 groups of 1024 x 2048: 15.5 us of 64, 23.5 of 128.
+  if (row_tiles(a, 64) * ((width + 127) / 128) < 96)
+    return launch_rows<T, WCOL, Gemm<T, WCOL, false, 128, 16, 4, 1, 4, DMA>>(a, in, w, out, s);
+  if (mean < 64 || row_tiles(a, 128) * ((width + 127) / 128) < 300)
+    return launch_rows<T, WCOL, Gemm<T, WCOL, false, 128, 64, 2, 2, 3, DMA>>(a, in, w, out, s);
+  if constexpr (DMA) {
+    // One workgroup a CU with a third step in flight, where there are three
+    // tiles a CU and sums long enough for its fill and drain; otherwise two
+    // workgroups a CU. Input gradient of 16384 rows over 32 groups of 4096 x
+    // 2048: 320 us against 330; forward of 8000 over 16 of 4096 x 512: 72 against 61.
+    const int red = WCOL ? a.n : a.k;
+    if (row_tiles(a, 128) * ((width + 255) / 256) >= 768 && red >= 1024)
+      return launch_rows<T, WCOL, Gemm<T, WCOL, false, 256, 128, 4, 2, 3, DMA>>(a, in, w, out, s);
+  }
   return launch_rows<T, WCOL, Gemm<T, WCOL, false, 128, 128, 2, 2, 2, DMA>>(a, in, w, out, s);
 }
 
@@ -221,7 +253,7 @@ int grouped(Way way, const moe_grouped* g, const void* in, const void* w, const 
   const size_t es = elem_bytes(g->out_type);
   if ((uintptr_t)in % 2 || (uintptr_t)w % 2 || (uintptr_t)out % es || (uintptr_t)offsets % 4 || (uintptr_t)status % 4)
     return fail(MOE_EINVAL, "grouped: a pointer is not aligned to its elements%s%lld");
-  const GroupedArgs a = grouped_args(*g, offsets, rows, status);
+  const GroupedArgs a = grouped_args(*g, way, offsets, rows, status);
   const hipStream_t s = (hipStream_t)stream;
   return g->type == MOE_TYPE_BF16 ? launch_way<bf16_t>(way, a, in, w, out, s)
                                   : launch_way<fp16_t>(way, a, in, w, out, s);

@@ -81,15 +81,20 @@ __global__ __launch_bounds__(TPR < kJoinThreads ? kJoinThreads : TPR) void k_joi
   const int t = threadIdx.x % TPR;
   const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
   if (row >= a.m) return;   // whole waves; with TPR > 64 the whole workgroup
+  // Everything is asked for at once, the vectors too (from the caches): a call of few rows waits for memory once.
   f32x8 xv[NC];
   const float inv_dim = 1.0f / (float)a.dim;
+  const bool room = a.dim >= 8;
   oct<RT> xr[NC];
-  oct<T> br[NC];
+  oct<T> br[NC] = {}, po[NC] = {}, ga[NC] = {}, pr[NC] = {};
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
-    const int c = 8 * (t + TPR * i);
-    if (b) br[i] = load_oct(b + row * a.b_stride + c, a.dim - c);
-    xr[i] = load_oct(x + row * a.x_stride + c, a.dim - c);
+    const int c = 8 * (t + TPR * i), left = a.dim - c;
+    xr[i] = load_oct(x + row * a.x_stride + c, left, room);
+    if (b) br[i] = load_oct(b + row * a.b_stride + c, left, room);
+    if (w_post) po[i] = load_oct(w_post + c, left, room);
+    if (gate) ga[i] = load_oct(gate + (a.gate_rows ? row * a.gate_stride : 0) + c, left, room);
+    if (w_pre) pr[i] = load_oct(w_pre + c, left, room);
   }
   if (b) {
     float rb = 1.0f;
@@ -102,10 +107,9 @@ __global__ __launch_bounds__(TPR < kJoinThreads ? kJoinThreads : TPR) void k_joi
     }
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      const int c = 8 * (t + TPR * i);
       f32x8 z = to_f32(br[i]);
-      if (w_post) z = z * rb * to_f32(load_oct(w_post + c, a.dim - c));
-      if (gate) z = z * to_f32(load_oct(gate + (a.gate_rows ? row * a.gate_stride : 0) + c, a.dim - c));
+      if (w_post) z = z * rb * to_f32(po[i]);
+      if (gate) z = z * to_f32(ga[i]);
       xv[i] = to_f32(xr[i]) + a.scale * z;
     }
   } else {
@@ -128,13 +132,26 @@ __global__ __launch_bounds__(TPR < kJoinThreads ? kJoinThreads : TPR) void k_joi
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     const int c = 8 * (t + TPR * i);
-    store_oct(y + row * a.y_stride + c, xv[i] * rx * to_f32(load_oct(w_pre + c, a.dim - c)), a.dim - c);
+    store_oct(y + row * a.y_stride + c, xv[i] * rx * to_f32(pr[i]), a.dim - c);
   }
 }
 
 // The gradients: workgroup p takes the rows p, p + P, ... (P workgroups), so
 // that its threads keep the sums over rows of their columns in registers; they
 // are written as f32 partial sums [P][3][dim] that k_join_sums adds up.
+// Registers permitting, the vectors and the row stay in them (workgroups of up
+// to 512 threads; otherwise they are read again where they are used, from the
+// caches), and the next row is on its way while one is worked on (NC = 1).
+//
+// One reduction a row: with d = dy w_pre and h = gate w_post b, the sum that
+// db needs, of dz w_post nb, is s rb (sum h dx_out + rx (sum h d - c1 sum h x')),
+// so its three parts are summed together with those of x'^2, d x' and b^2.
+template <typename T, typename RT>
+struct JoinChunk {
+  oct<RT> dxo, xo;
+  oct<T> dy, b, gate;
+};
+
 template <typename T, typename RT, int TPR, int NC>
 __global__ __launch_bounds__(TPR) void k_join_back(JoinArgs a, const T* __restrict__ dy, const RT* dxo,
                                                    const RT* __restrict__ xo, const T* b,
@@ -142,77 +159,107 @@ __global__ __launch_bounds__(TPR) void k_join_back(JoinArgs a, const T* __restri
                                                    const T* __restrict__ w_pre, RT* dx, T* db,
                                                    T* __restrict__ dgate_rows,
                                                    float* __restrict__ part, int sums) {
-  __shared__ float buf[2][3 * (TPR / 64)];
+  constexpr bool kKeep = TPR <= 512, kAhead = kKeep && NC == 1;
+  typedef JoinChunk<T, RT> Chunk;
+  struct Vectors {
+    oct<T> pre, post, gate;
+  };
+  __shared__ float buf[2][6 * (TPR / 64)];
   const int t = threadIdx.x;
   const float inv_dim = 1.0f / (float)a.dim;
+  const bool room = a.dim >= 8;
+  const bool through = db && w_post;   // db goes through the norm
+  auto vectors_at = [&](int c) {
+    Vectors v = {};
+    if (dy) v.pre = load_oct(w_pre + c, a.dim - c, room);
+    if (w_post) v.post = load_oct(w_post + c, a.dim - c, room);
+    if (gate && !a.gate_rows) v.gate = load_oct(gate + c, a.dim - c, room);
+    return v;
+  };
+  auto chunk_at = [&](int64_t row, int c) {
+    Chunk r = {};
+    const int left = a.dim - c;
+    if (dxo) r.dxo = load_oct(dxo + row * a.x_out_stride + c, left, room);
+    if (dy) {
+      r.xo = load_oct(xo + row * a.x_out_stride + c, left, room);
+      r.dy = load_oct(dy + row * a.y_stride + c, left, room);
+    }
+    if (b) r.b = load_oct(b + row * a.b_stride + c, left, room);
+    if (gate && a.gate_rows) r.gate = load_oct(gate + row * a.gate_stride + c, left, room);
+    return r;
+  };
   f32x8 s_pre[NC] = {}, s_post[NC] = {}, s_gate[NC] = {};
-  for (int64_t row = blockIdx.x; row < a.m; row += gridDim.x) {
-    f32x8 xv[NC], dn[NC], g[NC];
-    float s[3] = {0.0f, 0.0f, 0.0f};
+  Vectors vec[NC];
+  Chunk cur[NC], next[NC];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    if (kKeep) vec[i] = vectors_at(8 * (t + TPR * i));
+    if (kAhead) next[i] = chunk_at(blockIdx.x, 8 * (t + TPR * i));
+  }
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < a.m; row += gridDim.x, turn ^= 1) {
+    if (kAhead) {
+      // (dx may be dx_out and db may be b: only this workgroup writes its rows, each after it was read)
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        cur[i] = next[i];
+        if (row + gridDim.x < a.m) next[i] = chunk_at(row + gridDim.x, 8 * (t + TPR * i));
+      }
+    }
+    float s[6] = {};
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      const int c = 8 * (t + TPR * i), left = a.dim - c;
-      if (dxo) g[i] = to_f32(load_oct(dxo + row * a.x_out_stride + c, left));
-      else g[i] = f32x8{};
-      if (dy) {
-        xv[i] = to_f32(load_oct(xo + row * a.x_out_stride + c, left));
-        dn[i] = to_f32(load_oct(dy + row * a.y_stride + c, left));
-        const f32x8 d = dn[i] * to_f32(load_oct(w_pre + c, left));
-        s[0] += sum_of_squares(xv[i]);
-        s[1] += dot8(d, xv[i]);
+      const int c = 8 * (t + TPR * i);
+      if (kKeep && !kAhead) cur[i] = chunk_at(row, c);
+      const Chunk r = kKeep ? cur[i] : chunk_at(row, c);
+      const Vectors v = kKeep ? vec[i] : vectors_at(c);
+      const f32x8 bv = to_f32(r.b), xv = to_f32(r.xo), d = to_f32(r.dy) * to_f32(v.pre);
+      s[0] += sum_of_squares(xv);
+      s[1] += dot8(d, xv);
+      if (w_post) s[2] += sum_of_squares(bv);
+      if (through) {
+        f32x8 h = bv * to_f32(v.post);
+        if (gate) h = h * to_f32(a.gate_rows ? r.gate : v.gate);
+        s[3] += dot8(h, to_f32(r.dxo));
+        s[4] += dot8(h, d);
+        s[5] += dot8(h, xv);
       }
-      if (b && w_post) s[2] += sum_of_squares(to_f32(load_oct(b + row * a.b_stride + c, left)));
     }
-    row_sums<TPR>(s, buf[0]);
+    row_sums<TPR>(s, buf[turn]);   // (the next row takes the other buffer: one barrier a row is enough)
     const float rx = 1.0f / sqrtf(s[0] * inv_dim + a.eps);
     const float c1 = s[1] * rx * rx * inv_dim;   // mean(dn n) rx: n mean(dn n) = x' c1
-    const float rb = b && w_post ? 1.0f / sqrtf(s[2] * inv_dim + a.eps) : 1.0f;
-    float q[1] = {0.0f};
+    const float rb = w_post ? 1.0f / sqrtf(s[2] * inv_dim + a.eps) : 1.0f;
+    // rb mean(dz w_post nb)
+    const float c2 = through ? rb * rb * a.scale * inv_dim * (dy ? s[3] + rx * (s[4] - c1 * s[5]) : s[3]) : 0.0f;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = 8 * (t + TPR * i), left = a.dim - c;
+      const Chunk r = kKeep ? cur[i] : chunk_at(row, c);
+      const Vectors v = kKeep ? vec[i] : vectors_at(c);
+      f32x8 g = to_f32(r.dxo);
       if (dy) {
-        s_pre[i] += dn[i] * (xv[i] * rx);
-        g[i] += rx * (dn[i] * to_f32(load_oct(w_pre + c, left)) - xv[i] * c1);
+        const f32x8 xv = to_f32(r.xo), dn = to_f32(r.dy);
+        s_pre[i] += dn * (xv * rx);
+        g += rx * (dn * to_f32(v.pre) - xv * c1);
       }
-      store_oct(dx + row * a.x_stride + c, g[i], left);
+      store_oct(dx + row * a.x_stride + c, g, left);
       if (!b) continue;
-      const f32x8 nb = to_f32(load_oct(b + row * a.b_stride + c, left)) * rb;
-      f32x8 dz = g[i] * a.scale;
+      const f32x8 bv = to_f32(r.b), nb = bv * rb;
+      f32x8 dz = g * a.scale;
       f32x8 z = nb;
-      f32x8 wp;
-      if (w_post) {
-        wp = to_f32(load_oct(w_post + c, left));
-        z = z * wp;
-      }
+      if (w_post) z = z * to_f32(v.post);
       if (gate) {
         const f32x8 dg = dz * z;
-        if (a.gate_rows) {
-          if (dgate_rows) store_oct(dgate_rows + row * a.gate_stride + c, dg, left);
-        } else {
-          s_gate[i] += dg;
-        }
-        dz = dz * to_f32(load_oct(gate + (a.gate_rows ? row * a.gate_stride : 0) + c, left));
+        if (!a.gate_rows) s_gate[i] += dg;
+        else if (dgate_rows) store_oct(dgate_rows + row * a.gate_stride + c, dg, left);
+        dz = dz * to_f32(a.gate_rows ? r.gate : v.gate);
       }
       if (w_post) {
         s_post[i] += dz * nb;
-        dz = dz * wp;
-        q[0] += dot8(dz, nb);
+        dz = rb * (dz * to_f32(v.post) - bv * c2);
       }
-      g[i] = dz;
+      if (db) store_oct(db + row * a.b_stride + c, dz, left);
     }
-    if (db) {
-      if (w_post) row_sums<TPR>(q, buf[1]);
-      const float c2 = q[0] * inv_dim;
-#pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        const int c = 8 * (t + TPR * i), left = a.dim - c;
-        f32x8 d = g[i];
-        if (w_post) d = rb * (d - to_f32(load_oct(b + row * a.b_stride + c, left)) * (rb * c2));
-        store_oct(db + row * a.b_stride + c, d, left);
-      }
-    }
-    if (!(db && w_post) && TPR > 64) __syncthreads();   // buf[0] is written again by the next row
   }
   if (!sums) return;
   float* out = part + (int64_t)blockIdx.x * 3 * a.dim;
@@ -227,26 +274,39 @@ __global__ __launch_bounds__(TPR) void k_join_back(JoinArgs a, const T* __restri
 }
 
 // Column sums of the partial sums [parts][3 * dim], in a fixed order: 64
-// columns a workgroup, wave w adding the rows w, w + 4, ...
-__global__ __launch_bounds__(256) void k_join_sums(const float* __restrict__ part, int parts, int dim,
-                                                   float* __restrict__ dw_pre, float* __restrict__ dw_post,
-                                                   float* __restrict__ dgate) {
-  __shared__ float buf[4][64];
+// columns a workgroup, wave w adding the rows w, w + 16, ...
+__global__ __launch_bounds__(1024) void k_join_sums(const float* __restrict__ part, int parts, int dim,
+                                                    float* __restrict__ dw_pre, float* __restrict__ dw_post,
+                                                    float* __restrict__ dgate) {
+  __shared__ float buf[16][64];
   const int which = blockIdx.y;
   float* out = which == 0 ? dw_pre : which == 1 ? dw_post : dgate;
   if (!out) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int col = blockIdx.x * 64 + lane;
+  const float* from = part + (int64_t)which * dim + min(col, dim - 1);
   float s = 0.0f;
-  if (col < dim)
-    for (int p = wave; p < parts; p += 4) s += part[((int64_t)p * 3 + which) * dim + col];
+#pragma unroll 8
+  for (int p = wave; p < parts; p += 16) s += from[(int64_t)p * 3 * dim];
   buf[wave][lane] = s;
   __syncthreads();
-  if (wave == 0 && col < dim) out[col] = (buf[0][lane] + buf[1][lane]) + (buf[2][lane] + buf[3][lane]);
+  if (wave == 0 && col < dim) {
+#pragma unroll
+    for (int w = 1; w < 16; ++w) s += buf[w][lane];
+    out[col] = s;
+  }
 }
 
-// Workgroups of the gradient kernel for m rows.
-int join_parts(int64_t m) { return (int)(m < 512 ? (m < 1 ? 1 : m) : 512); }
+// Workgroups of the gradient kernel for m rows: as many as run at once (its
+// registers leave 8 waves a CU), but at least 4 rows each where that still gives one a CU: a workgroup's
+// partial sums cost as much traffic as a row. 8192 rows of 512: 31 us with
+// 512 workgroups, 51 with 256; 4096 rows of 4096: 61 with 512, 58 with 256.
+int join_parts(int dim, int64_t m) {
+  const int64_t at_once = dim <= 1024 ? 1024 : dim <= 2048 ? 512 : 256;
+  const int64_t fed = m / 4 > 256 ? m / 4 : 256;
+  const int64_t parts = at_once < fed ? at_once : fed;
+  return (int)(m < parts ? (m < 1 ? 1 : m) : parts);
+}
 
 int check_join(const moe_join* j, int64_t m) {
   if (!j) return fail(MOE_EINVAL, "join is NULL%s%lld");
@@ -298,7 +358,7 @@ template <typename T, typename RT, int TPR, int NC>
 void launch_back_as(const JoinArgs& a, const void* dy, const void* dxo, const void* xo, const void* b,
                     const void* w_post, const void* gate, const void* w_pre, void* dx, void* db, void* dgate_rows,
                     float* part, int sums, hipStream_t s) {
-  k_join_back<T, RT, TPR, NC><<<dim3(join_parts(a.m)), dim3(TPR), 0, s>>>(
+  k_join_back<T, RT, TPR, NC><<<dim3(join_parts(a.dim, a.m)), dim3(TPR), 0, s>>>(
       a, (const T*)dy, (const RT*)dxo, (const RT*)xo, (const T*)b, (const T*)w_post, (const T*)gate, (const T*)w_pre,
       (RT*)dx, (T*)db, (T*)dgate_rows, part, sums);
 }
@@ -306,9 +366,10 @@ void launch_back_as(const JoinArgs& a, const void* dy, const void* dxo, const vo
 template <typename T, typename RT, typename... A>
 void launch_back(const JoinArgs& a, A... args) {
   if (a.dim <= 512) launch_back_as<T, RT, 64, 1>(a, args...);
+  else if (a.dim <= 1024) launch_back_as<T, RT, 128, 1>(a, args...);
   else if (a.dim <= 2048) launch_back_as<T, RT, 256, 1>(a, args...);
   else if (a.dim <= 4096) launch_back_as<T, RT, 512, 1>(a, args...);
-  else if (a.dim <= 8192) launch_back_as<T, RT, 1024, 1>(a, args...);
+  else if (a.dim <= 8192) launch_back_as<T, RT, 512, 2>(a, args...);
   else launch_back_as<T, RT, 1024, 2>(a, args...);
 }
 
@@ -346,7 +407,7 @@ int moe_join_forward(const moe_join* j, const void* x, const void* b, const void
 
 size_t moe_join_workspace_bytes(const moe_join* j, int64_t max_m) {
   if (check_join(j, max_m)) return 0;
-  return ((size_t)join_parts(max_m) * 3 * j->dim * sizeof(float) + 255) & ~(size_t)255;
+  return ((size_t)join_parts(j->dim, max_m) * 3 * j->dim * sizeof(float) + 255) & ~(size_t)255;
 }
 
 int moe_join_backward(const moe_join* j, const void* dy, const void* dx_out, const void* x_out, const void* b,
@@ -388,7 +449,7 @@ int moe_join_backward(const moe_join* j, const void* dy, const void* dx_out, con
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return hip_fail(e, "join_back");
   if (sums) {
-    k_join_sums<<<dim3((j->dim + 63) / 64, 3), dim3(256), 0, s>>>(part, join_parts(m), j->dim, dw_pre, dw_post,
+    k_join_sums<<<dim3((j->dim + 63) / 64, 3), dim3(1024), 0, s>>>(part, join_parts(j->dim, m), j->dim, dw_pre, dw_post,
                                                                   dgate_sum);
     e = hipGetLastError();
     if (e != hipSuccess) return hip_fail(e, "join_sums");
