@@ -96,7 +96,7 @@ __global__ __launch_bounds__(G::NT, 2) void k_adapter_part(AdapterArgs a, Slices
   typename G::Acc acc = {};
   G::run(P, Q, red, lds, acc);
   float* out = (base ? part : upart) + ((int64_t)slice * a.m + t0) * width + p0;
-  G::store(acc, out, true, false, width, width - p0,
+  G::store(acc, out, true, width, width - p0,
            [&](int q) { return q < tokens && (base || (users >> q & 1)) ? q : -1; });
 }
 
@@ -378,7 +378,7 @@ __global__ __launch_bounds__(G::NT, 2) void k_adapter_main(AdapterArgs a, Sorted
       oct<T> v[G::PT::kPer];
       G::PT::template offsets<false>(B, off);
       G::PT::load(B, B.base, off, a.rank - r0, v);
-      G::PT::store(v, lds);
+      G::PT::store(B, a.rank - r0, v, lds);
       lds_barrier();
 #pragma unroll
       for (int j = 0; j < G::NQ; ++j) {
@@ -395,7 +395,7 @@ __global__ __launch_bounds__(G::NT, 2) void k_adapter_main(AdapterArgs a, Sorted
     }
   }
   uint8_t* o = (uint8_t*)out + (int64_t)p0 * (a.f32 ? 4 : 2);
-  G::store(acc, o, a.f32, false, a.out_stride, a.n - p0, [&](int q) { return so.token[row0 + q]; });
+  G::store(acc, o, a.f32, a.out_stride, a.n - p0, [&](int q) { return so.token[row0 + q]; });
 }
 
 int check_adapters(const moe_adapters* p, int64_t m) {

@@ -43,45 +43,53 @@ using oct = typename oct_of<T>::type;
 template <typename V>
 __device__ __forceinline__ f32x8 to_f32(V v) { return __builtin_convertvector(v, f32x8); }
 
-// Elements p[0..7] of which the first n are there (n >= 8: all); the others
-// are zero. `room` (the same in every lane): p lies in a row of at least 8
-// elements that ends at p + n if n < 8. Then the row's last 8 elements are loaded at once
-// and moved down; a shorter row is loaded one by one.
+// Elements p[0..7] of which the first n are there (n >= 8: all) are loaded in
+// two steps: raw_oct asks for them, and placed_oct, where they are used, moves
+// them to their places and fills up with zeros. A load with a branch on its own
+// data would make the wave wait for each load in turn.
+// `room` (the same in every lane): p lies in a row of at least 8 elements that
+// ends at p + n if n < 8; the row's last 8 elements are loaded then. A shorter row is loaded one by one.
 template <typename T>
-__device__ __forceinline__ oct<T> load_oct(const T* p, int n, bool room) {
+__device__ __forceinline__ oct<T> raw_oct(const T* p, int n, bool room) {
   oct<T> o = {};
-  if (n >= 8) {
-    __builtin_memcpy(&o, p, 8 * sizeof(T));
+  if (room) {
+    if (n > 0) __builtin_memcpy(&o, p + min(n - 8, 0), 8 * sizeof(T));
   } else if (n > 0) {
-    if (room) {
-      constexpr int W = 2 * sizeof(T);   // words
-      uint32_t w[W];
-      const int by = 8 - n;
-      __builtin_memcpy(w, p - by, sizeof(w));
-      if constexpr (sizeof(T) == 2) {
-#pragma unroll
-        for (int i = 0; i < W; ++i) w[i] = by & 4 ? (i + 2 < W ? w[i + 2] : 0) : w[i];
-#pragma unroll
-        for (int i = 0; i < W; ++i) w[i] = by & 2 ? (i + 1 < W ? w[i + 1] : 0) : w[i];
-#pragma unroll
-        for (int i = 0; i < W; ++i) w[i] = by & 1 ? (i + 1 < W ? w[i + 1] << 16 : 0) | w[i] >> 16 : w[i];
-      } else {
-#pragma unroll
-        for (int s = 4; s > 0; s /= 2)
-#pragma unroll
-          for (int i = 0; i < W; ++i) w[i] = by & s ? (i + s < W ? w[i + s] : 0) : w[i];
-      }
-      __builtin_memcpy(&o, w, sizeof(w));
-    } else {
 #pragma unroll 1
-      for (int i = 0; i < n; ++i) {
-        const T v = p[i];
+    for (int i = 0; i < min(n, 8); ++i) {
+      const T v = p[i];
 #pragma unroll
-        for (int e = 0; e < 7; ++e) o[e] = e == i ? v : o[e];
-      }
+      for (int e = 0; e < 8; ++e) o[e] = e == i ? v : o[e];
     }
   }
   return o;
+}
+template <typename T>
+__device__ __forceinline__ oct<T> placed_oct(oct<T> o, int n, bool room) {
+  if (!room) return o;
+  constexpr int W = 2 * sizeof(T);   // words
+  uint32_t w[W];
+  const int by = n > 0 ? max(8 - n, 0) : 0;
+  __builtin_memcpy(w, &o, sizeof(w));
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = by & 4 ? (i + 2 < W ? w[i + 2] : 0) : w[i];
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = by & 2 ? (i + 1 < W ? w[i + 1] : 0) : w[i];
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = by & 1 ? (i + 1 < W ? w[i + 1] << 16 : 0) | w[i] >> 16 : w[i];
+  } else {
+#pragma unroll
+    for (int s = 4; s > 0; s /= 2)
+#pragma unroll
+      for (int i = 0; i < W; ++i) w[i] = by & s ? (i + s < W ? w[i + s] : 0) : w[i];
+  }
+  __builtin_memcpy(&o, w, sizeof(w));
+  return o;
+}
+template <typename T>
+__device__ __forceinline__ oct<T> load_oct(const T* p, int n, bool room) {
+  return placed_oct<T>(raw_oct(p, n, room), n, room);
 }
 
 // The first n of f rounded to nearest even in T (infinities and NaN kept).

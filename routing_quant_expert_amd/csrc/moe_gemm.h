@@ -21,6 +21,7 @@
 #include "moe_element.h"
 #include "moe_internal.h"
 #include "moe_kquant.h"
+#include "moe_wave.h"
 
 namespace moe {
 
@@ -119,25 +120,53 @@ struct TileOf {
 
 #pragma clang diagnostic pop
 
-  // The same through registers, at any alignment: r past `left` and columns
-  // past the operand's are zero.
-  __device__ static __forceinline__ void load(const Operand<T>& o, const T* at, const Off (&off)[kPer], int left,
-                                              oct<T> (&v)[kPer]) {
-    if (left >= kStep && (!COL || o.count >= R)) {
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) __builtin_memcpy(&v[k], at + off[k], 16);
-      return;
-    }
+  // COL: a last step of `left` r: the rows past it repeat the last one, until clear() zeroes them in LDS.
+  __device__ static __forceinline__ void dma_part(const Operand<T>& o, const T* at, int left, uint32_t tile) {
+    static_assert(COL, "a partial step of a column tile is whole rows");
+    Off off[kPer];
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       int r, own;
       place(position(k), r, own);
-      v[k] = load_oct(at + off[k], COL ? (r < left ? o.count - own : 0) : left - r, o.room);
+      off[k] = (Off)min(r, left - 1) * (Off)o.ld + min(own, o.count - 8);
+    }
+    dma(at, off, tile);
+  }
+  __device__ static __forceinline__ void clear(int left, uint8_t* tile) {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+      if (position(k) / kRowChunks >= left) *reinterpret_cast<oct<T>*>(tile + 16 * position(k)) = oct<T>{};
+  }
+
+  // The same through registers, at any alignment: r past `left` and columns
+  // past the operand's are zero.
+  __device__ static __forceinline__ bool whole(const Operand<T>& o, int left) {
+    return left >= kStep && (!COL || o.count >= R);
+  }
+  __device__ static __forceinline__ int there(const Operand<T>& o, int k, int left) {   // of the thread's k-th chunk
+    int r, own;
+    place(position(k), r, own);
+    return COL ? (r < left ? o.count - own : 0) : left - r;
+  }
+  __device__ static __forceinline__ void load(const Operand<T>& o, const T* at, const Off (&off)[kPer], int left,
+                                              oct<T> (&v)[kPer]) {
+    if (whole(o, left)) {
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) __builtin_memcpy(&v[k], at + off[k], 16);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) v[k] = raw_oct(at + off[k], there(o, k, left), o.room);
     }
   }
-  __device__ static __forceinline__ void store(const oct<T> (&v)[kPer], uint8_t* tile) {
+  __device__ static __forceinline__ void store(const Operand<T>& o, int left, const oct<T> (&v)[kPer], uint8_t* tile) {
+    if (whole(o, left)) {
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) *reinterpret_cast<oct<T>*>(tile + 16 * position(k)) = v[k];
+      for (int k = 0; k < kPer; ++k) *reinterpret_cast<oct<T>*>(tile + 16 * position(k)) = v[k];
+    } else {
+#pragma unroll
+      for (int k = 0; k < kPer; ++k)
+        *reinterpret_cast<oct<T>*>(tile + 16 * position(k)) = placed_oct<T>(v[k], there(o, k, left), o.room);
+    }
   }
 
   // The MFMA operand of the 16 rows (columns) from `own`, r = 32 kk + 8 * (lane / 16) + 0..7.
@@ -174,13 +203,13 @@ __device__ __forceinline__ uint32_t lds_offset(const uint8_t* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)p;
 }
 
-// Waits until at most N * `steps` of this wave's loads are in flight (steps <= MAX).
-template <int N, int MAX>
+// Waits until at most N * `steps` (steps <= MAX) + MORE of this wave's loads and stores are in flight.
+template <int N, int MAX, int MORE = 0>
 __device__ __forceinline__ void wait_steps(int steps) {
   if constexpr (MAX > 0) {
-    if (steps < MAX) return wait_steps<N, MAX - 1>(steps);
+    if (steps < MAX) return wait_steps<N, MAX - 1, MORE>(steps);
   }
-  wait_vmcnt<N * MAX>();
+  wait_vmcnt<N * MAX + MORE>();
 }
 
 // WP x WQ waves of BP/WP x BQ/WQ outputs each; ST slots of one step in LDS.
@@ -196,6 +225,7 @@ struct Gemm {
   static constexpr int kP = BP, kQ = BQ;
   static constexpr int NP = BP / WP / 16, NQ = BQ / WQ / 16;
   typedef f32x4 Acc[NP][NQ];
+  static constexpr int kStores = NP * NQ;   // store instructions of a wave's whole part of a tile
 
   __device__ static __forceinline__ int wave_p() { return (threadIdx.x >> 6) % WP * (BP / WP); }
   __device__ static __forceinline__ int wave_q() { return (threadIdx.x >> 6) / WP * (BQ / WQ); }
@@ -283,8 +313,8 @@ struct Gemm {
         oct<T> pv[PT::kPer], qv[QT::kPer];
         PT::load(p, p.base + nk * ps, po, tail, pv);
         QT::load(q, q.base + nk * qs, qo, tail, qv);
-        PT::store(pv, put);
-        QT::store(qv, put + PT::kBytes);
+        PT::store(p, tail, pv, put);
+        QT::store(q, tail, qv, put + PT::kBytes);
         lds_barrier();
         compute(put, acc);
         lds_barrier();
@@ -339,8 +369,8 @@ struct Gemm {
       };
       auto store = [&](int s) {
         uint8_t* slot = lds + (s & 1) * kSlot;
-        PT::store(pv, slot);
-        QT::store(qv, slot + PT::kBytes);
+        PT::store(p, red - s * kStep, pv, slot);
+        QT::store(q, red - s * kStep, qv, slot + PT::kBytes);
       };
       if (nk > 0) {
         load(0);
@@ -356,44 +386,194 @@ struct Gemm {
     }
   }
 
+  // The same as a stream of tiles without a pause between them (DMA, both
+  // operands in columns): the slots that a tile's last steps leave take the next
+  // tile's first ones, so that they arrive while the tile is finished and stored.
+  struct Ring {
+    uint8_t* lds;
+    Operand<T> p, q;   // the tile whose steps are asked for
+    int red, issued;   // its sum's length, and its steps asked for so far
+    int get, put;      // slots of the next step to use and of the next one asked for
+    int arrived;       // 1: its first step has been waited for
+    int stores;        // store instructions of the tile before, issued after this tile's first steps
+    typename PT::Off po[PT::kPer];
+    typename QT::Off qo[QT::kPer];
+
+    __device__ __forceinline__ explicit Ring(uint8_t* lds) : lds(lds), get(0), put(0), stores(0) {}
+    __device__ __forceinline__ void start(const Operand<T>& p_, const Operand<T>& q_, int red_) {
+      p = p_;
+      q = q_;
+      p.base = uniform(p.base);
+      q.base = uniform(q.base);
+      red = red_;
+      issued = 0;
+      arrived = 0;
+      PT::template offsets<true>(p, po);
+      QT::template offsets<true>(q, qo);
+    }
+    __device__ __forceinline__ int steps() const { return (red + kStep - 1) / kStep; }
+    __device__ __forceinline__ void issue() {
+      const uint32_t at = lds_offset(lds) + put * kSlot;
+      const int left = red - kStep * issued;
+      const T *pat = p.base + issued * PT::step_stride(p), *qat = q.base + issued * QT::step_stride(q);
+      if (left >= kStep) {
+        PT::dma(pat, po, at);
+        QT::dma(qat, qo, at + PT::kBytes);
+      } else {
+        PT::dma_part(p, pat, left, at);
+        QT::dma_part(q, qat, left, at + PT::kBytes);
+      }
+      ++issued;
+      put = put + 1 == ST ? 0 : put + 1;
+    }
+    __device__ __forceinline__ void fill() {
+      while (issued < ST && issued < steps()) issue();
+    }
+  };
+  // Adds the sums of the ring's tile; next() starts the ring on the tile after
+  // it and says whether there is one. Every wave is past its reads of LDS at the end.
+  template <typename Next>
+  __device__ static __forceinline__ int run_on(Ring& ring, Acc& acc, Next&& next) {
+    constexpr int kPer = PT::kPer + QT::kPer;
+    const int red = ring.red, nk = ring.steps(), tail = red % kStep;
+    int over = 0, more = 0;
+    auto advance = [&] {
+      ring.get = ring.get + 1 == ST ? 0 : ring.get + 1;
+    };
+    auto slot = [&] { return ring.lds + ring.get * kSlot; };
+    auto clear = [&](int s) {   // the partial last step
+      if (s + 1 < nk || !tail) return;
+      PT::clear(tail, slot());
+      QT::clear(tail, slot() + PT::kBytes);
+      lds_barrier();
+    };
+    // Loads and stores complete in the order of their issue. The steps that were
+    // asked for before the last tile's stores do not wait for them; later ones do.
+    const int before = ring.stores ? ring.issued : 0;
+    ring.fill();
+    if (nk > 0) {
+      Half h0, h1;
+      if (!ring.arrived) wait_steps<kPer, ST - 1>(ring.issued - 1);
+      lds_barrier();
+      clear(0);
+      read(slot(), 0, h0);
+      int s = 0;
+      const T *pat = ring.p.base + ring.issued * PT::step_stride(ring.p);
+      const T *qat = ring.q.base + ring.issued * QT::step_stride(ring.q);
+#pragma unroll 1
+      for (; ring.issued < red / kStep; ++s) {   // whole steps to ask for
+        read(slot(), 1, h1);
+        multiply(h0, acc);
+        interleave();
+        if (s + 1 < before) wait_vmcnt<kPer * (ST - 2) + kStores>();   // step s + 1 is in
+        else wait_vmcnt<kPer * (ST - 2)>();
+        lds_barrier();                                                 // for every wave; and all have read step s
+        const uint32_t at = lds_offset(slot());   // (ST steps are on their way: the one asked for next takes this slot)
+        PT::dma(pat, ring.po, at);
+        QT::dma(qat, ring.qo, at + PT::kBytes);
+        pat += PT::step_stride(ring.p);
+        qat += QT::step_stride(ring.q);
+        ++ring.issued;
+        advance();
+        read(slot(), 0, h0);
+        multiply(h1, acc);
+        interleave();
+      }
+      ring.put = (ring.get + ring.issued - s) % ST;
+#pragma unroll 1
+      for (; s < nk - 1; ++s) {
+        read(slot(), 1, h1);
+        multiply(h0, acc);
+        interleave();
+        const int flying = over ? nk - 2 - s + ring.issued : ring.issued - 2 - s;
+        if (s + 1 < before) wait_steps<kPer, ST - 2, kStores>(flying);   // step s + 1 is in
+        else wait_steps<kPer, ST - 2>(flying);
+        lds_barrier();   // for every wave; and all have read step s
+        if (!over && ring.issued == nk) {
+          over = 1;
+          more = next();
+        }
+        if (over ? more && ring.issued < ring.steps() : true) ring.issue();
+        advance();
+        clear(s + 1);
+        read(slot(), 0, h0);
+        multiply(h1, acc);
+        interleave();
+      }
+      read(slot(), 1, h1);
+      multiply(h0, acc);
+      multiply(h1, acc);
+      advance();
+      lds_barrier();
+    }
+    if (!over) more = next();
+    if (more) {
+      ring.fill();
+      if (ring.issued > 0) {   // before the stores, which would be waited for too
+        wait_steps<kPer, ST - 1>(ring.issued - 1);
+        ring.arrived = 1;
+      }
+    }
+    return more;
+  }
+
   // Writes the tile's first `pn` outputs of each row at `out` (type f32 or T),
   // rows `ld` apart; row(q) is the place of tile row q (below 0: not stored).
-  // `stream`: past the caches (the non-temporal bit), where the whole output is larger than they are.
   template <typename Row>
-  __device__ static __forceinline__ void store(const Acc& acc, void* out, bool f32, bool stream, int64_t ld, int pn,
-                                               Row&& row) {
-    if (f32) store_to(acc, (float*)out, stream, ld, pn, row);
-    else store_to(acc, (T*)out, stream, ld, pn, row);
+  __device__ static __forceinline__ void store(const Acc& acc, void* out, bool f32, int64_t ld, int pn, Row&& row) {
+    if (f32) store_to(acc, (float*)out, ld, pn, row);
+    else store_to(acc, (T*)out, ld, pn, row);
   }
   template <typename U, typename Row>
-  __device__ static __forceinline__ void store_to(const Acc& acc, U* out, bool stream, int64_t ld, int pn, Row& row) {
-    if (pn < BP) store_as<false, false>(acc, out, ld, pn, row);
-    else if (stream) store_as<true, true>(acc, out, ld, pn, row);
-    else store_as<true, false>(acc, out, ld, pn, row);
+  __device__ static __forceinline__ void store_to(const Acc& acc, U* out, int64_t ld, int pn, Row& row) {
+    if constexpr (NP % 2 == 0) {
+      if (pn >= BP) return store_whole(acc, out, ld, row);
+    }
+    store_part(acc, out, ld, pn, row);
   }
-  template <bool FULL, bool STREAM, typename U, typename Row>
-  __device__ static __forceinline__ void store_as(const Acc& acc, U* out, int64_t ld, int pn, Row& row) {
+  template <typename U, typename Row>
+  __device__ static __forceinline__ void store_part(const Acc& acc, U* out, int64_t ld, int pn, Row& row) {
     const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int j = 0; j < NQ; ++j) {
       const int64_t q = row(wave_q() + 16 * j + (lane & 15));
       if (q < 0) continue;
       const int p = wave_p() + 4 * (lane >> 4);
-      U* at = out + q * ld + p;
 #pragma unroll
-      for (int i = 0; i < NP; ++i) store_quad<STREAM>(at + 16 * i, acc[i][j], FULL ? 4 : pn - p - 16 * i);
+      for (int i = 0; i < NP; ++i) store_quad(out + q * ld + p + 16 * i, acc[i][j], pn - p - 16 * i);
+    }
+  }
+  // Lanes q and q + 8 of 16 exchange a quad, so that a store writes 32
+  // neighbouring outputs of 8 rows instead of 16 of 16 rows.
+  template <typename U, typename Row>
+  __device__ static __forceinline__ void store_whole(const Acc& acc, U* out, int64_t ld, Row& row) {
+    const int lane = threadIdx.x & 63, upper = lane >> 3 & 1;
+#pragma unroll
+    for (int j = 0; j < NQ; ++j) {
+      const int64_t qa = row(wave_q() + 16 * j + (lane & 7)), qb = row(wave_q() + 16 * j + 8 + (lane & 7));
+      U* const at = out + wave_p() + 16 * upper + 4 * (lane >> 4);
+#pragma unroll
+      for (int i = 0; i < NP; i += 2) {
+        f32x4 a = acc[i][j], b = acc[i + 1][j], x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[e] = dpp_f32<kDppRor8>(upper ? a[e] : b[e]);
+          a[e] = upper ? x[e] : a[e];
+          b[e] = upper ? b[e] : x[e];
+        }
+        if (qa >= 0) store_quad(at + qa * ld + 16 * i, a, 4);
+        if (qb >= 0) store_quad(at + qb * ld + 16 * i, b, 4);
+      }
     }
   }
 
   // The first n of four outputs, rounded to nearest even in U.
-  template <bool STREAM, typename U>
+  template <typename U>
   __device__ static __forceinline__ void store_quad(U* at, f32x4 f, int n) {
     typedef U quad __attribute__((ext_vector_type(4)));
-    typedef quad quad_at __attribute__((aligned(sizeof(U))));   // any element alignment
     const quad v = __builtin_convertvector(f, quad);
     if (n >= 4) {
-      if (STREAM) __builtin_nontemporal_store(v, (quad_at*)at);
-      else *(quad_at*)at = v;
+      __builtin_memcpy(at, &v, sizeof(v));
     } else {
 #pragma unroll
       for (int i = 0; i < 3; ++i)

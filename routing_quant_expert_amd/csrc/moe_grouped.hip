@@ -22,8 +22,7 @@ struct GroupedArgs {
   int32_t* status;
   int groups, rows;
   int n, k;
-  int f32;      // outputs in f32
-  int stream;   // outputs past the caches
+  int f32;   // outputs in f32
   int64_t x_stride, y_stride, w_stride, w_group;
 };
 
@@ -117,7 +116,7 @@ __global__ __launch_bounds__(G::NT, 2) void k_grouped(GroupedArgs a, const T* __
   typename G::Acc acc = {};
   G::run(P, Q, none ? 0 : red, lds, acc);
   uint8_t* o = (uint8_t*)out + (t.row * out_stride + p0) * (a.f32 ? 4 : 2);
-  G::store(acc, o, a.f32, a.stream, out_stride, width - p0, [&](int q) { return q < t.rows ? q : -1; });
+  G::store(acc, o, a.f32, out_stride, width - p0, [&](int q) { return q < t.rows ? q : -1; });
 }
 
 template <typename T, typename G>
@@ -138,7 +137,55 @@ __global__ __launch_bounds__(G::NT, 2) void k_grouped_dw(GroupedArgs a, const T*
   typename G::Acc acc = {};
   G::run(P, Q, hi - lo, lds, acc);
   uint8_t* o = (uint8_t*)dw + (g * a.w_group + q0 * a.w_stride + p0) * (a.f32 ? 4 : 2);
-  G::store(acc, o, a.f32, a.stream, a.w_stride, a.k - p0, [&](int q) { return q0 + q < a.n ? q : -1; });
+  G::store(acc, o, a.f32, a.w_stride, a.k - p0, [&](int q) { return q0 + q < a.n ? q : -1; });
+}
+
+// The weight gradients' tiles in chunks of `wide` x `tall` (q x p) tiles of one
+// group. Chunks go to the XCDs in turn, so that each finds a chunk's operands in
+// its own L2 and gets a share of every group's work; its workgroups take its tiles in turn.
+// The tiles follow one another without a pause (Gemm::run_on): the sum of a
+// group of 512 rows is 8 steps, as long as a tile's start and end take.
+struct Chunks {
+  int wide, tall, nq, np;   // tiles of a chunk, chunks of a group
+};
+
+template <typename T, typename G>
+__global__ __launch_bounds__(G::NT, 2) void k_grouped_dw_ring(GroupedArgs a, Chunks ch, const T* __restrict__ dy,
+                                                              const T* __restrict__ x, void* __restrict__ dw) {
+  extern __shared__ __align__(16) uint8_t lds[];
+  report(a);
+  const int np = (a.k + G::kP - 1) / G::kP, nq = (a.n + G::kQ - 1) / G::kQ;
+  const int per = ch.wide * ch.tall, chunks = a.groups * ch.nq * ch.np, stride = gridDim.x / 8;
+  struct Place {
+    int g, p0, q0;
+  };
+  auto same = [](int v) { return __builtin_amdgcn_readfirstlane(v); };   // (divisions are done in vector registers)
+  int t = (int)(blockIdx.x / 8) - stride;
+  typename G::Ring ring(lds);
+  Place cur = {}, then = {};
+  auto next = [&]() -> int {
+    for (;;) {
+      t += stride;
+      const int c = same(t / per) * 8 + (int)(blockIdx.x % 8), in = t - t / per * per;
+      if (c >= chunks) return 0;
+      const int g = same(c / (ch.nq * ch.np)), rest = c % (ch.nq * ch.np);
+      const int qt = same(rest / ch.np * ch.wide + in / ch.tall), pt = same(rest % ch.np * ch.tall + in % ch.tall);
+      if (qt >= nq || pt >= np) continue;
+      then = {g, pt * G::kP, qt * G::kQ};
+      const int lo = same(edge(a, g + 1)), hi = same(edge(a, g + 2));
+      ring.start({x + lo * a.x_stride + then.p0, a.x_stride, a.k - then.p0, nullptr, true},
+                 {dy + lo * a.y_stride + then.q0, a.y_stride, a.n - then.q0, nullptr, true}, max(hi - lo, 0));
+      return 1;
+    }
+  };
+  for (int more = next(); more;) {
+    cur = then;
+    typename G::Acc acc = {};
+    more = G::run_on(ring, acc, next);
+    uint8_t* o = (uint8_t*)dw + (cur.g * a.w_group + cur.q0 * a.w_stride + cur.p0) * (a.f32 ? 4 : 2);
+    G::store(acc, o, a.f32, a.w_stride, a.k - cur.p0, [&](int q) { return cur.q0 + q < a.n ? q : -1; });
+    ring.stores = cur.q0 + G::kQ <= a.n && cur.p0 + G::kP <= a.k ? G::kStores : 0;
+  }
 }
 
 enum Way { kForward, kInput, kWeight };
@@ -165,17 +212,8 @@ int check_grouped(const moe_grouped* g, int64_t rows) {
   return MOE_OK;
 }
 
-// f32 outputs of 64 MiB and more, twice what the L2s hold, are written past
-// the caches: they would push the operands out that neighbouring tiles share.
-// The weight gradient of 16384 rows over 32 groups of 4096 x 2048 (1.07 GB):
-// 466 us against 575. (16-bit outputs are the same either way.)
-bool past_caches(const moe_grouped& g, Way way, int64_t rows) {
-  const double count = way == kWeight ? (double)g.n_groups * g.n * g.k : (double)rows * (way == kForward ? g.n : g.k);
-  return g.out_type == MOE_TYPE_F32 && 4 * count >= (double)(64 << 20);
-}
-
-GroupedArgs grouped_args(const moe_grouped& g, Way way, const int32_t* offsets, int64_t rows, int32_t* status) {
-  return {offsets, status, g.n_groups, (int)rows, g.n, g.k, g.out_type == MOE_TYPE_F32, past_caches(g, way, rows),
+GroupedArgs grouped_args(const moe_grouped& g, const int32_t* offsets, int64_t rows, int32_t* status) {
+  return {offsets, status, g.n_groups, (int)rows, g.n, g.k, g.out_type == MOE_TYPE_F32,
           g.x_stride, g.y_stride, g.w_stride, g.w_group_stride};
 }
 
@@ -228,6 +266,32 @@ int launch_dw(const GroupedArgs& a, const void* dy, const void* x, void* dw, hip
   return launch<k_grouped_dw<T, G>, G>(tiles, s, a, (const T*)dy, (const T*)x, dw);
 }
 
+template <typename T, typename G>
+int launch_dw_ring(const GroupedArgs& a, int at_once, const void* dy, const void* x, void* dw, hipStream_t s) {
+  const int np = (a.k + G::kP - 1) / G::kP, nq = (a.n + G::kQ - 1) / G::kQ;
+  int wide = nq < 8 ? nq : 8, tall = np;
+  auto parts = [](int n, int d) { return (n + d - 1) / d; };
+  while ((int64_t)a.groups * parts(nq, wide) * parts(np, tall) < 64 && wide * tall > 1) {   // a share for every XCD
+    if (tall > wide || wide == 1) tall = parts(tall, 2);
+    else wide = parts(wide, 2);
+  }
+  const Chunks ch = {wide, tall, parts(nq, wide), parts(np, tall)};
+  const int64_t tiles = (int64_t)np * nq * a.groups;
+  if ((int64_t)a.groups * ch.nq * ch.np * wide * tall >= INT32_MAX / 16)
+    return fail(MOE_EUNSUPPORTED, "grouped: too many tiles for one launch%s (%lld)", "", tiles);
+  return launch_tiles<k_grouped_dw_ring<T, G>>("grouped", dim3(tiles < at_once ? (tiles + 7) / 8 * 8 : at_once),
+                                               G::NT, G::kLds, s, a, ch, (const T*)dy, (const T*)x, dw);
+}
+
+template <typename T>
+int launch_dw_aligned(const GroupedArgs& a, const void* dy, const void* x, void* dw, hipStream_t s) {
+  // Four tiles a CU and more: the larger tile, one workgroup a CU with a third step in flight. 16384 rows over 32
+  // groups of 4096 x 2048 (16384 small tiles): 565 us against 640; 1200 over 4 of 1024 x 2048 (512): 17.1 against 15.5.
+  const int64_t tiles = (int64_t)((a.k + 255) / 256) * ((a.n + 127) / 128) * a.groups;
+  if (tiles >= 1024) return launch_dw_ring<T, Gemm<T, true, true, 256, 128, 4, 2, 3, true>>(a, 256, dy, x, dw, s);
+  return launch_dw_ring<T, Gemm<T, true, true, 128, 128, 2, 2, 2, true>>(a, 512, dy, x, dw, s);
+}
+
 template <typename T>
 int launch_way(Way way, const GroupedArgs& a, const void* in, const void* w, void* out, hipStream_t s) {
   if (way == kForward)
@@ -239,7 +303,7 @@ int launch_way(Way way, const GroupedArgs& a, const void* in, const void* w, voi
                ? launch_rows_as<T, true, true>(a, in, w, out, s)
                : launch_rows_as<T, true, false>(a, in, w, out, s);
   return rows16(in, a.y_stride) && rows16(w, a.x_stride) && a.n % 8 == 0 && a.k % 8 == 0
-             ? launch_dw<T, Gemm<T, true, true, 128, 128, 2, 2, 2, true>>(a, in, w, out, s)
+             ? launch_dw_aligned<T>(a, in, w, out, s)
              : launch_dw<T, Gemm<T, true, true, 128, 128, 2, 2, 2, false>>(a, in, w, out, s);
 }
 
@@ -253,7 +317,7 @@ int grouped(Way way, const moe_grouped* g, const void* in, const void* w, const 
   const size_t es = elem_bytes(g->out_type);
   if ((uintptr_t)in % 2 || (uintptr_t)w % 2 || (uintptr_t)out % es || (uintptr_t)offsets % 4 || (uintptr_t)status % 4)
     return fail(MOE_EINVAL, "grouped: a pointer is not aligned to its elements%s%lld");
-  const GroupedArgs a = grouped_args(*g, way, offsets, rows, status);
+  const GroupedArgs a = grouped_args(*g, offsets, rows, status);
   const hipStream_t s = (hipStream_t)stream;
   return g->type == MOE_TYPE_BF16 ? launch_way<bf16_t>(way, a, in, w, out, s)
                                   : launch_way<fp16_t>(way, a, in, w, out, s);

@@ -9,7 +9,8 @@
 //
 // Bound by HBM: every operand is read once and every result written once, the
 // row stays in registers in between. A row belongs to TPR threads (one wave,
-// or a workgroup), thread t holding the chunks t, t + TPR, ... of 8 elements.
+// or a workgroup), thread t holding the chunks t, t + TPR, ... of 8 elements
+// (the last one short where the row is no multiple of 8).
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -71,8 +72,23 @@ __device__ __forceinline__ float dot8(f32x8 a, f32x8 b) {
   return s;
 }
 
+// How rows end (chosen by the launch: a branch at every load costs 10 to 30%):
+// whole chunks, a short one at the end, or a row of less than one chunk.
+enum Rows { kWhole, kRagged, kTiny };
+template <int ROWS, typename T>
+__device__ __forceinline__ oct<T> raw_chunk(const T* p, int n) {
+  if constexpr (ROWS != kWhole) return raw_oct(p, n, ROWS == kRagged);
+  oct<T> o = {};
+  if (n > 0) __builtin_memcpy(&o, p, sizeof(o));
+  return o;
+}
+template <int ROWS, typename T>
+__device__ __forceinline__ oct<T> placed_chunk(oct<T> o, int n) {
+  return ROWS == kRagged ? placed_oct<T>(o, n, true) : o;
+}
+
 // (x_out may be x and y may be b: each thread has read what it overwrites.)
-template <typename T, typename RT, int TPR, int NC>
+template <typename T, typename RT, int TPR, int NC, int ROWS>
 __global__ __launch_bounds__(TPR < kJoinThreads ? kJoinThreads : TPR) void k_join(
     JoinArgs a, const RT* x, const T* b, const T* __restrict__ w_post, const T* __restrict__ gate,
     const T* __restrict__ w_pre, RT* x_out, T* y) {
@@ -84,17 +100,27 @@ __global__ __launch_bounds__(TPR < kJoinThreads ? kJoinThreads : TPR) void k_joi
   // Everything is asked for at once, the vectors too (from the caches): a call of few rows waits for memory once.
   f32x8 xv[NC];
   const float inv_dim = 1.0f / (float)a.dim;
-  const bool room = a.dim >= 8;
   oct<RT> xr[NC];
   oct<T> br[NC] = {}, po[NC] = {}, ga[NC] = {}, pr[NC] = {};
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     const int c = 8 * (t + TPR * i), left = a.dim - c;
-    xr[i] = load_oct(x + row * a.x_stride + c, left, room);
-    if (b) br[i] = load_oct(b + row * a.b_stride + c, left, room);
-    if (w_post) po[i] = load_oct(w_post + c, left, room);
-    if (gate) ga[i] = load_oct(gate + (a.gate_rows ? row * a.gate_stride : 0) + c, left, room);
-    if (w_pre) pr[i] = load_oct(w_pre + c, left, room);
+    xr[i] = raw_chunk<ROWS>(x + row * a.x_stride + c, left);
+    if (b) br[i] = raw_chunk<ROWS>(b + row * a.b_stride + c, left);
+    if (w_post) po[i] = raw_chunk<ROWS>(w_post + c, left);
+    if (gate) ga[i] = raw_chunk<ROWS>(gate + (a.gate_rows ? row * a.gate_stride : 0) + c, left);
+    if (w_pre) pr[i] = raw_chunk<ROWS>(w_pre + c, left);
+  }
+  if (ROWS != kWhole) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int left = a.dim - 8 * (t + TPR * i);
+      xr[i] = placed_chunk<ROWS, RT>(xr[i], left);
+      br[i] = placed_chunk<ROWS, T>(br[i], left);
+      po[i] = placed_chunk<ROWS, T>(po[i], left);
+      ga[i] = placed_chunk<ROWS, T>(ga[i], left);
+      pr[i] = placed_chunk<ROWS, T>(pr[i], left);
+    }
   }
   if (b) {
     float rb = 1.0f;
@@ -152,7 +178,7 @@ struct JoinChunk {
   oct<T> dy, b, gate;
 };
 
-template <typename T, typename RT, int TPR, int NC>
+template <typename T, typename RT, int TPR, int NC, int ROWS>
 __global__ __launch_bounds__(TPR) void k_join_back(JoinArgs a, const T* __restrict__ dy, const RT* dxo,
                                                    const RT* __restrict__ xo, const T* b,
                                                    const T* __restrict__ w_post, const T* __restrict__ gate,
@@ -167,26 +193,38 @@ __global__ __launch_bounds__(TPR) void k_join_back(JoinArgs a, const T* __restri
   __shared__ float buf[2][6 * (TPR / 64)];
   const int t = threadIdx.x;
   const float inv_dim = 1.0f / (float)a.dim;
-  const bool room = a.dim >= 8;
   const bool through = db && w_post;   // db goes through the norm
   auto vectors_at = [&](int c) {
     Vectors v = {};
-    if (dy) v.pre = load_oct(w_pre + c, a.dim - c, room);
-    if (w_post) v.post = load_oct(w_post + c, a.dim - c, room);
-    if (gate && !a.gate_rows) v.gate = load_oct(gate + c, a.dim - c, room);
+    if (dy) v.pre = raw_chunk<ROWS>(w_pre + c, a.dim - c);
+    if (w_post) v.post = raw_chunk<ROWS>(w_post + c, a.dim - c);
+    if (gate && !a.gate_rows) v.gate = raw_chunk<ROWS>(gate + c, a.dim - c);
     return v;
   };
   auto chunk_at = [&](int64_t row, int c) {
     Chunk r = {};
     const int left = a.dim - c;
-    if (dxo) r.dxo = load_oct(dxo + row * a.x_out_stride + c, left, room);
+    if (dxo) r.dxo = raw_chunk<ROWS>(dxo + row * a.x_out_stride + c, left);
     if (dy) {
-      r.xo = load_oct(xo + row * a.x_out_stride + c, left, room);
-      r.dy = load_oct(dy + row * a.y_stride + c, left, room);
+      r.xo = raw_chunk<ROWS>(xo + row * a.x_out_stride + c, left);
+      r.dy = raw_chunk<ROWS>(dy + row * a.y_stride + c, left);
     }
-    if (b) r.b = load_oct(b + row * a.b_stride + c, left, room);
-    if (gate && a.gate_rows) r.gate = load_oct(gate + row * a.gate_stride + c, left, room);
+    if (b) r.b = raw_chunk<ROWS>(b + row * a.b_stride + c, left);
+    if (gate && a.gate_rows) r.gate = raw_chunk<ROWS>(gate + row * a.gate_stride + c, left);
     return r;
+  };
+  // Rows of no multiple of 8 elements: the chunks put in place, where they are used.
+  auto place_vectors = [&](Vectors& v, int c) {
+    v.pre = placed_chunk<ROWS, T>(v.pre, a.dim - c);
+    v.post = placed_chunk<ROWS, T>(v.post, a.dim - c);
+    v.gate = placed_chunk<ROWS, T>(v.gate, a.dim - c);
+  };
+  auto place_chunk = [&](Chunk& r, int c) {
+    r.dxo = placed_chunk<ROWS, RT>(r.dxo, a.dim - c);
+    r.xo = placed_chunk<ROWS, RT>(r.xo, a.dim - c);
+    r.dy = placed_chunk<ROWS, T>(r.dy, a.dim - c);
+    r.b = placed_chunk<ROWS, T>(r.b, a.dim - c);
+    r.gate = placed_chunk<ROWS, T>(r.gate, a.dim - c);
   };
   f32x8 s_pre[NC] = {}, s_post[NC] = {}, s_gate[NC] = {};
   Vectors vec[NC];
@@ -195,6 +233,7 @@ __global__ __launch_bounds__(TPR) void k_join_back(JoinArgs a, const T* __restri
   for (int i = 0; i < NC; ++i) {
     if (kKeep) vec[i] = vectors_at(8 * (t + TPR * i));
     if (kAhead) next[i] = chunk_at(blockIdx.x, 8 * (t + TPR * i));
+    if (kKeep) place_vectors(vec[i], 8 * (t + TPR * i));
   }
   int turn = 0;
   for (int64_t row = blockIdx.x; row < a.m; row += gridDim.x, turn ^= 1) {
@@ -210,9 +249,14 @@ __global__ __launch_bounds__(TPR) void k_join_back(JoinArgs a, const T* __restri
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = 8 * (t + TPR * i);
-      if (kKeep && !kAhead) cur[i] = chunk_at(row, c);
-      const Chunk r = kKeep ? cur[i] : chunk_at(row, c);
-      const Vectors v = kKeep ? vec[i] : vectors_at(c);
+      if (!kAhead) cur[i] = chunk_at(row, c);
+      if (!kKeep) {
+        vec[i] = vectors_at(c);
+        place_vectors(vec[i], c);
+      }
+      place_chunk(cur[i], c);
+      const Chunk& r = cur[i];
+      const Vectors& v = vec[i];
       const f32x8 bv = to_f32(r.b), xv = to_f32(r.xo), d = to_f32(r.dy) * to_f32(v.pre);
       s[0] += sum_of_squares(xv);
       s[1] += dot8(d, xv);
@@ -234,8 +278,14 @@ __global__ __launch_bounds__(TPR) void k_join_back(JoinArgs a, const T* __restri
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = 8 * (t + TPR * i), left = a.dim - c;
-      const Chunk r = kKeep ? cur[i] : chunk_at(row, c);
-      const Vectors v = kKeep ? vec[i] : vectors_at(c);
+      if (!kKeep) {
+        cur[i] = chunk_at(row, c);
+        vec[i] = vectors_at(c);
+        place_chunk(cur[i], c);
+        place_vectors(vec[i], c);
+      }
+      const Chunk& r = cur[i];
+      const Vectors& v = vec[i];
       f32x8 g = to_f32(r.dxo);
       if (dy) {
         const f32x8 xv = to_f32(r.xo), dn = to_f32(r.dy);
@@ -335,42 +385,55 @@ JoinArgs join_args(const moe_join& j, int64_t m) {
   return {j.dim, j.gate_rows, j.scale, j.eps, m, j.x_stride, j.x_out_stride, j.b_stride, j.gate_stride, j.y_stride};
 }
 
-template <typename T, typename RT, int TPR, int NC>
+template <typename T, typename RT, int TPR, int NC, int ROWS>
 void launch_join_as(const JoinArgs& a, const void* x, const void* b, const void* w_post, const void* gate,
                     const void* w_pre, void* x_out, void* y, hipStream_t s) {
   constexpr int kRows = TPR < kJoinThreads ? kJoinThreads / TPR : 1;
-  k_join<T, RT, TPR, NC><<<dim3((unsigned)((a.m + kRows - 1) / kRows)), dim3(kRows * TPR), 0, s>>>(
+  k_join<T, RT, TPR, NC, ROWS><<<dim3((unsigned)((a.m + kRows - 1) / kRows)), dim3(kRows * TPR), 0, s>>>(
       a, (const RT*)x, (const T*)b, (const T*)w_post, (const T*)gate, (const T*)w_pre, (RT*)x_out, (T*)y);
 }
 
-template <typename T, typename RT>
-void launch_join(const JoinArgs& a, const void* x, const void* b, const void* w_post, const void* gate,
-                 const void* w_pre, void* x_out, void* y, hipStream_t s) {
-  if (a.dim <= 512) launch_join_as<T, RT, 64, 1>(a, x, b, w_post, gate, w_pre, x_out, y, s);
-  else if (a.dim <= 1024) launch_join_as<T, RT, 64, 2>(a, x, b, w_post, gate, w_pre, x_out, y, s);
-  else if (a.dim <= 2048) launch_join_as<T, RT, 256, 1>(a, x, b, w_post, gate, w_pre, x_out, y, s);
-  else if (a.dim <= 4096) launch_join_as<T, RT, 256, 2>(a, x, b, w_post, gate, w_pre, x_out, y, s);
-  else if (a.dim <= 8192) launch_join_as<T, RT, 512, 2>(a, x, b, w_post, gate, w_pre, x_out, y, s);
-  else launch_join_as<T, RT, 1024, 2>(a, x, b, w_post, gate, w_pre, x_out, y, s);
+template <typename T, typename RT, int ROWS, typename... A>
+void launch_join_rows(const JoinArgs& a, A... args) {
+  if (a.dim <= 512) launch_join_as<T, RT, 64, 1, ROWS>(a, args...);
+  else if (a.dim <= 1024) launch_join_as<T, RT, 64, 2, ROWS>(a, args...);
+  else if (a.dim <= 2048) launch_join_as<T, RT, 256, 1, ROWS>(a, args...);
+  else if (a.dim <= 4096) launch_join_as<T, RT, 256, 2, ROWS>(a, args...);
+  else if (a.dim <= 8192) launch_join_as<T, RT, 512, 2, ROWS>(a, args...);
+  else launch_join_as<T, RT, 1024, 2, ROWS>(a, args...);
 }
 
-template <typename T, typename RT, int TPR, int NC>
+template <typename T, typename RT, typename... A>
+void launch_join(const JoinArgs& a, A... args) {
+  if (a.dim < 8) launch_join_as<T, RT, 64, 1, kTiny>(a, args...);
+  else if (a.dim % 8) launch_join_rows<T, RT, kRagged>(a, args...);
+  else launch_join_rows<T, RT, kWhole>(a, args...);
+}
+
+template <typename T, typename RT, int TPR, int NC, int ROWS>
 void launch_back_as(const JoinArgs& a, const void* dy, const void* dxo, const void* xo, const void* b,
                     const void* w_post, const void* gate, const void* w_pre, void* dx, void* db, void* dgate_rows,
                     float* part, int sums, hipStream_t s) {
-  k_join_back<T, RT, TPR, NC><<<dim3(join_parts(a.dim, a.m)), dim3(TPR), 0, s>>>(
+  k_join_back<T, RT, TPR, NC, ROWS><<<dim3(join_parts(a.dim, a.m)), dim3(TPR), 0, s>>>(
       a, (const T*)dy, (const RT*)dxo, (const RT*)xo, (const T*)b, (const T*)w_post, (const T*)gate, (const T*)w_pre,
       (RT*)dx, (T*)db, (T*)dgate_rows, part, sums);
 }
 
+template <typename T, typename RT, int ROWS, typename... A>
+void launch_back_rows(const JoinArgs& a, A... args) {
+  if (a.dim <= 512) launch_back_as<T, RT, 64, 1, ROWS>(a, args...);
+  else if (a.dim <= 1024) launch_back_as<T, RT, 128, 1, ROWS>(a, args...);
+  else if (a.dim <= 2048) launch_back_as<T, RT, 256, 1, ROWS>(a, args...);
+  else if (a.dim <= 4096) launch_back_as<T, RT, 512, 1, ROWS>(a, args...);
+  else if (a.dim <= 8192) launch_back_as<T, RT, 512, 2, ROWS>(a, args...);
+  else launch_back_as<T, RT, 1024, 2, ROWS>(a, args...);
+}
+
 template <typename T, typename RT, typename... A>
 void launch_back(const JoinArgs& a, A... args) {
-  if (a.dim <= 512) launch_back_as<T, RT, 64, 1>(a, args...);
-  else if (a.dim <= 1024) launch_back_as<T, RT, 128, 1>(a, args...);
-  else if (a.dim <= 2048) launch_back_as<T, RT, 256, 1>(a, args...);
-  else if (a.dim <= 4096) launch_back_as<T, RT, 512, 1>(a, args...);
-  else if (a.dim <= 8192) launch_back_as<T, RT, 512, 2>(a, args...);
-  else launch_back_as<T, RT, 1024, 2>(a, args...);
+  if (a.dim < 8) launch_back_as<T, RT, 64, 1, kTiny>(a, args...);
+  else if (a.dim % 8) launch_back_rows<T, RT, kRagged>(a, args...);
+  else launch_back_rows<T, RT, kWhole>(a, args...);
 }
 
 }  // namespace
