@@ -485,7 +485,7 @@ struct Gemm {
         read(slot(), 1, h1);
         multiply(h0, acc);
         interleave();
-        const int flying = over ? nk - 2 - s + ring.issued : ring.issued - 2 - s;
+        const int flying = !over ? ring.issued - 2 - s : nk - 2 - s + (more ? ring.issued : 0);
         if (s + 1 < before) wait_steps<kPer, ST - 2, kStores>(flying);   // step s + 1 is in
         else wait_steps<kPer, ST - 2>(flying);
         lds_barrier();   // for every wave; and all have read step s
