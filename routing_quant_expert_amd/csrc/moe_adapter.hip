@@ -15,6 +15,12 @@
 // rounded value and the rounded rest (three where a bf16 product makes an f32
 // output), so that it is exact to 2^-16 of itself at least (2^-24 for f32
 // outputs of either type, 2^-22 for fp16).
+//
+// One token of 2048 x 4096, rank 16: 9.8 us a call, 4.6 in the reading launch
+// (3.7 TB/s) and 4.7 in the joining one, whose time is latency. 48 tokens, 24
+// adapters of rank 32: 13.5 us. 4096 tokens of 4096 x 2048, rank 64: 94 us (759
+// TFLOP/s): sort 7.5, u 13 (reading A again for every 16 tokens), tiles 78,
+// where the plain product alone takes a library 52.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -498,6 +504,8 @@ int launch_many(const AdapterArgs& a, const T* x, const T* w, const T* wa, const
   else k_adapter_low<T, 4><<<grid, threads, 0, s>>>(a, so, x, wa);
   e = hipGetLastError();
   if (e != hipSuccess) return hip_fail(e, "adapters");
+  // Tiles by their number, as for the grouped products: 64 x 64 where larger ones would leave CUs idle (1000 tokens of
+  // 1024 x 1024: 19 us), 256 x 128 from three a CU on with long sums (at two a CU, 4096 tokens of 4096 x 2048: 101.6 us against 99.8).
   const int64_t rows = (a.m + 127) / 128;
   if (rows * ((a.n + 127) / 128) < 256)
     return launch_main<T, Gemm<T, false, false, 64, 64, 2, 2, 4, DMA, true>>(a, so, x, w, wb, out, s);

@@ -14,6 +14,12 @@
 //
 // P is the output's contiguous axis and the MFMA's row operand: a lane then
 // holds four neighbouring outputs of one row.
+//
+// What keeps the matrix instructions fed: loads into LDS that no compiler wait
+// stands behind, one barrier a step, and the operands of one half step read
+// while the products of the half before run (in place of a wait for all loads
+// in every step: 128 x 128 tiles went from 648 to 830 TFLOP/s on 16384 rows
+// over 32 groups of 4096 x 2048). No LDS bank conflicts by the counters.
 #pragma once
 
 #include <type_traits>

@@ -5,6 +5,14 @@
 //   input    dx[r] = W[g(r)]^T dy[r]                 P = W columns, Q = dy rows, sum over n
 //   weight   dW[g] = sum over g's rows dy[r] x[r]^T  P = x columns, Q = dy columns
 //
+// Few rows a group: bound by HBM, every used weight is read once (48 rows over
+// 384 groups of 2048 x 4096: 134 us, 6.0 TB/s; 12288 rows: 1119 us, 5.9 TB/s).
+// Many: by the matrix instructions and what the ragged groups leave of them
+// (input gradient of 16384 rows over 32 groups of 4096 x 2048: 335 us, 821
+// TFLOP/s; four even groups of 4096 x 4096: 1150 TFLOP/s; a library product of
+// this size class reaches 1355 to 1450 on even sizes). The weight gradient of
+// the same rows writes 1.07 GB in f32: 554 us, 341 without its stores.
+//
 // The offsets stay on the device: the grid is an upper bound of the tiles (a
 // group adds at most one partial tile), every wave finds its tile from the
 // offsets by two wave-wide prefix sums, and workgroups past the last tile end
@@ -286,7 +294,7 @@ int launch_dw_ring(const GroupedArgs& a, int at_once, const void* dy, const void
 template <typename T>
 int launch_dw_aligned(const GroupedArgs& a, const void* dy, const void* x, void* dw, hipStream_t s) {
   // Four tiles a CU and more: the larger tile, one workgroup a CU with a third step in flight. 16384 rows over 32
-  // groups of 4096 x 2048 (16384 small tiles): 565 us against 640; 1200 over 4 of 1024 x 2048 (512): 17.1 against 15.5.
+  // groups of 4096 x 2048 (16384 small tiles): 565 us against 640; 4000 over 8 of 512 x 1024 (256): 24 against 18.
   const int64_t tiles = (int64_t)((a.k + 255) / 256) * ((a.n + 127) / 128) * a.groups;
   if (tiles >= 1024) return launch_dw_ring<T, Gemm<T, true, true, 256, 128, 4, 2, 3, true>>(a, 256, dy, x, dw, s);
   return launch_dw_ring<T, Gemm<T, true, true, 128, 128, 2, 2, 2, true>>(a, 512, dy, x, dw, s);
