@@ -121,20 +121,26 @@ __global__ __launch_bounds__(256) void k_adapter_sum(AdapterArgs a, int slices, 
     for (int i = 0; i < slices; ++i) s += from[(int64_t)i * a.m * width];
     return s;
   };
+  constexpr int kFirst = 4;   // the first 32 ranks of B are asked for with the sums
+  const T* b = wb + max(mine, 0) * a.b_group + col * a.b_stride;
+  oct<T> first[kFirst];
+#pragma unroll
+  for (int i = 0; i < kFirst; ++i) first[i] = raw_oct(b + 8 * i, mine >= 0 ? a.rank - 8 * i : 0, a.rank >= 8);
   float s = total(part + col, a.n);
   if (mine >= 0) {
     for (int j = threadIdx.x; j < a.rank; j += 256) u[j] = factor_of(a, mine) * total(upart + j, a.rank);
   }
   __syncthreads();
   if (mine >= 0) {
-    const T* b = wb + mine * a.b_group + col * a.b_stride;
-#pragma unroll 2
-    for (int j = 0; j < a.rank; j += 8) {
-      const f32x8 v = to_f32(load_oct(b + j, a.rank - j, a.rank >= 8));
+    auto add = [&](oct<T> o, int j) {
+      const f32x8 v = to_f32(o);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (j + i < a.rank) s = fmaf(u[j + i], v[i], s);
-    }
+    };
+#pragma unroll
+    for (int i = 0; i < kFirst; ++i) add(placed_oct<T>(first[i], a.rank - 8 * i, a.rank >= 8), 8 * i);
+    for (int j = 8 * kFirst; j < a.rank; j += 8) add(load_oct(b + j, a.rank - j, a.rank >= 8), j);
   }
   if (c < a.n) out[t * a.out_stride + c] = (U)s;
 }
@@ -353,9 +359,6 @@ __global__ __launch_bounds__(G::NT, 2) void k_adapter_main(AdapterArgs a, Sorted
   const int p0 = pt * G::kP, row0 = qt * G::kQ, lane = threadIdx.x & 63;
   const Operand<T> P = {w + p0 * a.w_stride, a.w_stride, min(G::kP, a.n - p0), nullptr, a.k >= 8};
   const Operand<T> Q = {x, a.x_stride, G::kQ, so.token + row0, a.k >= 8};
-  typename G::Acc acc = {};
-  G::run(P, Q, a.k, lds, acc);
-
   constexpr int kOwners = (G::kQ + 63) / 64;
   int owner[kOwners];   // of row 64 i + lane of the tile: ascending, but for rows of no token at the end
 #pragma unroll
@@ -363,6 +366,9 @@ __global__ __launch_bounds__(G::NT, 2) void k_adapter_main(AdapterArgs a, Sorted
   int mine[G::NQ];      // of the rows whose outputs this lane holds
 #pragma unroll
   for (int j = 0; j < G::NQ; ++j) mine[j] = so.owner[row0 + G::wave_q() + 16 * j + (lane & 15)];
+  typename G::Acc acc = {};
+  G::run(P, Q, a.k, lds, acc);
+
   // the first adapter of the tile above `done`, or -1
   auto after = [&](int done) {
     int next = -1;
@@ -374,17 +380,25 @@ __global__ __launch_bounds__(G::NT, 2) void k_adapter_main(AdapterArgs a, Sorted
     return next;
   };
   const int first = after(-1);
+  oct<T> bv[G::PT::kPer];
+  auto b_of = [&](int adapter, int r0) -> Operand<T> {
+    return {wb + adapter * a.b_group + p0 * a.b_stride + r0, a.b_stride, min(G::kP, a.n - p0), nullptr, a.rank >= 8};
+  };
+  auto ask_b = [&](int adapter, int r0) {
+    const Operand<T> B = b_of(adapter, r0);
+    typename G::PT::Off off[G::PT::kPer];
+    G::PT::template offsets<false>(B, off);
+    G::PT::load(B, B.base, off, a.rank - r0, bv);
+  };
   for (int r0 = 0; first >= 0 && r0 < a.rank; r0 += kStep) {
     uint8_t* const ut = lds + G::PT::kBytes;
+    ask_b(first, r0);
     lds_barrier();
     stage_u<T, G, PIECES>(so, row0, r0, ut, row_scale);
-    for (int next = first; next >= 0; next = after(next)) {
-      const Operand<T> B = {wb + next * a.b_group + p0 * a.b_stride + r0, a.b_stride, min(G::kP, a.n - p0), nullptr, a.rank >= 8};
-      typename G::PT::Off off[G::PT::kPer];
-      oct<T> v[G::PT::kPer];
-      G::PT::template offsets<false>(B, off);
-      G::PT::load(B, B.base, off, a.rank - r0, v);
-      G::PT::store(B, a.rank - r0, v, lds);
+    for (int next = first, then; next >= 0; next = then) {
+      G::PT::store(b_of(next, r0), a.rank - r0, bv, lds);
+      then = after(next);
+      if (then >= 0) ask_b(then, r0);   // on its way while this one's products run
       lds_barrier();
 #pragma unroll
       for (int j = 0; j < G::NQ; ++j) {

@@ -606,14 +606,15 @@ __device__ __forceinline__ void tile_at(int64_t l, int n_rt, int np, int& rt, in
   pt = in / wide;
 }
 
-// The wave's inclusive prefix sums.
+// The wave's inclusive prefix sums: within 16 lanes by shifts, then the last
+// lane of each 16 (and of the lower 32) to those above. All lanes take part.
 __device__ __forceinline__ int wave_scan(int v, int lane) {
-#pragma unroll
-  for (int s = 1; s < 64; s *= 2) {
-    const int o = __shfl_up(v, s);
-    if (lane >= s) v += o;
-  }
-  return v;
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);   // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);   // row_shr:2
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);   // row_shr:4
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);   // row_shr:8
+  const int a = __builtin_amdgcn_readlane(v, 15), b = __builtin_amdgcn_readlane(v, 31), c = __builtin_amdgcn_readlane(v, 47);
+  return v + (lane < 16 ? 0 : lane < 32 ? a : lane < 48 ? a + b : a + b + c);
 }
 
 // Rows that can be brought into LDS 16 bytes at a time.

@@ -57,7 +57,8 @@ __device__ __forceinline__ Tile find_tile(const GroupedArgs& a, int np) {
   const int lane = threadIdx.x & 63, entries = a.groups + 2, U = (entries + 63) / 64;
   auto tiles = [](int lo, int hi) { return hi > lo ? (hi - lo + BQ - 1) / BQ : 0; };
   int sum = 0;
-  int lo = edge(a, lane * U);
+  const int lo0 = edge(a, lane * U);
+  int lo = lo0;
   for (int u = 0; u < U; ++u) {
     const int e = lane * U + u;
     if (e >= entries) break;
@@ -66,24 +67,33 @@ __device__ __forceinline__ Tile find_tile(const GroupedArgs& a, int np) {
     lo = hi;
   }
   const int incl = wave_scan(sum, lane);
-  const int64_t total = (int64_t)__shfl(incl, 63) * np;
+  const int64_t total = (int64_t)__builtin_amdgcn_readlane(incl, 63) * np;
   const int64_t place = xcd_order(blockIdx.x, total);
   if (place >= total) return {0, 0, 0, 0};
   const int t = (int)(place / np);
   const uint64_t lanes = __ballot(incl > t);
   if (!lanes) return {0, 0, 0, 0};   // (counts of offsets that do not ascend may wrap)
   const int sel = __builtin_ctzll(lanes);
-  const int before = __shfl(incl - sum, sel);
-  const int e = sel * U + lane;
-  const bool mine = lane < U && e < entries;
-  const int elo = mine ? edge(a, e) : 0, ehi = mine ? edge(a, e + 1) : 0;
-  const int cnt = tiles(elo, ehi);
-  const int incl2 = before + wave_scan(cnt, lane);
-  const uint64_t hits = __ballot(incl2 > t);
-  if (!hits) return {0, 0, 0, 0};
-  const int s = __builtin_ctzll(hits);
-  const int first = __shfl(incl2 - cnt, s), n_rt = __shfl(cnt, s);
-  const int glo = __shfl(elo, s), ghi = __shfl(ehi, s);
+  // the sums of the entries before, and the entry's own tiles and rows
+  int s = 0, first = __builtin_amdgcn_readlane(incl - sum, sel), n_rt, glo, ghi;
+  if (U == 1) {   // (a lane has one entry: its edges are there)
+    n_rt = __builtin_amdgcn_readlane(sum, sel);
+    glo = __builtin_amdgcn_readlane(lo0, sel);
+    ghi = __builtin_amdgcn_readlane(lo, sel);
+  } else {
+    const int e = sel * U + lane;
+    const bool mine = lane < U && e < entries;
+    const int elo = mine ? edge(a, e) : 0, ehi = mine ? edge(a, e + 1) : 0;
+    const int cnt = tiles(elo, ehi);
+    const int incl2 = first + wave_scan(cnt, lane);
+    const uint64_t hits = __ballot(incl2 > t);
+    if (!hits) return {0, 0, 0, 0};
+    s = __builtin_ctzll(hits);
+    first = __builtin_amdgcn_readlane(incl2 - cnt, s);
+    n_rt = __builtin_amdgcn_readlane(cnt, s);
+    glo = __builtin_amdgcn_readlane(elo, s);
+    ghi = __builtin_amdgcn_readlane(ehi, s);
+  }
   int rt, pt;
   tile_at(place - (int64_t)first * np, n_rt, np, rt, pt);
   if (rt < 0 || rt >= n_rt) return {0, 0, 0, 0};
