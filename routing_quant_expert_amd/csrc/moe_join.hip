@@ -17,6 +17,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "moe_element.h"
 #include "moe_host.h"
@@ -66,6 +67,17 @@ __device__ __forceinline__ float sum_of_squares(f32x8 f) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) s = fmaf(f[i], f[i], s);
   return s;
+}
+
+__device__ __forceinline__ f32x8 fma8(f32x8 a, f32x8 b, f32x8 c) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) c[i] = fmaf(a[i], b[i], c[i]);
+  return c;
+}
+__device__ __forceinline__ f32x8 fma8(f32x8 a, float b, f32x8 c) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) c[i] = fmaf(a[i], b, c[i]);
+  return c;
 }
 
 __device__ __forceinline__ float dot8(f32x8 a, f32x8 b) {
@@ -170,7 +182,7 @@ __global__ __launch_bounds__(TPR < kJoinThreads ? kJoinThreads : TPR) void k_joi
 // are written as f32 partial sums [P][3][dim] that k_join_sums adds up.
 // Registers permitting, the vectors and the row stay in them (workgroups of up
 // to 512 threads; otherwise they are read again where they are used, from the
-// caches), and the next row is on its way while one is worked on (NC = 1).
+// caches), and the next two rows are on their way while one is worked on (NC = 1).
 //
 // One reduction a row: with d = dy w_pre and h = gate w_post b, the sum that
 // db needs, of dz w_post nb, is s rb (sum h dx_out + rx (sum h d - c1 sum h x')),
@@ -190,8 +202,10 @@ __global__ __launch_bounds__(TPR) void k_join_back(JoinArgs a, const T* __restri
                                                    float* __restrict__ part, int sums) {
   constexpr bool kKeep = TPR <= 512, kAhead = kKeep && NC == 1;
   typedef JoinChunk<T, RT> Chunk;
+  // (in f32 where they fit: at 16 bits the kernel's time is its vector instructions as much as HBM's)
+  typedef std::conditional_t<kAhead, f32x8, oct<T>> Vector;
   struct Vectors {
-    oct<T> pre, post, gate;
+    Vector pre, post, gate;
   };
   __shared__ float buf[2][6 * (TPR / 64)];
   const int t = threadIdx.x;
@@ -199,9 +213,13 @@ __global__ __launch_bounds__(TPR) void k_join_back(JoinArgs a, const T* __restri
   const bool through = db && w_post;   // db goes through the norm
   auto vectors_at = [&](int c) {
     Vectors v = {};
-    if (dy) v.pre = raw_chunk<ROWS>(w_pre + c, a.dim - c);
-    if (w_post) v.post = raw_chunk<ROWS>(w_post + c, a.dim - c);
-    if (gate && !a.gate_rows) v.gate = raw_chunk<ROWS>(gate + c, a.dim - c);
+    auto get = [&](const T* p) {
+      const oct<T> o = placed_chunk<ROWS, T>(raw_chunk<ROWS>(p + c, a.dim - c), a.dim - c);
+      return __builtin_convertvector(o, Vector);
+    };
+    if (dy) v.pre = get(w_pre);
+    if (w_post) v.post = get(w_post);
+    if (gate && !a.gate_rows) v.gate = get(gate);
     return v;
   };
   auto chunk_at = [&](int64_t row, int c) {
@@ -217,11 +235,6 @@ __global__ __launch_bounds__(TPR) void k_join_back(JoinArgs a, const T* __restri
     return r;
   };
   // Rows of no multiple of 8 elements: the chunks put in place, where they are used.
-  auto place_vectors = [&](Vectors& v, int c) {
-    v.pre = placed_chunk<ROWS, T>(v.pre, a.dim - c);
-    v.post = placed_chunk<ROWS, T>(v.post, a.dim - c);
-    v.gate = placed_chunk<ROWS, T>(v.gate, a.dim - c);
-  };
   auto place_chunk = [&](Chunk& r, int c) {
     r.dxo = placed_chunk<ROWS, RT>(r.dxo, a.dim - c);
     r.xo = placed_chunk<ROWS, RT>(r.xo, a.dim - c);
@@ -229,14 +242,17 @@ __global__ __launch_bounds__(TPR) void k_join_back(JoinArgs a, const T* __restri
     r.b = placed_chunk<ROWS, T>(r.b, a.dim - c);
     r.gate = placed_chunk<ROWS, T>(r.gate, a.dim - c);
   };
+  auto gate_of = [&](const Chunk& r, const Vectors& v) { return a.gate_rows ? to_f32(r.gate) : to_f32(v.gate); };
   f32x8 s_pre[NC] = {}, s_post[NC] = {}, s_gate[NC] = {};
   Vectors vec[NC];
-  Chunk cur[NC], next[NC];
+  Chunk cur[NC], next[NC], then[NC];
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     if (kKeep) vec[i] = vectors_at(8 * (t + TPR * i));
-    if (kAhead) next[i] = chunk_at(blockIdx.x, 8 * (t + TPR * i));
-    if (kKeep) place_vectors(vec[i], 8 * (t + TPR * i));
+    if (kAhead) {
+      next[i] = chunk_at(blockIdx.x, 8 * (t + TPR * i));
+      if (blockIdx.x + gridDim.x < a.m) then[i] = chunk_at(blockIdx.x + gridDim.x, 8 * (t + TPR * i));
+    }
   }
   int turn = 0;
   for (int64_t row = blockIdx.x; row < a.m; row += gridDim.x, turn ^= 1) {
@@ -245,7 +261,8 @@ __global__ __launch_bounds__(TPR) void k_join_back(JoinArgs a, const T* __restri
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         cur[i] = next[i];
-        if (row + gridDim.x < a.m) next[i] = chunk_at(row + gridDim.x, 8 * (t + TPR * i));
+        next[i] = then[i];
+        if (row + 2 * (int64_t)gridDim.x < a.m) then[i] = chunk_at(row + 2 * (int64_t)gridDim.x, 8 * (t + TPR * i));
       }
     }
     float s[6] = {};
@@ -253,10 +270,7 @@ __global__ __launch_bounds__(TPR) void k_join_back(JoinArgs a, const T* __restri
     for (int i = 0; i < NC; ++i) {
       const int c = 8 * (t + TPR * i);
       if (!kAhead) cur[i] = chunk_at(row, c);
-      if (!kKeep) {
-        vec[i] = vectors_at(c);
-        place_vectors(vec[i], c);
-      }
+      if (!kKeep) vec[i] = vectors_at(c);
       place_chunk(cur[i], c);
       const Chunk& r = cur[i];
       const Vectors& v = vec[i];
@@ -266,7 +280,7 @@ __global__ __launch_bounds__(TPR) void k_join_back(JoinArgs a, const T* __restri
       if (w_post) s[2] += sum_of_squares(bv);
       if (through) {
         f32x8 h = bv * to_f32(v.post);
-        if (gate) h = h * to_f32(a.gate_rows ? r.gate : v.gate);
+        if (gate) h = h * gate_of(r, v);
         s[3] += dot8(h, to_f32(r.dxo));
         s[4] += dot8(h, d);
         s[5] += dot8(h, xv);
@@ -285,15 +299,14 @@ __global__ __launch_bounds__(TPR) void k_join_back(JoinArgs a, const T* __restri
         cur[i] = chunk_at(row, c);
         vec[i] = vectors_at(c);
         place_chunk(cur[i], c);
-        place_vectors(vec[i], c);
       }
       const Chunk& r = cur[i];
       const Vectors& v = vec[i];
       f32x8 g = to_f32(r.dxo);
       if (dy) {
         const f32x8 xv = to_f32(r.xo), dn = to_f32(r.dy);
-        s_pre[i] += dn * (xv * rx);
-        g += rx * (dn * to_f32(v.pre) - xv * c1);
+        s_pre[i] = fma8(dn, xv * rx, s_pre[i]);
+        g = fma8(fma8(xv, -c1, dn * to_f32(v.pre)), rx, g);
       }
       store_oct(dx + row * a.x_stride + c, g, left);
       if (!b) continue;
@@ -302,14 +315,13 @@ __global__ __launch_bounds__(TPR) void k_join_back(JoinArgs a, const T* __restri
       f32x8 z = nb;
       if (w_post) z = z * to_f32(v.post);
       if (gate) {
-        const f32x8 dg = dz * z;
-        if (!a.gate_rows) s_gate[i] += dg;
-        else if (dgate_rows) store_oct(dgate_rows + row * a.gate_stride + c, dg, left);
-        dz = dz * to_f32(a.gate_rows ? r.gate : v.gate);
+        if (!a.gate_rows) s_gate[i] = fma8(dz, z, s_gate[i]);
+        else if (dgate_rows) store_oct(dgate_rows + row * a.gate_stride + c, dz * z, left);
+        dz = dz * gate_of(r, v);
       }
       if (w_post) {
-        s_post[i] += dz * nb;
-        dz = rb * (dz * to_f32(v.post) - bv * c2);
+        s_post[i] = fma8(dz, nb, s_post[i]);
+        dz = fma8(bv, -c2, dz * to_f32(v.post)) * rb;
       }
       if (db) store_oct(db + row * a.b_stride + c, dz, left);
     }
