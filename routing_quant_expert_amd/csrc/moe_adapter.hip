@@ -16,9 +16,9 @@
 // output), so that it is exact to 2^-16 of itself at least (2^-24 for f32
 // outputs of either type, 2^-22 for fp16).
 //
-// One token of 2048 x 4096, rank 16: 9.8 us a call, 4.6 in the reading launch
+// One token of 2048 x 4096, rank 16: 9.9 us a call, 4.6 in the reading launch
 // (3.7 TB/s) and 4.7 in the joining one, whose time is latency. 48 tokens, 24
-// adapters of rank 32: 13.5 us. 4096 tokens of 4096 x 2048, rank 64: 94 us (759
+// adapters of rank 32: 12.4 us. 4096 tokens of 4096 x 2048, rank 64: 95 us (751
 // TFLOP/s): sort 7.5, u 13 (reading A again for every 16 tokens), tiles 78,
 // where the plain product alone takes a library 52.
 #include <hip/hip_runtime.h>

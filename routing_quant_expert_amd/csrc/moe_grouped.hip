@@ -8,10 +8,10 @@
 // Few rows a group: bound by HBM, every used weight is read once (48 rows over
 // 384 groups of 2048 x 4096: 134 us, 6.0 TB/s; 12288 rows: 1119 us, 5.9 TB/s).
 // Many: by the matrix instructions and what the ragged groups leave of them
-// (input gradient of 16384 rows over 32 groups of 4096 x 2048: 335 us, 821
+// (input gradient of 16384 rows over 32 groups of 4096 x 2048: 337 us, 815
 // TFLOP/s; four even groups of 4096 x 4096: 1150 TFLOP/s; a library product of
 // this size class reaches 1355 to 1450 on even sizes). The weight gradient of
-// the same rows writes 1.07 GB in f32: 554 us, 341 without its stores.
+// the same rows writes 1.07 GB in f32: 546 us, 341 without its stores.
 //
 // The offsets stay on the device: the grid is an upper bound of the tiles (a
 // group adds at most one partial tile), every wave finds its tile from the

@@ -10,7 +10,7 @@
 // Bound by HBM: every operand is read once and every result written once, the
 // row stays in registers in between (8192 rows of 4096, f32 stream: forward 75
 // us, 5.4 TB/s, gradients 118 us, 5.1 TB/s; a copy reaches 5.1). 4096 rows in
-// 16 bits, gradients: 58 us, 3.5 TB/s, of which the column sums take 4. One
+// 16 bits, gradients: 51 us, 3.9 TB/s, of which the column sums take 4. One
 // row of 4096: 3.8 us in the kernel, 5.3 with the call. A row belongs to TPR threads (one wave,
 // or a workgroup), thread t holding the chunks t, t + TPR, ... of 8 elements
 // (the last one short where the row is no multiple of 8).
