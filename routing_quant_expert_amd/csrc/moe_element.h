@@ -69,8 +69,10 @@ __device__ __forceinline__ oct<T> placed_oct(oct<T> o, int n, bool room) {
   if (!room) return o;
   constexpr int W = 2 * sizeof(T);   // words
   uint32_t w[W];
-  const int by = n > 0 ? max(8 - n, 0) : 0;
+  const int by = min(max(8 - n, 0), 8);
   __builtin_memcpy(w, &o, sizeof(w));
+#pragma unroll
+  for (int i = 0; i < W; ++i) w[i] = by & 8 ? 0 : w[i];
   if constexpr (sizeof(T) == 2) {
 #pragma unroll
     for (int i = 0; i < W; ++i) w[i] = by & 4 ? (i + 2 < W ? w[i + 2] : 0) : w[i];

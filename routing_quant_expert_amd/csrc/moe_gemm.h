@@ -159,9 +159,19 @@ struct TileOf {
     if (whole(o, left)) {
 #pragma unroll
       for (int k = 0; k < kPer; ++k) __builtin_memcpy(&v[k], at + off[k], 16);
+    } else if (o.room) {
+      // Every lane loads, where its chunk is not there the row's last elements (or the last row's): without a
+      // branch the loads need not be waited for one by one. store() puts them in place.
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        int r, own;
+        place(position(k), r, own);
+        const int64_t e = COL ? min(r, left - 1) * o.ld + min(own, o.count - 8) : (int64_t)off[k] - r + min(r, left - 8);
+        __builtin_memcpy(&v[k], at + e, 16);
+      }
     } else {
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) v[k] = raw_oct(at + off[k], there(o, k, left), o.room);
+      for (int k = 0; k < kPer; ++k) v[k] = raw_oct(at + off[k], there(o, k, left), false);
     }
   }
   __device__ static __forceinline__ void store(const Operand<T>& o, int left, const oct<T> (&v)[kPer], uint8_t* tile) {
@@ -365,29 +375,51 @@ struct Gemm {
       multiply(h1, acc);
     } else {
       const int nk = (red + kStep - 1) / kStep;
-      oct<T> pv[PT::kPer], qv[QT::kPer];
+      struct Stage {
+        oct<T> p[PT::kPer], q[QT::kPer];
+      };
       const T *pat = p.base, *qat = q.base;
-      auto load = [&](int s) {
-        PT::load(p, pat, po, red - s * kStep, pv);
-        QT::load(q, qat, qo, red - s * kStep, qv);
+      auto load = [&](int s, Stage& g) {
+        PT::load(p, pat, po, red - s * kStep, g.p);
+        QT::load(q, qat, qo, red - s * kStep, g.q);
         pat += ps;
         qat += qs;
       };
-      auto store = [&](int s) {
+      auto store = [&](int s, const Stage& g) {
         uint8_t* slot = lds + (s & 1) * kSlot;
-        PT::store(p, red - s * kStep, pv, slot);
-        QT::store(q, red - s * kStep, qv, slot + PT::kBytes);
+        PT::store(p, red - s * kStep, g.p, slot);
+        QT::store(q, red - s * kStep, g.q, slot + PT::kBytes);
       };
-      if (nk > 0) {
-        load(0);
-        store(0);
-      }
+      if (nk == 0) return;
+      if constexpr (PT::kPer + QT::kPer <= 6) {   // two steps on their way, where the registers hold them
+        Stage g0, g1;
+        load(0, g0);
+        if (nk > 1) load(1, g1);
+        store(0, g0);
 #pragma unroll 1
-      for (int s = 0; s < nk; ++s) {
-        lds_barrier();   // step s is there, and all are done with step s - 1
-        if (s + 1 < nk) load(s + 1);
-        compute(lds + (s & 1) * kSlot, acc);
-        if (s + 1 < nk) store(s + 1);
+        for (int s = 0;; s += 2) {
+          lds_barrier();   // step s is there, and all are done with step s - 1
+          if (s + 2 < nk) load(s + 2, g0);
+          compute(lds, acc);
+          if (s + 1 == nk) break;
+          store(s + 1, g1);
+          lds_barrier();
+          if (s + 3 < nk) load(s + 3, g1);
+          compute(lds + kSlot, acc);
+          if (s + 2 == nk) break;
+          store(s + 2, g0);
+        }
+      } else {
+        Stage g;
+        load(0, g);
+        store(0, g);
+#pragma unroll 1
+        for (int s = 0; s < nk; ++s) {
+          lds_barrier();   // step s is there, and all are done with step s - 1
+          if (s + 1 < nk) load(s + 1, g);
+          compute(lds + (s & 1) * kSlot, acc);
+          if (s + 1 < nk) store(s + 1, g);
+        }
       }
     }
   }
