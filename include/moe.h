@@ -521,8 +521,12 @@ int moe_grouped_backward_w(const moe_grouped* g, const void* dy, const void* x, 
 
 /* A shared projection with one low-rank adapter per token:
  *   out[t] = W x[t] + factor[a] B[a] (A[a] x[t]),  a = index[t]; a = -1: W x[t].
- * Products of 16-bit elements, f32 sums, one rounding at the end (A x is not
- * rounded to 16 bits in between).
+ * Products of 16-bit elements, f32 sums, one rounding at the end. factor A x is
+ * not rounded to 16 bits in between: it enters the products with B in f32, or,
+ * where tokens are sorted by adapter, as the sum of 16-bit terms that leave at
+ * most 2^-16 of it (bf16 outputs), 2^-22 (fp16 inputs) or 2^-24 (f32 outputs of
+ * bf16 inputs), and 2^-39 of the token's largest one in fp16. An infinite element
+ * of B makes outputs that are not finite, infinite or NaN.
  *   x      type [m][k]       w    type [n][k]      out  out_type [m][n]
  *   index  int32 [m] on the device: adapters in any order, each -1 or below n_adapters
  * Adapters of a smaller rank are filled up with zeros. Outputs must not

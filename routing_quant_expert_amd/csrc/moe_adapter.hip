@@ -13,8 +13,11 @@
 // adds them to the outputs of that adapter's tokens alone: no other token's
 // values meet its weights. u enters those products as two 16-bit terms, its
 // rounded value and the rounded rest (three where a bf16 product makes an f32
-// output), so that it is exact to 2^-16 of itself at least (2^-24 for f32
-// outputs of either type, 2^-22 for fp16).
+// output), which leave at most 2^-16 of u (bf16 outputs), 2^-24 (f32 of bf16) or
+// 2^-22 (fp16, f32 outputs too: the size of the roundings of its own f32 sums; a
+// third term costs 5% of 700 tokens of 4096 x 256, rank 64). fp16 has few
+// exponents, so a token's u of 64 ranks is scaled by a power of two that brings
+// its largest value to their top: nothing is lost above 2^-39 of that value.
 //
 // One token of 2048 x 4096, rank 16: 9.9 us a call, 4.6 in the reading launch
 // (3.7 TB/s) and 4.7 in the joining one, whose time is latency. 48 tokens, 24
@@ -313,8 +316,11 @@ __global__ __launch_bounds__(64 * kLowWaves) void k_adapter_low(AdapterArgs a, S
 }
 
 // u of a tile's rows and 64 ranks as `PIECES` 16-bit tiles whose sum it is.
-// fp16: a row whose largest value would pass the type's range is scaled by a
-// power of two (row_scale), and its products back.
+// fp16: a row is scaled by the power of two (row_scale) that brings its largest
+// value to [2^14, 2^15), and its products back: unscaled, values above 65504
+// would be infinite, and the second term of values below 2^-3 would meet the
+// type's smallest step (a u of 1e-4 kept to 2e-4 of itself). The exponent stays
+// within 126, where the scale and its inverse are normal numbers.
 template <typename T, typename G, int PIECES>
 __device__ __forceinline__ void stage_u(const Sorted& so, int row0, int r0, uint8_t* tiles, float* row_scale) {
   typedef typename G::QT QT;
@@ -332,7 +338,7 @@ __device__ __forceinline__ void stage_u(const Sorted& so, int row0, int r0, uint
 #pragma unroll
       for (int d = 1; d < 8; d *= 2) most = fmaxf(most, __shfl_xor(most, d));
       float scale = 1.0f;
-      if (most > 32768.0f && most < INFINITY) scale = ldexpf(1.0f, 14 - ilogbf(most));
+      if (most > 0.0f && most < INFINITY) scale = ldexpf(1.0f, min(14 - ilogbf(most), 126));
       v = v * scale;
       if (r == 0) row_scale[row] = scale;   // (chunk 0 of the row, wherever it is stored)
     }
