@@ -317,7 +317,7 @@ __global__ __launch_bounds__(64 * kLowWaves) void k_adapter_low(AdapterArgs a, S
 
 // u of a tile's rows and 64 ranks as `PIECES` 16-bit tiles whose sum it is.
 // fp16: a row is scaled by the power of two (row_scale) that brings its largest
-// value to [2^14, 2^15), and its products back: unscaled, values above 65504
+// finite value to [2^14, 2^15), and its products back: unscaled, values above 65504
 // would be infinite, and the second term of values below 2^-3 would meet the
 // type's smallest step (a u of 1e-4 kept to 2e-4 of itself). The exponent stays
 // within 126, where the scale and its inverse are normal numbers.
@@ -334,11 +334,11 @@ __device__ __forceinline__ void stage_u(const Sorted& so, int row0, int r0, uint
     if constexpr (std::is_same_v<T, fp16_t>) {
       float most = 0.0f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(v[e]));
+      for (int e = 0; e < 8; ++e) most = fmaxf(most, __builtin_isinf(v[e]) ? 0.0f : fabsf(v[e]));
 #pragma unroll
       for (int d = 1; d < 8; d *= 2) most = fmaxf(most, __shfl_xor(most, d));
       float scale = 1.0f;
-      if (most > 0.0f && most < INFINITY) scale = ldexpf(1.0f, min(14 - ilogbf(most), 126));
+      if (most > 0.0f) scale = ldexpf(1.0f, min(14 - ilogbf(most), 126));
       v = v * scale;
       if (r == 0) row_scale[row] = scale;   // (chunk 0 of the row, wherever it is stored)
     }

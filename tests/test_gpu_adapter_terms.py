@@ -72,3 +72,20 @@ def test_small_values_beside_large_ones(m):
     b[:, :, 1::2] *= 2.0 ** -8
     v, tol = want(s, F32)
     assert_within(adapter.run(s, F32), v, tol, f"m {m}")
+
+
+@pytest.mark.parametrize("m", [40, 700])
+def test_large_values_beside_an_infinite_one(m):
+    """A row of A that is infinite, beside values of u past fp16's range that B meets with the other sign: the
+    infinity decides alone."""
+    s = make(m, 16, seed=m, low=2.0 ** 11)
+    x, a, b = s["x"], s["a"].view(3, 16, 264), s["b"].view(3, 136, 16)
+    x.abs_()
+    a.abs_()
+    a[:, 3] = float("inf")
+    b.copy_(-b.abs() - 2.0 ** -6)
+    b[:, :, 3] = 1.0
+    mine = s["index"] >= 0
+    assert float((x.double().cpu() @ a[0, 4].double().cpu()).min()) > 65504
+    y = adapter.run(s, F32)
+    assert (y[mine] == float("inf")).all() and not y[~mine].any()
