@@ -111,6 +111,9 @@ __device__ __forceinline__ void report(const GroupedArgs& a) {
   if (bad) atomicOr(a.status, MOE_STATUS_BAD_OFFSETS);
 }
 
+// No rows: nothing to write, but the offsets are looked at.
+__global__ __launch_bounds__(64) void k_grouped_offsets(GroupedArgs a) { report(a); }
+
 // Forward (WCOL false): in = x, out = y. Input gradient (WCOL true): in = dy, out = dx.
 template <typename T, bool WCOL, typename G>
 __global__ __launch_bounds__(G::NT, 2) void k_grouped(GroupedArgs a, const T* __restrict__ in, const T* __restrict__ w,
@@ -329,7 +332,14 @@ int grouped(Way way, const moe_grouped* g, const void* in, const void* w, const 
             void* out, int32_t* status, void* stream) {
   if (int r = check_grouped(g, rows)) return r;
   if (!offsets) return fail(MOE_EINVAL, "grouped: offsets must be non-NULL%s%lld");
-  if (way != kWeight && rows == 0) return MOE_OK;   // nothing to write
+  if (way != kWeight && rows == 0) {   // nothing to write
+    if (!status) return MOE_OK;
+    if ((uintptr_t)offsets % 4 || (uintptr_t)status % 4)
+      return fail(MOE_EINVAL, "grouped: a pointer is not aligned to its elements%s%lld");
+    k_grouped_offsets<<<dim3(1), dim3(64), 0, (hipStream_t)stream>>>(grouped_args(*g, offsets, rows, status));
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess ? MOE_OK : hip_fail(e, "grouped");
+  }
   if ((rows && !in) || ((rows || way != kWeight) && !w) || !out)
     return fail(MOE_EINVAL, "grouped: operands and output must be non-NULL%s%lld");
   const size_t es = elem_bytes(g->out_type);
