@@ -451,7 +451,7 @@ int moe_read_probe(const void* buf, uint64_t bytes, uint32_t* sink, int32_t bloc
  *   b, y       type [m][dim]
  *   w_post, w_pre  type [dim]
  *   gate       type [dim] (gate_rows 0), or [m][dim] with rows gate_stride apart
- * x_out may be x, and y may be b, in place. Rows must not overlap. Any dim
+ * x_out may be x, and y may be b, in place, with the same stride. Rows must not overlap. Any dim
  * from 1 to MOE_JOIN_MAX_DIM and any element alignment; 1 <= m < 2^22. */
 #define MOE_JOIN_MAX_DIM 16384
 typedef struct moe_join {
@@ -477,7 +477,7 @@ int moe_join_forward(const moe_join* j, const void* x, const void* b, const void
  *   db     type [m][dim], may be NULL
  *   dw_post, dw_pre  f32 [dim], may be NULL: sums over the rows
  *   dgate  f32 [dim] summed over the rows (gate_rows 0) or type [m][dim], may be NULL
- * dx may be dx_out, and db may be b, in place. Every output is written whole (nothing is added to
+ * dx may be dx_out, with the same stride, and db may be b, in place. Every output is written whole (nothing is added to
  * what was there). The sums over rows run in a fixed order: the same call
  * gives the same bits. ws: moe_join_workspace_bytes(j, m) bytes, 256-byte
  * aligned, uninitialised; not needed (NULL) where no sum over rows is asked for. */

@@ -393,6 +393,12 @@ int check_join(const moe_join* j, int64_t m) {
   return MOE_OK;
 }
 
+// In place (`out` is `in`): rows of one stride. With two strides a row would be
+// written where another one, still to be read by another workgroup, lies.
+bool other_rows(const void* in, int64_t in_stride, const void* out, int64_t out_stride, int64_t m) {
+  return out && in == out && in_stride != out_stride && m > 1;
+}
+
 // An element pointer is aligned to its element.
 bool off_element(const void* p, int type) { return (uintptr_t)p % elem_bytes(type) != 0; }
 
@@ -470,6 +476,8 @@ int moe_join_forward(const moe_join* j, const void* x, const void* b, const void
     if (off_element(p, j->type)) return fail(MOE_EINVAL, "join: a pointer is not aligned to its elements%s%lld");
   for (const void* p : {x, (const void*)x_out})
     if (off_element(p, j->residual_type)) return fail(MOE_EINVAL, "join: a pointer is not aligned to its elements%s%lld");
+  if (other_rows(x, j->x_stride, x_out, j->x_out_stride, m) || other_rows(b, j->b_stride, y, j->y_stride, m))
+    return fail(MOE_EINVAL, "join: in place with two row strides%s%lld");
   const JoinArgs a = join_args(*j, m);
   const hipStream_t s = (hipStream_t)stream;
   const bool f32 = j->residual_type == MOE_TYPE_F32;
@@ -505,6 +513,8 @@ int moe_join_backward(const moe_join* j, const void* dy, const void* dx_out, con
   if (off_element(dgate, j->gate_rows ? j->type : MOE_TYPE_F32) || off_element(dw_post, MOE_TYPE_F32) ||
       off_element(dw_pre, MOE_TYPE_F32))
     return fail(MOE_EINVAL, "join: a pointer is not aligned to its elements%s%lld");
+  if (other_rows(dx_out, j->x_out_stride, dx, j->x_stride, m))
+    return fail(MOE_EINVAL, "join: in place with two row strides%s%lld");
   float* dgate_sum = j->gate_rows ? nullptr : (float*)dgate;
   const int sums = dw_pre || dw_post || dgate_sum;
   if (sums) {
