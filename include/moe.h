@@ -496,13 +496,14 @@ int moe_join_backward(const moe_join* j, const void* dy, const void* dx_out, con
  *   x, dx  [rows][k]   y, dy  [rows][n]   w, dw  [n_groups][n][k]
  * Inputs have `type`, the output `out_type`. Every output is written whole:
  * rows of no group (before offsets[0], after offsets[n_groups]) and the dW of
- * empty groups are 0. rows may be 0. Outputs must not overlap inputs. Any n,
+ * empty groups are 0. rows may be 0, and is at most MOE_GROUPED_MAX_ROWS. Outputs must not overlap inputs. Any n,
  * k >= 1, stride and element alignment; rows whose start is 16-byte aligned
  * (and widths that are multiples of 8) take the faster path. The same call
  * gives the same bits. status: MOE_STATUS_BAD_OFFSETS, may be NULL; outputs
  * are unspecified then. */
 #define MOE_GROUPED_MAX_GROUPS 1024
 #define MOE_GROUPED_MAX_STRIDE (1 << 22)
+#define MOE_GROUPED_MAX_ROWS 0x7fffff00
 typedef struct moe_grouped {
   int32_t n_groups, n, k;
   int32_t type;            /* MOE_TYPE_BF16 or MOE_TYPE_FP16              */

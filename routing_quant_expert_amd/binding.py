@@ -339,6 +339,7 @@ MOE_STATUS_BAD_ADAPTER = 16
 MOE_JOIN_MAX_DIM = 16384
 MOE_GROUPED_MAX_GROUPS = 1024
 MOE_GROUPED_MAX_STRIDE = 1 << 22
+MOE_GROUPED_MAX_ROWS = 0x7fffff00
 MOE_ADAPTER_MAX_ADAPTERS = 1024
 MOE_ADAPTER_MAX_RANK = 1024
 MOE_ADAPTER_MAX_TOKENS = 1 << 20

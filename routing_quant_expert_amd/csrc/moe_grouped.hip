@@ -229,7 +229,8 @@ int check_grouped(const moe_grouped* g, int64_t rows) {
       g->w_stride > MOE_GROUPED_MAX_STRIDE)
     return fail(MOE_EUNSUPPORTED, "grouped: a row stride above MOE_GROUPED_MAX_STRIDE%s%lld");
   if (rows < 0) return fail(MOE_EINVAL, "grouped: rows must be >= 0%s (%lld)", "", rows);
-  if (rows > INT32_MAX) return fail(MOE_EUNSUPPORTED, "grouped: rows above 2^31 - 1%s (%lld)", "", rows);
+  if (rows > MOE_GROUPED_MAX_ROWS)   // (row numbers rounded up to a tile or a step stay within 32 bits)
+    return fail(MOE_EUNSUPPORTED, "grouped: rows above MOE_GROUPED_MAX_ROWS%s (%lld)", "", rows);
   return MOE_OK;
 }
 
