@@ -130,7 +130,10 @@ def _stream(stream):
     if stream is None:
         # the current device's current stream, without the Stream object that torch.cuda.current_stream() makes (3 us)
         import torch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        try:
+            return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        except AttributeError:   # (a torch without that entry)
+            return torch.cuda.current_stream().cuda_stream
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
