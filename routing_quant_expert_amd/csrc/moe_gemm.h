@@ -27,6 +27,7 @@
 #include "moe_element.h"
 #include "moe_internal.h"
 #include "moe_kquant.h"
+#include "moe_once.h"
 #include "moe_wave.h"
 
 namespace moe {
@@ -655,10 +656,14 @@ inline bool rows16(const void* p, int64_t stride) { return ((uintptr_t)p & 15) =
 // `blocks` workgroups of Kernel with `lds` bytes of dynamic LDS.
 template <auto Kernel, typename... A>
 int launch_tiles(const char* what, dim3 blocks, int threads, int lds, hipStream_t s, A... args) {
-  static const hipError_t attr = hipFuncSetAttribute((const void*)Kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-  if (attr != hipSuccess) return hip_fail(attr, what);
+  static OncePerDevice attr;   // (a kernel's dynamic LDS is the same in every call)
+  int device = 0;
+  hipError_t e = hipGetDevice(&device);
+  if (e == hipSuccess)
+    e = attr(device, [&] { return hipFuncSetAttribute((const void*)Kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds); });
+  if (e != hipSuccess) return hip_fail(e, what);
   Kernel<<<blocks, dim3(threads), lds, s>>>(args...);
-  const hipError_t e = hipGetLastError();
+  e = hipGetLastError();
   return e == hipSuccess ? MOE_OK : hip_fail(e, what);
 }
 
