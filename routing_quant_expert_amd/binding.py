@@ -1,7 +1,9 @@
-"""ctypes binding of libmoe.so (include/moe.h). Argument marshalling only:
-device tensors are passed as raw pointers with the caller's current HIP
-stream; every computation runs in the library's kernels. There is no
-fallback: if the library is missing the import of a call fails loudly."""
+"""Binding of libmoe.so (include/moe.h). Argument marshalling only: device
+tensors are passed as raw pointers with the caller's current HIP stream; every
+computation runs in the library's kernels. The layer's calls go through
+ctypes; those of the operators beside it through _tensors.so, which refuses
+tensors that do not fit the call's description. There is no fallback: if a
+library is missing the import of a call fails loudly."""
 from __future__ import annotations
 
 import ctypes
@@ -11,6 +13,7 @@ import numpy as np
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmoe.so")
+TENSORS_PATH = os.path.join(HERE, "_tensors.so")
 
 MOE_STATUS_MISS = 1
 MOE_STATUS_NAN_KEY = 2
@@ -363,6 +366,27 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+_native = None
+
+
+def _tensors():
+    """The native module that holds these calls' tensors against their description and makes the calls
+    (csrc/moe_tensors.cpp)."""
+    global _native
+    if _native is None:
+        L = lib()
+        import torch  # noqa: F401  (its libraries are the module's)
+        try:
+            from . import _tensors as native
+        except ImportError as e:
+            raise ImportError(f"{TENSORS_PATH} is not built: run __graft_entry__.build()") from e
+        native.bind(MoeError, *(ctypes.cast(f, _VP).value for f in (
+            L.moe_join_forward, L.moe_join_backward, L.moe_grouped_forward, L.moe_grouped_backward_x,
+            L.moe_grouped_backward_w, L.moe_adapter_project, L.moe_last_error)))
+        _native = native
+    return _native
+
+
 class Join(ctypes.Structure):
     """moe_join: how a block joins a residual stream (norms after and before, gate, residual scale).
     Strides default to contiguous rows of dim."""
@@ -382,8 +406,7 @@ class Join(ctypes.Structure):
 def join_forward(j: Join, x, block, w_post, gate, w_pre, x_out, y, stream=None):
     """x_out = x + scale * gate * norm(block, w_post), y = norm(x_out, w_pre); block, w_post, gate, w_pre with y,
     and (without a block) x_out may be None."""
-    _check(lib().moe_join_forward(ctypes.byref(j), _addr(x), _addr(block), _addr(w_post), _addr(gate), _addr(w_pre),
-                                  x.shape[0], _addr(x_out), _addr(y), _stream(stream)))
+    _tensors().join_forward(j, x, block, w_post, gate, w_pre, x_out, y, _stream(stream))
 
 
 def join_workspace_bytes(j: Join, max_m: int) -> int:
@@ -393,10 +416,8 @@ def join_workspace_bytes(j: Join, max_m: int) -> int:
 def join_backward(j: Join, dy, dx_out, x_out, block, w_post, gate, w_pre, dx, dblock, dw_post, dgate, dw_pre, ws,
                   stream=None):
     """The gradients of join_forward: dx, dblock, dw_post, dgate, dw_pre (None where not wanted)."""
-    _check(lib().moe_join_backward(ctypes.byref(j), _addr(dy), _addr(dx_out), _addr(x_out), _addr(block),
-                                   _addr(w_post), _addr(gate), _addr(w_pre), dx.shape[0], _addr(dx), _addr(dblock),
-                                   _addr(dw_post), _addr(dgate), _addr(dw_pre), _addr(ws),
-                                   0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
+    _tensors().join_backward(j, dy, dx_out, x_out, block, w_post, gate, w_pre, dx, dblock, dw_post, dgate, dw_pre, ws,
+                             _stream(stream))
 
 
 class Grouped(ctypes.Structure):
@@ -416,20 +437,17 @@ class Grouped(ctypes.Structure):
 
 def grouped_forward(g: Grouped, x, w, offsets, y, status=None, stream=None):
     """y[r] = w[group of r] @ x[r]; offsets: int32 [n_groups + 1] on the device."""
-    _check(lib().moe_grouped_forward(ctypes.byref(g), _addr(x), _addr(w), _addr(offsets), x.shape[0], _addr(y),
-                                     _addr(status), _stream(stream)))
+    _tensors().grouped_forward(g, x, w, offsets, y, status, _stream(stream))
 
 
 def grouped_backward_x(g: Grouped, dy, w, offsets, dx, status=None, stream=None):
     """dx[r] = w[group of r]^T @ dy[r]."""
-    _check(lib().moe_grouped_backward_x(ctypes.byref(g), _addr(dy), _addr(w), _addr(offsets), dy.shape[0], _addr(dx),
-                                        _addr(status), _stream(stream)))
+    _tensors().grouped_backward_x(g, dy, w, offsets, dx, status, _stream(stream))
 
 
 def grouped_backward_w(g: Grouped, dy, x, offsets, dw, status=None, stream=None):
     """dw[g] = the sum of dy[r] x[r]^T over the group's rows."""
-    _check(lib().moe_grouped_backward_w(ctypes.byref(g), _addr(dy), _addr(x), _addr(offsets), dy.shape[0], _addr(dw),
-                                        _addr(status), _stream(stream)))
+    _tensors().grouped_backward_w(g, dy, x, offsets, dw, status, _stream(stream))
 
 
 class Adapters(ctypes.Structure):
@@ -465,6 +483,4 @@ def adapter_workspace_bytes(p: Adapters, max_m: int) -> int:
 
 def adapter_project(p: Adapters, x, w, index, out, ws, status=None, stream=None):
     """out[t] = w @ x[t] + factor[a] * b[a] @ (a[a] @ x[t]) with a = index[t] (-1: w @ x[t] alone)."""
-    _check(lib().moe_adapter_project(ctypes.byref(p), _addr(x), _addr(w), _addr(index), x.shape[0], _addr(out),
-                                     _addr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _addr(status),
-                                     _stream(stream)))
+    _tensors().adapter_project(p, x, w, index, out, ws, status, _stream(stream))

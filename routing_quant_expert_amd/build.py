@@ -1,8 +1,11 @@
-"""Builds libmoe.so (the HIP library, gfx950) and the device input generator
-libsynth.so with hipcc, in-tree."""
+"""Builds libmoe.so (the HIP library, gfx950), the device input generator
+libsynth.so with hipcc and the tensor binding _tensors.so with the host
+compiler, in-tree."""
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -10,6 +13,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libmoe.so")
+TENSORS_SRC = os.path.join(CSRC, "moe_tensors.cpp")
+TENSORS_LIB = os.path.join(HERE, "_tensors.so")
 SYNTH_SRC = os.path.join(ROOT, "synth", "synth_device.hip")
 SYNTH_LIB = os.path.join(ROOT, "synth", "libsynth.so")
 
@@ -38,6 +43,14 @@ def _run(cmd, verbose):
     return r
 
 
+def _tensors_command(out: str) -> list:
+    """The host compiler's call for the tensor binding: this Python, and the torch that it imports."""
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+            "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(torch, "include"), TENSORS_SRC,
+            "-o", out, "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+
+
 def build(verbose: bool = False, jobs: int = 4) -> str:
     os.makedirs(BUILD, exist_ok=True)
     objs = []
@@ -48,6 +61,7 @@ def build(verbose: bool = False, jobs: int = 4) -> str:
         cmds.append([HIPCC, *FLAGS, *EXTRA.get(src, []), "-c", os.path.join(CSRC, src), "-o", obj])
     synth_obj = os.path.join(BUILD, "synth_device.o")
     cmds.append([HIPCC, *FLAGS, "-c", SYNTH_SRC, "-o", synth_obj])
+    cmds.append(_tensors_command(TENSORS_LIB + ".tmp"))
     with ThreadPoolExecutor(max_workers=jobs) as ex:
         list(ex.map(lambda c: _run(c, verbose), cmds))
     tmp = LIB + ".tmp"
@@ -56,6 +70,7 @@ def build(verbose: bool = False, jobs: int = 4) -> str:
     tmp = SYNTH_LIB + ".tmp"
     _run([HIPCC, "-shared", f"--offload-arch={ARCH}", synth_obj, "-o", tmp], verbose)
     os.replace(tmp, SYNTH_LIB)
+    os.replace(TENSORS_LIB + ".tmp", TENSORS_LIB)
     return LIB
 
 
