@@ -19,11 +19,13 @@
 // exponents, so a token's u of 64 ranks is scaled by a power of two that brings
 // its largest value to their top: nothing is lost above 2^-39 of that value.
 //
-// One token of 2048 x 4096, rank 16: 9.9 us a call, 4.6 in the reading launch
-// (3.7 TB/s) and 4.7 in the joining one, whose time is latency. 48 tokens, 24
-// adapters of rank 32: 12.4 us. 4096 tokens of 4096 x 2048, rank 64: 95 us (751
-// TFLOP/s): sort 7.5, u 13 (reading A again for every 16 tokens), tiles 78,
-// where the plain product alone takes a library 52.
+// One token of 2048 x 4096, rank 16: 9.8 us a call, 4.5 in the reading launch
+// (3.7 TB/s) and 4.9 in the joining one, whose time is latency. Workgroups of
+// adapters that no token uses end at once, but are launched: 16.8 us beside 1024
+// adapters. 48 tokens, 24 adapters of rank 32: 12.4 us. 4096 tokens of 4096 x
+// 2048, rank 64: 93 to 98 us (730 to 770 TFLOP/s): sort 7 (in one workgroup), u
+// 13 (reading A again for every 16 tokens), tiles 79, where the plain product
+// alone takes a library 52.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -528,7 +530,7 @@ int launch_many(const AdapterArgs& a, const T* x, const T* w, const T* wa, const
   e = hipGetLastError();
   if (e != hipSuccess) return hip_fail(e, "adapters");
   // Tiles by their number, as for the grouped products: 64 x 64 where larger ones would leave CUs idle (1000 tokens of
-  // 1024 x 1024: 19 us), 256 x 128 from three a CU on with long sums (at two a CU, 4096 tokens of 4096 x 2048: 101.6 us against 99.8).
+  // 1024 x 1024: 19 us), 256 x 128 from three a CU on with long sums (at two a CU, 4096 tokens of 4096 x 2048: 95 us of either).
   const int64_t rows = (a.m + 127) / 128;
   if (rows * ((a.n + 127) / 128) < 256)
     return launch_main<T, Gemm<T, false, false, 64, 64, 2, 2, 4, DMA, true>>(a, so, x, w, wb, out, s);

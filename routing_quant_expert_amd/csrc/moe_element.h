@@ -13,15 +13,6 @@ namespace moe {
 typedef __bf16 bf16_t;
 typedef _Float16 fp16_t;
 
-template <typename T>
-struct elem_code;
-template <>
-struct elem_code<bf16_t> { static constexpr int value = MOE_TYPE_BF16; };
-template <>
-struct elem_code<fp16_t> { static constexpr int value = MOE_TYPE_FP16; };
-template <>
-struct elem_code<float> { static constexpr int value = MOE_TYPE_F32; };
-
 inline size_t elem_bytes(int type) { return type == MOE_TYPE_F32 ? 4 : 2; }
 
 typedef float f32x8 __attribute__((ext_vector_type(8)));

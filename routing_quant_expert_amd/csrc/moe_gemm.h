@@ -35,7 +35,6 @@ namespace moe {
 constexpr int kStep = 64;   // r per step
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef int32_t i32x4g __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4* lds_tr_t;
 

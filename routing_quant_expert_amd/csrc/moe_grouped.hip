@@ -6,12 +6,13 @@
 //   weight   dW[g] = sum over g's rows dy[r] x[r]^T  P = x columns, Q = dy columns
 //
 // Few rows a group: bound by HBM, every used weight is read once (48 rows over
-// 384 groups of 2048 x 4096: 134 us, 6.0 TB/s; 12288 rows: 1119 us, 5.9 TB/s).
+// 384 groups of 2048 x 4096: 135 us, 6.0 TB/s; 12288 rows: 1120 us, 5.9 TB/s).
 // Many: by the matrix instructions and what the ragged groups leave of them
-// (input gradient of 16384 rows over 32 groups of 4096 x 2048: 337 us, 815
-// TFLOP/s; four even groups of 4096 x 4096: 1150 TFLOP/s; a library product of
-// this size class reaches 1355 to 1450 on even sizes). The weight gradient of
-// the same rows writes 1.07 GB in f32: 546 us, 341 without its stores.
+// (16384 rows over 32 groups of 4096 x 2048: input gradient 335 to 353 us from
+// card to card, 780 to 820 TFLOP/s, forward 333; four even groups of 4096 x
+// 4096: 1150 TFLOP/s; a library product of this size class reaches 1355 to 1450
+// on even sizes). The weight gradient of the same rows writes 1.07 GB in f32:
+// 546 to 555 us, 341 without its stores.
 //
 // The offsets stay on the device: the grid is an upper bound of the tiles (a
 // group adds at most one partial tile), every wave finds its tile from the
@@ -261,6 +262,8 @@ int launch_rows(const GroupedArgs& a, const void* in, const void* w, void* out, 
 
 template <typename T, bool WCOL, bool DMA>
 int launch_rows_as(const GroupedArgs& a, const void* in, const void* w, void* out, hipStream_t s) {
+  // (The offsets are on the device: the tile goes by the mean of the groups. Where few groups have most of the rows
+  // it is too small: 5000 rows, all but 800 in one of 384 groups of 2048 x 4096, take 339 us in tiles of 16 rows, 166 of 64.)
   const int64_t mean = a.rows / a.groups;
   const int width = WCOL ? a.k : a.n;
   if (mean < 16) return launch_rows<T, WCOL, Gemm<T, WCOL, false, 128, 16, 4, 1, 4, DMA>>(a, in, w, out, s);
@@ -273,8 +276,8 @@ int launch_rows_as(const GroupedArgs& a, const void* in, const void* w, void* ou
   if constexpr (DMA) {
     // One workgroup a CU with a third step in flight, where there are three
     // tiles a CU and sums long enough for its fill and drain; otherwise two
-    // workgroups a CU. Input gradient of 16384 rows over 32 groups of 4096 x
-    // 2048: 320 us against 330; forward of 8000 over 16 of 4096 x 512: 72 against 61.
+    // workgroups a CU. 16384 rows over 32 groups of 4096 x 2048: forward 333 us
+    // against 342, input gradient 337 against 341; forward of 8000 over 16 of 4096 x 512: 69 against 63.
     const int red = WCOL ? a.n : a.k;
     if (row_tiles(a, 128) * ((width + 255) / 256) >= 768 && red >= 1024)
       return launch_rows<T, WCOL, Gemm<T, WCOL, false, 256, 128, 4, 2, 3, DMA>>(a, in, w, out, s);
@@ -308,7 +311,7 @@ int launch_dw_ring(const GroupedArgs& a, int at_once, const void* dy, const void
 template <typename T>
 int launch_dw_aligned(const GroupedArgs& a, const void* dy, const void* x, void* dw, hipStream_t s) {
   // Four tiles a CU and more: the larger tile, one workgroup a CU with a third step in flight. 16384 rows over 32
-  // groups of 4096 x 2048 (16384 small tiles): 565 us against 640; 4000 over 8 of 512 x 1024 (256): 24 against 18.
+  // groups of 4096 x 2048 (16384 small tiles): 551 us against 612; 4000 over 8 of 512 x 1024 (256): 21 against 16.
   const int64_t tiles = (int64_t)((a.k + 255) / 256) * ((a.n + 127) / 128) * a.groups;
   if (tiles >= 1024) return launch_dw_ring<T, Gemm<T, true, true, 256, 128, 4, 2, 3, true>>(a, 256, dy, x, dw, s);
   return launch_dw_ring<T, Gemm<T, true, true, 128, 128, 2, 2, 2, true>>(a, 512, dy, x, dw, s);

@@ -9,9 +9,11 @@
 //
 // Bound by HBM: every operand is read once and every result written once, the
 // row stays in registers in between (8192 rows of 4096, f32 stream: forward 75
-// us, 5.4 TB/s, gradients 118 us, 5.1 TB/s; a copy reaches 5.1). 4096 rows in
+// us, 5.4 TB/s, gradients 120 us, 5.0 TB/s; a copy reaches 5.1). 4096 rows in
 // 16 bits, gradients: 51 us, 3.9 TB/s, of which the column sums take 4. One
-// row of 4096: 3.8 us in the kernel, 5.3 with the call. A row belongs to TPR threads (one wave,
+// row of 4096: 3.8 us in the kernel, 4.6 with the call. Gradients of rows wider
+// than 8192 are read twice and do not fit the registers (k_join_back): 1500
+// rows of 16384 take 223 us, 1.3 TB/s, where the forward pass takes 46. A row belongs to TPR threads (one wave,
 // or a workgroup), thread t holding the chunks t, t + TPR, ... of 8 elements
 // (the last one short where the row is no multiple of 8).
 #include <hip/hip_runtime.h>
@@ -180,9 +182,13 @@ __global__ __launch_bounds__(TPR < kJoinThreads ? kJoinThreads : TPR) void k_joi
 // The gradients: workgroup p takes the rows p, p + P, ... (P workgroups), so
 // that its threads keep the sums over rows of their columns in registers; they
 // are written as f32 partial sums [P][3][dim] that k_join_sums adds up.
-// Registers permitting, the vectors and the row stay in them (workgroups of up
-// to 512 threads; otherwise they are read again where they are used, from the
-// caches), and the next two rows are on their way while one is worked on (NC = 1).
+// The vectors and the row stay in registers in workgroups of up to 512 threads
+// (dim <= 8192), and the next two rows are on their way while one is worked on
+// where NC is 1 (dim <= 4096). Wider rows are read again where they are used,
+// from the caches: 1024 threads have 128 registers each, of which the sums of
+// two chunks take 48, and the compiler still keeps 132 to 155 of a thread's
+// values in scratch memory, as it does 64 of f32 streams of odd widths from
+// 4097 to 8191 (1500 rows: 82 us of 8191, 52 of 8192).
 //
 // One reduction a row: with d = dy w_pre and h = gate w_post b, the sum that
 // db needs, of dz w_post nb, is s rb (sum h dx_out + rx (sum h d - c1 sum h x')),
@@ -364,8 +370,9 @@ __global__ __launch_bounds__(1024) void k_join_sums(const float* __restrict__ pa
 
 // Workgroups of the gradient kernel for m rows: as many as run at once (its
 // registers leave 8 waves a CU), but at least 4 rows each where that still gives one a CU: a workgroup's
-// partial sums cost as much traffic as a row. 8192 rows of 512: 31 us with
-// 512 workgroups, 51 with 256; 4096 rows of 4096: 61 with 512, 58 with 256.
+// partial sums cost as much traffic as a row. 8192 rows of 512: 24 us with 1024
+// workgroups, 31 with 512, 48 with 256; of 2048: 50 with 512, 60 with 256; 4096
+// rows of 4096: 59 with 512, 52 with 256.
 int join_parts(int dim, int64_t m) {
   const int64_t at_once = dim <= 1024 ? 1024 : dim <= 2048 ? 512 : 256;
   const int64_t fed = m / 4 > 256 ? m / 4 : 256;
