@@ -287,7 +287,10 @@ int grouped(PyObject* const* a) {
 // The adapters' own tensors, which the description keeps beside their addresses.
 void kept_on_device(PyObject* plan) {
   PyObject* kept = PyObject_GetAttrString(plan, "_kept");
-  if (!kept) throw PythonError();
+  if (!kept) {   // (a description that was copied or filled in by hand)
+    PyErr_Clear();
+    return;
+  }
   const Py_ssize_t n = PyTuple_Check(kept) ? PyTuple_GET_SIZE(kept) : 0;
   bool there = true;
   for (Py_ssize_t i = 0; i < n; ++i) {

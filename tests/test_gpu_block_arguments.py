@@ -77,3 +77,15 @@ def test_adapters_on_the_host():
         refused(lambda: R.adapter_project(q, x, w, index, out, ws), "not on the device")
     refused(lambda: R.adapter_project(p, x, w, index, out, ws.cpu()), "not on the device")
     refused(lambda: R.adapter_project(p, x, w, index.long(), out, ws), "must be int32")
+
+
+def test_a_copied_description():
+    m, n, k, rank = 5, 32, 64, 8
+    x, w, a, b = rnd(m, k), rnd(n, k, seed=1), rnd(2, rank, k, seed=2), rnd(2, n, rank, seed=3)
+    index = torch.tensor([0, 1, -1, 0, 1], dtype=torch.int32, device="cuda")
+    p = R.Adapters(a, b)
+    ws = torch.empty(R.adapter_workspace_bytes(p, m), dtype=torch.uint8, device="cuda")
+    out, again = (torch.empty(m, n, dtype=BF16, device="cuda") for _ in range(2))
+    R.adapter_project(p, x, w, index, out, ws)
+    R.adapter_project(R.Adapters.from_buffer_copy(p), x, w, index, again, ws)
+    assert torch.equal(out, again)
