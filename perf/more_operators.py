@@ -1,0 +1,426 @@
+"""The experts' feed-forward operators as they are measured: their cases, their
+inputs, their plain forms in elementary torch operations, and their definitions
+in 64 bits.
+
+  gated     h = act(Wg x) * (Wu x), grouped by expert: forward and what the
+            hidden row's and the input row's gradients need
+  mx rows   rows to microscaled 4-bit floats (32 elements share a power of two) and back
+  mx        products grouped by expert with both operands in that format, plain and gated
+
+`run` computes the plain form where `own` is false and calls the library where
+it is true. Inputs depend on the case and the seed alone.
+"""
+import math
+import random
+
+import torch
+
+own = False
+
+_TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "f32": torch.float32}
+_LIMIT = 7.0   # the layer's clamp of the gated activation
+
+
+def listed():
+    return [
+        # 8 decoded tokens with 6 picks each: 48 rows over 384 experts, most groups empty
+        {"name": "gated 48 of 384", "op": "gated", "groups": 384, "rows": 48, "n": 2048, "k": 4096, "skew": 0.3,
+         "act": "silu", "limit": _LIMIT, "kept": False, "type": "bf16"},
+        # a training batch on the experts of one rank, what the backward pass reads kept
+        {"name": "gated 16384 of 32", "op": "gated", "groups": 32, "rows": 16384, "n": 2048, "k": 4096, "skew": 0.4,
+         "act": "silu", "limit": _LIMIT, "kept": True, "type": "bf16"},
+        # its backward pass through the down projection and the activation, the hidden row made again
+        {"name": "gated dh 16384 of 32", "op": "gated dh", "groups": 32, "rows": 16384, "n": 2048, "k": 4096,
+         "skew": 0.4, "act": "silu", "limit": _LIMIT, "again": True, "type": "bf16"},
+        # a small layer with odd widths: rows that start at odd addresses
+        {"name": "gated dh 1000 odd", "op": "gated dh", "groups": 13, "rows": 1000, "n": 257, "k": 515, "skew": 0.8,
+         "act": "gelu", "limit": 0.0, "again": False, "type": "fp16"},
+        # and through both projections into the input's gradient
+        {"name": "gated dx 16384 of 32", "op": "gated dx", "groups": 32, "rows": 16384, "n": 2048, "k": 4096,
+         "skew": 0.4, "out": "bf16", "type": "bf16"},
+        {"name": "gated dx 1000 odd", "op": "gated dx", "groups": 13, "rows": 1000, "n": 257, "k": 515, "skew": 0.8,
+         "out": "f32", "type": "fp16"},
+        # one decoded token's row to 4 bits and back: the cost of two calls
+        {"name": "mx rows 1x4096", "op": "mx rows", "rows": 1, "k": 4096, "scale": "floor", "type": "bf16"},
+        # the weights of 32 experts as they are converted
+        {"name": "mx rows 65536x4096", "op": "mx rows", "rows": 65536, "k": 4096, "scale": "ceil", "type": "bf16"},
+        # a decode batch over the whole layer: what counts is the weights' 4 bits
+        {"name": "mx gated 48 of 384", "op": "mx gated", "groups": 384, "rows": 48, "n": 2048, "k": 4096, "skew": 0.3,
+         "act": "silu", "limit": _LIMIT, "out": "bf16"},
+        # a 2048-token prompt with 6 picks each over all experts
+        {"name": "mx gated 12288 of 384", "op": "mx gated", "groups": 384, "rows": 12288, "n": 2048, "k": 4096,
+         "skew": 0.5, "act": "silu", "limit": _LIMIT, "out": "bf16"},
+        # a long prompt on the experts of one rank, through the down projection
+        {"name": "mx 16384 of 32", "op": "mx", "groups": 32, "rows": 16384, "n": 4096, "k": 2048, "skew": 0.4,
+         "out": "bf16"},
+        # a small layer whose width no block of 32 divides
+        {"name": "mx 1000 odd", "op": "mx", "groups": 13, "rows": 1000, "n": 257, "k": 515, "skew": 0.8,
+         "out": "f32"},
+    ]
+
+
+def _spread(rng, lo, hi):
+    """A whole number of [lo, hi], evenly over its logarithm."""
+    return max(lo, min(hi, round(math.exp(rng.uniform(math.log(lo), math.log(hi))))))
+
+
+def _width(rng, lo, hi):
+    """A width: mostly multiples of 64 as models have them, sometimes any number."""
+    v = _spread(rng, lo, hi)
+    return max(64, 64 * round(v / 64)) if rng.random() < 0.75 else v
+
+
+def draw(rng):
+    op = rng.choice(["gated", "gated dh", "gated dx", "mx rows", "mx", "mx gated"])
+    t = rng.choice(["bf16", "fp16"])
+    if op == "mx rows":
+        return {"op": op, "rows": _spread(rng, 1, 32768), "k": _width(rng, 64, 4096),
+                "scale": rng.choice(["floor", "ceil"]), "type": rng.choice([t, t, "f32"])}
+    c = {"op": op, "groups": _spread(rng, 1, 128), "rows": _spread(rng, 1, 12000), "n": _width(rng, 64, 2048),
+         "k": _width(rng, 64, 4096), "skew": round(rng.uniform(0.0, 1.0), 2)}
+    if op in ("gated", "gated dh", "mx gated"):
+        c["act"] = rng.choice(["silu", "silu", "gelu"])
+        c["limit"] = rng.choice([_LIMIT, 0.0, 1.5])
+    if op.startswith("gated"):
+        c["type"] = t
+    if op == "gated":
+        c["kept"] = rng.random() < 0.5
+    elif op == "gated dh":
+        c["again"] = rng.random() < 0.5
+    elif op == "gated dx":
+        c["out"] = rng.choice([t, t, "f32"])
+    else:
+        c["out"] = rng.choice([t, t, "f32"])
+    return c
+
+
+def _sizes(rows, groups, skew):
+    """Rows of each group, largest first: group i's share falls as (i + 1)^-skew."""
+    w = [(i + 1.0) ** -skew for i in range(groups)]
+    sizes = [int(rows * v / sum(w)) for v in w]
+    for i in range(rows - sum(sizes)):
+        sizes[i % groups] += 1
+    return sizes
+
+
+def _row_sizes(case, seed):
+    """The groups' sizes in the seed's order."""
+    sizes = _sizes(case["rows"], case["groups"], case["skew"])
+    random.Random(seed).shuffle(sizes)
+    return sizes
+
+
+def _normal(gen, shape, dtype, sigma=1.0):
+    return torch.randn(shape, generator=gen, device="cuda", dtype=dtype).mul_(sigma)
+
+
+# ---- microscaled 4-bit floats in elementary operations ------------------------------------
+_STEPS = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+
+
+def _to_mx(v, rule):
+    """f32 [rows, k] -> codes uint8 [rows, ceil(k / 2)], the even element in the low half, and scales uint8
+    [rows, ceil(k / 32)], exponents from -127 on."""
+    rows, k = v.shape
+    blocks = -(-k // 32)
+    b = torch.zeros((rows, blocks * 32), dtype=torch.float32, device=v.device)
+    b[:, :k] = v
+    b = b.view(rows, blocks, 32)
+    size = b.abs()
+    top = size.amax(-1)
+    part, power = torch.frexp(top)   # top = part 2^power, part in [1/2, 1)
+    e = power - 3
+    if rule == "ceil":
+        e = e + (part > 0.75)
+    e = torch.where(top > 0, e, -127).clamp(min=-127)
+    a = torch.ldexp(size, -e[:, :, None])
+    code = ((a > 0.25).to(torch.uint8) + (a >= 0.75) + (a > 1.25) + (a >= 1.75) + (a > 2.5) + (a >= 3.5) + (a > 5))
+    code = (code + 8 * (b < 0)).view(rows, -1)
+    return code[:, 0::2][:, :-(-k // 2)] + 16 * code[:, 1::2][:, :-(-k // 2)], (e + 127).to(torch.uint8)
+
+
+def _from_mx(codes, scales, k):
+    """The values that codes and scales stand for, in f32 [..., k]."""
+    steps = torch.tensor(_STEPS + tuple(-v for v in _STEPS), dtype=torch.float32, device=codes.device)
+    v = torch.stack([codes & 15, codes >> 4], -1).flatten(-2)[..., :k]
+    return steps[v.int()] * torch.exp2(scales.float() - 127).repeat_interleave(32, -1)[..., :k]
+
+
+def _mx_weights(gen, groups, n, k):
+    """Normal weights in 4 bits, as a checkpoint holds them, some groups at a time."""
+    codes = torch.empty((groups, n, (k + 1) // 2), dtype=torch.uint8, device="cuda")
+    scales = torch.empty((groups, n, (k + 31) // 32), dtype=torch.uint8, device="cuda")
+    some = max(1, (1 << 26) // (n * k))
+    for a in range(0, groups, some):
+        b = min(groups, a + some)
+        c, s = _to_mx(_normal(gen, ((b - a) * n, k), torch.float32, 0.02), "floor")
+        codes[a:b], scales[a:b] = c.view(b - a, n, -1), s.view(b - a, n, -1)
+    return codes, scales
+
+
+# ---- inputs ---------------------------------------------------------------------------------
+def _inputs(case, seed):
+    gen, op = torch.Generator(device="cuda").manual_seed(int(seed) * 7919 + 29), case["op"]
+    if op == "mx rows":
+        return {"x": _normal(gen, (case["rows"], case["k"]), _TYPES[case["type"]], 0.7)}
+    n, k, rows, groups, sizes = case["n"], case["k"], case["rows"], case["groups"], _row_sizes(case, seed)
+    bounds = [0]
+    for v in sizes:
+        bounds.append(bounds[-1] + v)
+    s = {"offsets": torch.tensor(bounds, dtype=torch.int32, device="cuda"), "most": max(sizes)}
+    if op.startswith("mx"):
+        s["x"] = _to_mx(_normal(gen, (rows, k), torch.float32), "floor")
+        s["w"] = [_mx_weights(gen, groups, n, k) for _ in range(2 if op == "mx gated" else 1)]
+        return s
+    t = _TYPES[case["type"]]
+    if op == "gated dh":
+        s["dy"] = _normal(gen, (rows, k), t)
+        s["w_down"] = _normal(gen, (groups, k, n), t, 0.02)
+        s["gate"], s["up"] = (_normal(gen, (rows, n), t, 1.3) for _ in range(2))
+        return s
+    s["w_gate"], s["w_up"] = (_normal(gen, (groups, n, k), t, 0.02) for _ in range(2))
+    if op == "gated":
+        s["x"] = _normal(gen, (rows, k), t)
+    else:
+        s["dgate"], s["dup"] = (_normal(gen, (rows, n), t) for _ in range(2))
+    return s
+
+
+def _handles(case):
+    """What a program that uses the library keeps: the description of the call and its output buffers."""
+    import routing_quant_expert_amd as R
+
+    def like(shape, dtype):
+        return torch.empty(shape, dtype=dtype, device="cuda")
+
+    op, rows, k = case["op"], case["rows"], case["k"]
+    if op == "mx rows":
+        t = _TYPES[case["type"]]
+        return {"plan": R.MxRows(k, t, scale=case["scale"]), "codes": like((rows, (k + 1) // 2), torch.uint8),
+                "scales": like((rows, (k + 31) // 32), torch.uint8), "values": like((rows, k), t)}
+    n, groups = case["n"], case["groups"]
+    if op.startswith("mx"):
+        out = _TYPES[case["out"]]
+        act = {"act": case["act"], "limit": case["limit"]} if op == "mx gated" else {}
+        return {"plan": R.Mx(groups, n, k, out, **act), "out": like((rows, n), out)}
+    t = _TYPES[case["type"]]
+    if op == "gated dx":
+        out = _TYPES[case["out"]]
+        return {"plan": R.Gated(groups, n, k, t, dx=out), "dx": like((rows, k), out)}
+    h = {"plan": R.Gated(groups, n, k, t, act=case["act"], limit=case["limit"]), "h": None}
+    if op == "gated":
+        h["h"] = like((rows, n), t)
+        h["gate"], h["up"] = (like((rows, n), t) if case["kept"] else None for _ in range(2))
+        return h
+    if case["again"]:
+        h["h"] = like((rows, n), t)
+    h["dgate"], h["dup"] = (like((rows, n), t) for _ in range(2))
+    return h
+
+
+def prepare(case, seed):
+    s = _inputs(case, seed)
+    s["case"] = case
+    if own:
+        s.update(_handles(case))
+    return s
+
+
+# ---- the library's calls ----------------------------------------------------------------------
+def _run_own(s):
+    import routing_quant_expert_amd as R
+
+    op = s["case"]["op"]
+    if op == "gated":
+        R.gated_forward(s["plan"], s["x"], s["w_gate"], s["w_up"], s["offsets"], s["h"], s["gate"], s["up"])
+        return {key: s[key] for key in ("h", "gate", "up") if s[key] is not None}
+    if op == "gated dh":
+        R.gated_backward_h(s["plan"], s["dy"], s["w_down"], s["gate"], s["up"], s["offsets"], s["dgate"], s["dup"],
+                           s["h"])
+        return {key: s[key] for key in ("dgate", "dup", "h") if s[key] is not None}
+    if op == "gated dx":
+        R.gated_backward_x(s["plan"], s["dgate"], s["dup"], s["w_gate"], s["w_up"], s["offsets"], s["dx"])
+        return s["dx"]
+    if op == "mx rows":
+        R.mx_quantise(s["plan"], s["x"], s["codes"], s["scales"])
+        R.mx_dequantise(s["plan"], s["codes"], s["scales"], s["values"])
+        return {"values": s["values"], "scales": s["scales"]}
+    if op == "mx":
+        R.mx_forward(s["plan"], *s["x"], *s["w"][0], s["offsets"], s["out"])
+    else:
+        R.mx_gated(s["plan"], *s["x"], *s["w"][0], *s["w"][1], s["offsets"], s["out"])
+    return s["out"]
+
+
+# ---- the plain forms --------------------------------------------------------------------------
+def _rows_by_weight(s, case, v, w):
+    """v [rows, c] f32 with each row's own group's w [groups, c, d]: few rows one by one, otherwise every group padded
+    to the largest."""
+    off, rows, groups = s["offsets"], case["rows"], case["groups"]
+    gid = torch.searchsorted(off[1:], torch.arange(rows, dtype=torch.int32, device="cuda"), right=True)
+    if rows < groups:
+        return torch.bmm(v[:, None, :], w(gid))[:, 0]
+    place = gid * s["most"] + torch.arange(rows, device="cuda") - off[gid]
+    p = torch.zeros((groups * s["most"], v.shape[1]), dtype=torch.float32, device="cuda")
+    p[place] = v
+    return torch.bmm(p.view(groups, s["most"], -1), w(slice(None))).flatten(0, 1)[place]
+
+
+def _activation(z, act):
+    """act(z) and its derivative."""
+    inner, slope = z, 1.0
+    if act == "gelu":
+        c = 2 * math.sqrt(2 / math.pi)
+        inner, slope = c * (z + 0.044715 * z * z * z), c * (1 + 3 * 0.044715 * z * z)
+    p = 1 / (1 + torch.exp(-inner))
+    return z * p, p + z * p * (1 - p) * slope
+
+
+def _clamped(g, u, limit):
+    return (g.clamp(max=limit), u.clamp(-limit, limit)) if limit else (g, u)
+
+
+def _plain_gated(s, case):
+    op = case["op"]
+    if op == "gated dx":
+        dx = _rows_by_weight(s, case, s["dgate"].float(), lambda i: s["w_gate"][i].float())
+        return (dx + _rows_by_weight(s, case, s["dup"].float(), lambda i: s["w_up"][i].float())).to(_TYPES[case["out"]])
+    t, limit = _TYPES[case["type"]], case["limit"]
+    if op == "gated":
+        x = s["x"].float()
+        g, u = (_rows_by_weight(s, case, x, lambda i, w=s[key]: w[i].float().transpose(1, 2))
+                for key in ("w_gate", "w_up"))
+        gc, uc = _clamped(g, u, limit)
+        out = {"h": (_activation(gc, case["act"])[0] * uc).to(t)}
+        return {**out, "gate": g.to(t), "up": u.to(t)} if case["kept"] else out
+    dh = _rows_by_weight(s, case, s["dy"].float(), lambda i: s["w_down"][i].float())
+    g, u = s["gate"].float(), s["up"].float()
+    gc, uc = _clamped(g, u, limit)
+    a, slope = _activation(gc, case["act"])
+    dgate, dup = dh * uc * slope, dh * a
+    if limit:
+        dgate, dup = dgate * (g <= limit), dup * (u.abs() <= limit)
+    out = {"dgate": dgate.to(t), "dup": dup.to(t)}
+    return {**out, "h": (a * uc).to(t)} if case["again"] else out
+
+
+def _plain_mx(s, case):
+    k, out = case["k"], _TYPES[case["out"]]
+    x = _from_mx(*s["x"], k)
+    y = [_rows_by_weight(s, case, x, lambda i, w=w: _from_mx(w[0][i], w[1][i], k).transpose(1, 2)) for w in s["w"]]
+    if case["op"] == "mx":
+        return y[0].to(out)
+    g, u = _clamped(y[0], y[1], case["limit"])
+    return (_activation(g, case["act"])[0] * u).to(out)
+
+
+def run(state):
+    if own:
+        return _run_own(state)
+    case = state["case"]
+    if case["op"] == "mx rows":
+        codes, scales = _to_mx(state["x"].float(), case["scale"])
+        return {"values": _from_mx(codes, scales, case["k"]).to(_TYPES[case["type"]]), "scales": scales}
+    return (_plain_gated if case["op"].startswith("gated") else _plain_mx)(state, case)
+
+
+def work(case):
+    op, rows, k = case["op"], case["rows"], case["k"]
+    quant = (k + 1) // 2 + (k + 31) // 32   # bytes of a row in 4 bits
+    if op == "mx rows":
+        e = 4 if case["type"] == "f32" else 2
+        return {"bytes": rows * (2 * k * e + 2 * quant), "flops": 4 * rows * k}   # there and back
+    n, groups = case["n"], case["groups"]
+    used = sum(v > 0 for v in _sizes(rows, groups, case["skew"]))
+    o, idx = 4 if case.get("out") == "f32" else 2, 4 * (groups + 1)
+    if op == "mx" or op == "mx gated":
+        w = 2 if op == "mx gated" else 1
+        return {"bytes": rows * quant + w * used * n * quant + rows * n * o + idx, "flops": 2.0 * w * rows * n * k}
+    if op == "gated":
+        made = 3 if case["kept"] else 1
+        return {"bytes": 2 * (rows * k + 2 * used * n * k + made * rows * n) + idx, "flops": 4.0 * rows * n * k}
+    if op == "gated dh":
+        moved = 5 if case["again"] else 4   # gate and up read, two gradients (and h) written
+        return {"bytes": 2 * (rows * k + used * n * k + moved * rows * n) + idx, "flops": 2.0 * rows * n * k}
+    return {"bytes": 2 * (2 * rows * n + 2 * used * n * k) + o * rows * k + idx, "flops": 4.0 * rows * n * k}
+
+
+# ---- the definitions in 64 bits -----------------------------------------------------------------
+def _exact_mx(case, x):
+    """Block by block of the f64 values: the scale's exponent, and the nearest step, ties to the even one."""
+    rows, k = x.shape
+    values = torch.empty((rows, k), dtype=torch.float64, device=x.device)
+    scales = torch.empty((rows, -(-k // 32)), dtype=torch.uint8, device=x.device)
+    steps = torch.tensor(_STEPS, dtype=torch.float64, device=x.device)
+    between = (steps[1:] + steps[:-1]) / 2
+    for i in range(scales.shape[1]):
+        v = x[:, 32 * i:32 * i + 32].double()
+        top = v.abs().max(1).values
+        e = torch.floor(torch.log2(torch.where(top > 0, top, 1.0)))
+        e = torch.where(torch.exp2(e) > top, e - 1, e)   # log2 next to a power of two
+        e = torch.where(torch.exp2(e + 1) <= top, e + 1, e) - 2
+        if case["scale"] == "ceil":
+            e = torch.where(6 * torch.exp2(e) < top, e + 1, e)
+        e = torch.where(top > 0, e, -127.0).clamp(min=-127)
+        a = v.abs() / torch.exp2(e)[:, None]
+        at = torch.searchsorted(between, a, right=False)
+        tie = (at < 7) & (a == between[at.clamp(max=6)]) & (at % 2 == 1)   # odd steps are those of odd mantissas
+        values[:, 32 * i:32 * i + 32] = steps[at + tie.long()] * torch.exp2(e)[:, None] * torch.where(v < 0, -1.0, 1.0)
+        scales[:, i] = (e + 127).to(torch.uint8)
+    return {"values": values, "scales": scales}
+
+
+def _decoded(codes, scales, k):
+    """Codes and scales as f64 values."""
+    v = torch.empty(codes.shape[:-1] + (2 * codes.shape[-1],), dtype=torch.float64, device=codes.device)
+    for half, c in ((0, codes % 16), (1, codes // 16)):
+        mant, power = (c % 2).double(), (c // 2 % 4).double()
+        size = torch.where(power == 0, mant / 2, (1 + mant / 2) * torch.exp2(power - 1))
+        v[..., half::2] = torch.where(c >= 8, -size, size)
+    return v[..., :k] * torch.pow(2.0, scales.double() - 127).repeat_interleave(32, -1)[..., :k]
+
+
+def exact(case, seed):
+    """Group by group in 64 bits."""
+    s, op = _inputs(case, seed), case["op"]
+    if op == "mx rows":
+        return _exact_mx(case, s["x"])
+    n, k, rows, ends = case["n"], case["k"], case["rows"], s["offsets"].tolist()
+    limit = case.get("limit") or math.inf
+
+    def by_group(width, product):
+        y = torch.zeros((rows, width), dtype=torch.float64, device="cuda")
+        for g, (a, b) in enumerate(zip(ends, ends[1:])):
+            if a < b:
+                y[a:b] = product(g, a, b)
+        return y
+
+    def half_sum(z):   # s of act(z) = z s(z), with the inner function's slope
+        if case["act"] == "gelu":
+            c = math.sqrt(8 / math.pi)
+            return torch.sigmoid(c * (z + 0.044715 * z.pow(3))), c * (1 + 0.134145 * z.pow(2))
+        return torch.sigmoid(z), torch.ones_like(z)
+
+    def hidden(g, u):
+        z = torch.minimum(g, torch.full_like(g, limit))
+        return z * half_sum(z)[0] * torch.maximum(torch.minimum(u, torch.full_like(u, limit)), torch.full_like(u, -limit))
+
+    if op.startswith("mx"):
+        x = _decoded(*s["x"], k)
+        y = [by_group(n, lambda g, a, b: x[a:b] @ _decoded(c[g], e[g], k).t()) for c, e in s["w"]]
+        return y[0] if op == "mx" else hidden(*y)
+    if op == "gated":
+        x = s["x"].double()
+        g, u = (by_group(n, lambda i, a, b: x[a:b] @ s[key][i].double().t()) for key in ("w_gate", "w_up"))
+        return {"h": hidden(g, u), "gate": g, "up": u} if case["kept"] else {"h": hidden(g, u)}
+    if op == "gated dx":
+        dg, du = s["dgate"].double(), s["dup"].double()
+        return by_group(k, lambda i, a, b: dg[a:b] @ s["w_gate"][i].double() + du[a:b] @ s["w_up"][i].double())
+    dy, g, u = s["dy"].double(), s["gate"].double(), s["up"].double()
+    dh = by_group(n, lambda i, a, b: dy[a:b] @ s["w_down"][i].double())
+    z = torch.where(g > limit, torch.full_like(g, limit), g)
+    p, slope = half_sum(z)
+    inside = torch.where(u > limit, torch.full_like(u, limit), torch.where(u < -limit, torch.full_like(u, -limit), u))
+    out = {"dgate": torch.where(g > limit, 0.0, dh * inside * p * (1 + z * (1 - p) * slope)),
+           "dup": torch.where(u.abs() > limit, 0.0, dh * z * p)}
+    return {**out, "h": hidden(g, u)} if case["again"] else out
