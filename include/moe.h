@@ -436,7 +436,7 @@ int moe_read_probe(const void* buf, uint64_t bytes, uint32_t* sink, int32_t bloc
 /* Bits that the device ORs into a call's optional status word (int32 on the
  * device, set to 0 by the caller) when the data of an index array is invalid;
  * the call stays inside its buffers in any case. */
-#define MOE_STATUS_BAD_OFFSETS 8   /* moe_grouped_*: offsets not ascending, or outside [0, rows] */
+#define MOE_STATUS_BAD_OFFSETS 8   /* offsets of groups not ascending, or outside [0, rows]      */
 #define MOE_STATUS_BAD_ADAPTER 16  /* moe_adapter_project: an index outside [-1, n_adapters)      */
 
 /* Joining a block to the residual stream. For each of m rows, with f32
@@ -519,6 +519,56 @@ int moe_grouped_backward_x(const moe_grouped* g, const void* dy, const void* w, 
                            void* dx, int32_t* status, void* stream);
 int moe_grouped_backward_w(const moe_grouped* g, const void* dy, const void* x, const int32_t* offsets, int64_t rows,
                            void* dw, int32_t* status, void* stream);
+
+/* The gated activation of the operators below: act(min(g, L)) * clamp(u, -L, L),
+ * act(z) = z s(z) with the logistic function s of z (MOE_ACT_SILU) or of
+ * 2 sqrt(2/pi) (z + 0.044715 z^3) (MOE_ACT_GELU, the tanh form); limit L, 0: no clamps. */
+#define MOE_ACT_SILU 0
+#define MOE_ACT_GELU 1
+
+/* A gated feed-forward block grouped by expert, rows sorted by group and offsets
+ * as for the grouped products (one group: a dense block). Products of 16-bit
+ * elements, f32 sums, one rounding of each output:
+ *   forward     g = Wg x, u = Wu x; h = act(min(g, L)) * clamp(u, -L, L) of the
+ *               unrounded g and u; gate = g and up = u, for the gradients (both or neither)
+ *   backward_h  from the gradient dy of y = Wd h: dh = Wd^T dy (not rounded), and of the kept gate and up
+ *               dgate = dh * clamp(up, -L, L) * act'(gate), 0 where gate > L
+ *               dup = dh * act(min(gate, L)), 0 where |up| > L
+ *               h (may be NULL) = act(min(gate, L)) * clamp(up, -L, L), for the gradient of Wd
+ *   backward_x  dx = Wg^T dgate + Wu^T dup
+ * y = Wd h is moe_grouped_forward; the weights' gradients are moe_grouped_backward_w of
+ * (dy, h), (dgate, x) and (dup, x): one call for the last two where gate and up are halves of rows of 2 n.
+ *   x, dx  [rows][k]   h, gate, up, dgate, dup  [rows][n]   dy  [rows][k]
+ *   w_gate, w_up  [n_groups][n][k]   w_down  [n_groups][k][n]
+ * Everything has `type`, dx `dx_type`. dgate may be gate and dup may be up, in
+ * place; other outputs must not overlap inputs or one another. Every output is
+ * written whole: rows of no group are 0. rows may be 0, and is at most MOE_GROUPED_MAX_ROWS. Any n, k >= 1,
+ * stride and element alignment; rows whose start is 16-byte aligned (and, in the
+ * backward calls, widths that are multiples of 8) take the faster path. A call looks
+ * only at the strides of its own tensors. The same call gives the same bits.
+ * status: MOE_STATUS_BAD_OFFSETS, may be NULL; outputs are unspecified then. */
+typedef struct moe_gated {
+  int32_t n_groups, n, k;
+  int32_t type;               /* MOE_TYPE_BF16 or MOE_TYPE_FP16             */
+  int32_t dx_type;            /* type, or MOE_TYPE_F32                      */
+  int32_t act;                /* MOE_ACT_*                                  */
+  float limit;                /* finite, >= 0                               */
+  int64_t x_stride;           /* elements between rows: x and dx, >= k      */
+  int64_t h_stride;           /* h, >= n                                    */
+  int64_t gate_stride;        /* gate, up, dgate and dup, >= n              */
+  int64_t y_stride;           /* dy, >= k                                   */
+  int64_t w_stride;           /* rows of w_gate and w_up, >= k              */
+  int64_t w_group_stride;     /* from one group's w_gate (w_up) to the next */
+  int64_t down_stride;        /* rows of w_down, >= n                       */
+  int64_t down_group_stride;
+} moe_gated;
+int moe_gated_forward(const moe_gated* g, const void* x, const void* w_gate, const void* w_up, const int32_t* offsets,
+                      int64_t rows, void* h, void* gate, void* up, int32_t* status, void* stream);
+int moe_gated_backward_h(const moe_gated* g, const void* dy, const void* w_down, const void* gate, const void* up,
+                         const int32_t* offsets, int64_t rows, void* dgate, void* dup, void* h, int32_t* status,
+                         void* stream);
+int moe_gated_backward_x(const moe_gated* g, const void* dgate, const void* dup, const void* w_gate, const void* w_up,
+                         const int32_t* offsets, int64_t rows, void* dx, int32_t* status, void* stream);
 
 /* A shared projection with one low-rank adapter per token:
  *   out[t] = W x[t] + factor[a] B[a] (A[a] x[t]),  a = index[t]; a = -1: W x[t].

@@ -115,6 +115,9 @@ def lib():
         L.moe_adapter_workspace_bytes.restype = ctypes.c_size_t
         L.moe_adapter_workspace_bytes.argtypes = [_VP, ctypes.c_int64]
         L.moe_adapter_project.argtypes = [_VP] * 4 + [ctypes.c_int64, _VP, _VP, ctypes.c_size_t, _VP, _VP]
+        L.moe_gated_forward.argtypes = [_VP] * 5 + [ctypes.c_int64] + [_VP] * 5
+        L.moe_gated_backward_h.argtypes = [_VP] * 6 + [ctypes.c_int64] + [_VP] * 5
+        L.moe_gated_backward_x.argtypes = [_VP] * 6 + [ctypes.c_int64] + [_VP] * 3
         L.moe_last_error.restype = ctypes.c_char_p
         _lib = L
     return _lib
@@ -346,6 +349,7 @@ MOE_JOIN_MAX_DIM = 16384
 MOE_GROUPED_MAX_GROUPS = 1024
 MOE_GROUPED_MAX_STRIDE = 1 << 22
 MOE_GROUPED_MAX_ROWS = 0x7fffff00
+MOE_ACT_SILU, MOE_ACT_GELU = 0, 1
 MOE_ADAPTER_MAX_ADAPTERS = 1024
 MOE_ADAPTER_MAX_RANK = 1024
 MOE_ADAPTER_MAX_TOKENS = 1 << 20
@@ -382,7 +386,8 @@ def _tensors():
             raise ImportError(f"{TENSORS_PATH} is not built: run __graft_entry__.build()") from e
         native.bind(MoeError, *(ctypes.cast(f, _VP).value for f in (
             L.moe_join_forward, L.moe_join_backward, L.moe_grouped_forward, L.moe_grouped_backward_x,
-            L.moe_grouped_backward_w, L.moe_adapter_project, L.moe_last_error)))
+            L.moe_grouped_backward_w, L.moe_adapter_project, L.moe_gated_forward, L.moe_gated_backward_h,
+            L.moe_gated_backward_x, L.moe_last_error)))
         _native = native
     return _native
 
@@ -448,6 +453,56 @@ def grouped_backward_x(g: Grouped, dy, w, offsets, dx, status=None, stream=None)
 def grouped_backward_w(g: Grouped, dy, x, offsets, dw, status=None, stream=None):
     """dw[g] = the sum of dy[r] x[r]^T over the group's rows."""
     _tensors().grouped_backward_w(g, dy, x, offsets, dw, status, _stream(stream))
+
+
+def act_code(act) -> int:
+    """The MOE_ACT_* code of "silu" or "gelu" (a code passes through)."""
+    if isinstance(act, int):
+        return act
+    code = {"silu": MOE_ACT_SILU, "gelu": MOE_ACT_GELU}.get(act)
+    if code is None:
+        raise MoeError(-1, f"act must be silu or gelu (got {act!r})")
+    return code
+
+
+class Gated(ctypes.Structure):
+    """moe_gated: a gated feed-forward block per group of rows, act(min(g, limit)) * clamp(u, -limit, limit) between
+    its projections (limit 0 or None: no clamps). dx: the type of the input's gradient. Strides default to contiguous
+    rows and weights."""
+    _fields_ = [("n_groups", ctypes.c_int32), ("n", ctypes.c_int32), ("k", ctypes.c_int32), ("type", ctypes.c_int32),
+                ("dx_type", ctypes.c_int32), ("act", ctypes.c_int32), ("limit", ctypes.c_float),
+                ("x_stride", ctypes.c_int64), ("h_stride", ctypes.c_int64), ("gate_stride", ctypes.c_int64),
+                ("y_stride", ctypes.c_int64), ("w_stride", ctypes.c_int64), ("w_group_stride", ctypes.c_int64),
+                ("down_stride", ctypes.c_int64), ("down_group_stride", ctypes.c_int64)]
+
+    def __init__(self, n_groups: int, n: int, k: int, dtype, act="silu", limit: float | None = None, dx=None,
+                 x_stride: int | None = None, h_stride: int | None = None, gate_stride: int | None = None,
+                 y_stride: int | None = None, w_stride: int | None = None, w_group_stride: int | None = None,
+                 down_stride: int | None = None, down_group_stride: int | None = None):
+        t = type_code(dtype)
+        ws = k if w_stride is None else w_stride
+        ds = n if down_stride is None else down_stride
+        super().__init__(n_groups, n, k, t, t if dx is None else type_code(dx), act_code(act), limit or 0.0,
+                         k if x_stride is None else x_stride, n if h_stride is None else h_stride,
+                         n if gate_stride is None else gate_stride, k if y_stride is None else y_stride, ws,
+                         n * ws if w_group_stride is None else w_group_stride, ds,
+                         k * ds if down_group_stride is None else down_group_stride)
+
+
+def gated_forward(g: Gated, x, w_gate, w_up, offsets, h, gate=None, up=None, status=None, stream=None):
+    """h[r] = act(w_gate[group of r] @ x[r]) * (w_up[group of r] @ x[r]); gate and up: the two products, kept for the
+    gradients."""
+    _tensors().gated_forward(g, x, w_gate, w_up, offsets, h, gate, up, status, _stream(stream))
+
+
+def gated_backward_h(g: Gated, dy, w_down, gate, up, offsets, dgate, dup, h=None, status=None, stream=None):
+    """dgate and dup of the kept gate and up, for h's gradient w_down[group of r]^T @ dy[r]; h: made again."""
+    _tensors().gated_backward_h(g, dy, w_down, gate, up, offsets, dgate, dup, h, status, _stream(stream))
+
+
+def gated_backward_x(g: Gated, dgate, dup, w_gate, w_up, offsets, dx, status=None, stream=None):
+    """dx[r] = w_gate[group of r]^T @ dgate[r] + w_up[group of r]^T @ dup[r]."""
+    _tensors().gated_backward_x(g, dgate, dup, w_gate, w_up, offsets, dx, status, _stream(stream))
 
 
 class Adapters(ctypes.Structure):

@@ -56,9 +56,15 @@ struct Operand {
   int count;
   const int32_t* rows;
   bool room;
+  int64_t then = 0;   // kTwoSums: elements from here to the second sum's operand
 };
 
-template <typename T, bool COL, int R, int NT, bool GATHER = false>
+// What a tile has of two matrices. kRowPairs: its rows p are 16 of the first and 16 of the second in turn (`count` and the
+// output's width are the first one's; second_rows() says which matrix a thread's `base` is in), so that a lane's sums i and i + 1 are
+// those of the same output of both. kTwoSums: C is the sum of two products of the same shape.
+enum Two { kSingle, kRowPairs, kTwoSums };
+
+template <typename T, bool COL, int R, int NT, bool GATHER = false, bool PAIRS = false>
 struct TileOf {
   typedef std::conditional_t<GATHER, int64_t, uint32_t> Off;   // a tile's elements stay within 2^31 of its base
   static constexpr int kBytes = R * kStep * 2;
@@ -67,6 +73,7 @@ struct TileOf {
   static constexpr int kRowChunks = COL ? R / 8 : kStep / 8;      // chunks of a stored row
   static_assert(kChunks % NT == 0 || NT % kChunks == 0, "chunks over threads");
   static_assert(!COL || R >= 64, "the swizzle of a column tile needs 8 chunks a row");
+  static_assert(!PAIRS || (!COL && !GATHER && NT % 256 == 0 && kChunks >= NT), "a thread's chunks are all of one matrix");
 
   // A transposing read takes four rows of 32 bytes for each quarter of the wave, the quarters 8 rows apart.
   // Rows of 256 bytes and more all start at LDS bank 0: 8 swizzles keep the 8 rows of half a wave apart (4 where a row has 8 chunks only).
@@ -98,6 +105,7 @@ struct TileOf {
         if (DMA) own = min(own, o.count - 8);
         off[k] = (Off)r * (Off)o.ld + own;
       } else {
+        if constexpr (PAIRS) own = own / 32 * 16 + own % 16;
         own = min(own, o.count - 1);
         if constexpr (GATHER) own = max(o.rows[own], 0);
         off[k] = (Off)own * (Off)o.ld + r;
@@ -230,21 +238,25 @@ __device__ __forceinline__ void wait_steps(int steps) {
 
 // WP x WQ waves of BP/WP x BQ/WQ outputs each; ST slots of one step in LDS.
 // DMA: 16-byte aligned rows, brought into LDS directly; otherwise through registers, any alignment.
-template <typename T, bool PCOL, bool QCOL, int BP, int BQ, int WP, int WQ, int ST, bool DMA, bool GATHER = false>
+template <typename T, bool PCOL, bool QCOL, int BP, int BQ, int WP, int WQ, int ST, bool DMA, bool GATHER = false,
+          Two TWO = kSingle>
 struct Gemm {
   static constexpr int NT = 64 * WP * WQ;
-  typedef TileOf<T, PCOL, BP, NT> PT;
+  typedef TileOf<T, PCOL, BP, NT, false, TWO == kRowPairs> PT;
   typedef TileOf<T, QCOL, BQ, NT, GATHER> QT;
   static constexpr int kSlots = DMA ? ST : 2;
   static constexpr int kSlot = PT::kBytes + QT::kBytes;
   static constexpr int kLds = kSlots * kSlot;
-  static constexpr int kP = BP, kQ = BQ;
+  static constexpr int kP = TWO == kRowPairs ? BP / 2 : BP, kQ = BQ;   // outputs of a tile
   static constexpr int NP = BP / WP / 16, NQ = BQ / WQ / 16;
   typedef f32x4 Acc[NP][NQ];
   static constexpr int kStores = NP * NQ;   // store instructions of a wave's whole part of a tile
 
   __device__ static __forceinline__ int wave_p() { return (threadIdx.x >> 6) % WP * (BP / WP); }
   __device__ static __forceinline__ int wave_q() { return (threadIdx.x >> 6) / WP * (BQ / WQ); }
+
+  // kRowPairs: the rows that this thread brings in are those of the first matrix or of the second (8 rows to 64 chunks).
+  __device__ static __forceinline__ bool second_rows() { return threadIdx.x >> 7 & 1; }
 
   // The MFMA operands of 32 r, and their products.
   struct Half {
@@ -301,7 +313,7 @@ struct Gemm {
     }
   }
 
-  // Adds the sum over r < red. LDS is free for other use after a barrier.
+  // Adds the sum over r < red (kTwoSums: both sums, each over r < red). LDS is free for other use after a barrier.
   __device__ static __forceinline__ void run(const Operand<T>& p, const Operand<T>& q, int red, uint8_t* lds,
                                              Acc& acc) {
     const int64_t ps = PT::step_stride(p), qs = QT::step_stride(q);
@@ -310,25 +322,34 @@ struct Gemm {
     PT::template offsets<DMA>(p, po);
     QT::template offsets<DMA>(q, qo);
     if constexpr (DMA) {
-      const int nk = red / kStep, tail = red % kStep;
+      const int each = red / kStep, tail = red % kStep, nk = TWO == kTwoSums ? 2 * each : each;
       constexpr int kPer = PT::kPer + QT::kPer;
       const T *pat = uniform(p.base), *qat = uniform(q.base);
+      int left = each;   // steps of the first sum to ask for
       auto issue = [&](const uint8_t* slot) {
         const uint32_t at = lds_offset(slot);
         PT::dma(pat, po, at);
         QT::dma(qat, qo, at + PT::kBytes);
         pat += ps;
         qat += qs;
+        if constexpr (TWO == kTwoSums) {
+          if (--left == 0) {
+            pat += p.then - each * ps;
+            qat += q.then - each * qs;
+          }
+        }
       };
       uint8_t* const end = lds + kLds;
 #pragma unroll
       for (int s = 0; s < ST - 1; ++s)
         if (s < nk) issue(lds + s * kSlot);
-      if (tail) {   // the last, partial step first, in the slot that the ring needs last
+#pragma unroll 1
+      for (int part = 0; part < (TWO == kTwoSums ? 2 : 1); ++part) {
+        if (!tail) break;   // the last, partial step first, in the slot that the ring needs last
         uint8_t* const put = end - kSlot;
         oct<T> pv[PT::kPer], qv[QT::kPer];
-        PT::load(p, p.base + nk * ps, po, tail, pv);
-        QT::load(q, q.base + nk * qs, qo, tail, qv);
+        PT::load(p, p.base + each * ps + part * p.then, po, tail, pv);
+        QT::load(q, q.base + each * qs + part * q.then, qo, tail, qv);
         PT::store(p, tail, pv, put);
         QT::store(q, tail, qv, put + PT::kBytes);
         lds_barrier();
@@ -374,21 +395,28 @@ struct Gemm {
       multiply(h0, acc);
       multiply(h1, acc);
     } else {
-      const int nk = (red + kStep - 1) / kStep;
+      const int each = (red + kStep - 1) / kStep, nk = TWO == kTwoSums ? 2 * each : each;
       struct Stage {
         oct<T> p[PT::kPer], q[QT::kPer];
       };
       const T *pat = p.base, *qat = q.base;
-      auto load = [&](int s, Stage& g) {
-        PT::load(p, pat, po, red - s * kStep, g.p);
-        QT::load(q, qat, qo, red - s * kStep, g.q);
+      auto left = [&](int s) { return red - (TWO == kTwoSums && s >= each ? s - each : s) * kStep; };
+      auto load = [&](int s, Stage& g) {   // (in the order of the steps)
+        if constexpr (TWO == kTwoSums) {
+          if (s == each) {
+            pat += p.then - each * ps;
+            qat += q.then - each * qs;
+          }
+        }
+        PT::load(p, pat, po, left(s), g.p);
+        QT::load(q, qat, qo, left(s), g.q);
         pat += ps;
         qat += qs;
       };
       auto store = [&](int s, const Stage& g) {
         uint8_t* slot = lds + (s & 1) * kSlot;
-        PT::store(p, red - s * kStep, g.p, slot);
-        QT::store(q, red - s * kStep, g.q, slot + PT::kBytes);
+        PT::store(p, left(s), g.p, slot);
+        QT::store(q, left(s), g.q, slot + PT::kBytes);
       };
       if (nk == 0) return;
       if constexpr (PT::kPer + QT::kPer <= 6) {   // two steps on their way, where the registers hold them
@@ -557,41 +585,43 @@ struct Gemm {
 
   // Writes the tile's first `pn` outputs of each row at `out` (type f32 or T),
   // rows `ld` apart; row(q) is the place of tile row q (below 0: not stored).
-  template <typename Row>
-  __device__ static __forceinline__ void store(const Acc& acc, void* out, bool f32, int64_t ld, int pn, Row&& row) {
+  template <int N, typename Row>
+  __device__ static __forceinline__ void store(const f32x4 (&acc)[N][NQ], void* out, bool f32, int64_t ld, int pn, Row&& row) {
     if (f32) store_to(acc, (float*)out, ld, pn, row);
     else store_to(acc, (T*)out, ld, pn, row);
   }
-  template <typename U, typename Row>
-  __device__ static __forceinline__ void store_to(const Acc& acc, U* out, int64_t ld, int pn, Row& row) {
-    if constexpr (NP % 2 == 0) {
-      if (pn >= BP) return store_whole(acc, out, ld, row);
+  template <int N, typename U, typename Row>
+  __device__ static __forceinline__ void store_to(const f32x4 (&acc)[N][NQ], U* out, int64_t ld, int pn, Row& row) {
+    if constexpr (N % 2 == 0) {
+      if (pn >= kP) return store_whole(acc, out, ld, row);
     }
     store_part(acc, out, ld, pn, row);
   }
-  template <typename U, typename Row>
-  __device__ static __forceinline__ void store_part(const Acc& acc, U* out, int64_t ld, int pn, Row& row) {
+  // The wave's first output column.
+  __device__ static __forceinline__ int wave_out() { return TWO == kRowPairs ? wave_p() / 2 : wave_p(); }
+  template <int N, typename U, typename Row>
+  __device__ static __forceinline__ void store_part(const f32x4 (&acc)[N][NQ], U* out, int64_t ld, int pn, Row& row) {
     const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int j = 0; j < NQ; ++j) {
       const int64_t q = row(wave_q() + 16 * j + (lane & 15));
       if (q < 0) continue;
-      const int p = wave_p() + 4 * (lane >> 4);
+      const int p = wave_out() + 4 * (lane >> 4);
 #pragma unroll
-      for (int i = 0; i < NP; ++i) store_quad(out + q * ld + p + 16 * i, acc[i][j], pn - p - 16 * i);
+      for (int i = 0; i < N; ++i) store_quad(out + q * ld + p + 16 * i, acc[i][j], pn - p - 16 * i);
     }
   }
   // Lanes q and q + 8 of 16 exchange a quad, so that a store writes 32
   // neighbouring outputs of 8 rows instead of 16 of 16 rows.
-  template <typename U, typename Row>
-  __device__ static __forceinline__ void store_whole(const Acc& acc, U* out, int64_t ld, Row& row) {
+  template <int N, typename U, typename Row>
+  __device__ static __forceinline__ void store_whole(const f32x4 (&acc)[N][NQ], U* out, int64_t ld, Row& row) {
     const int lane = threadIdx.x & 63, upper = lane >> 3 & 1;
 #pragma unroll
     for (int j = 0; j < NQ; ++j) {
       const int64_t qa = row(wave_q() + 16 * j + (lane & 7)), qb = row(wave_q() + 16 * j + 8 + (lane & 7));
-      U* const at = out + wave_p() + 16 * upper + 4 * (lane >> 4);
+      U* const at = out + wave_out() + 16 * upper + 4 * (lane >> 4);
 #pragma unroll
-      for (int i = 0; i < NP; i += 2) {
+      for (int i = 0; i < N; i += 2) {
         f32x4 a = acc[i][j], b = acc[i + 1][j], x;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -605,6 +635,65 @@ struct Gemm {
     }
   }
 
+  // The same places for a use of its own: load(q, p, n) at tile row q, output p and the n - 1 after it, for all of a
+  // row of sums before use(q, p, n, sums, loaded) of each. What a lane loads is what it is given to use.
+  template <int N, typename Row, typename Load, typename Use>
+  __device__ static __forceinline__ void each_quad(const f32x4 (&acc)[N][NQ], int pn, Row&& row, Load&& load, Use&& use) {
+    const int lane = threadIdx.x & 63, upper = lane >> 3 & 1;
+    typedef decltype(load((int64_t)0, 0, 0)) Loaded;
+    if (N % 2 == 0 && pn >= kP) {
+#pragma unroll
+      for (int j = 0; j < NQ; ++j) {
+        const int64_t qa = row(wave_q() + 16 * j + (lane & 7)), qb = row(wave_q() + 16 * j + 8 + (lane & 7));
+        const int p = wave_out() + 16 * upper + 4 * (lane >> 4);
+        Loaded la[N / 2], lb[N / 2];
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+          if (qa >= 0) la[i] = load(qa, p + 32 * i, 4);
+          if (qb >= 0) lb[i] = load(qb, p + 32 * i, 4);
+        }
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+          f32x4 a = acc[2 * i][j], b = acc[(2 * i + 1) % N][j], x;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[e] = dpp_f32<kDppRor8>(upper ? a[e] : b[e]);
+            a[e] = upper ? x[e] : a[e];
+            b[e] = upper ? b[e] : x[e];
+          }
+          if (qa >= 0) use(qa, p + 32 * i, 4, a, la[i]);
+          if (qb >= 0) use(qb, p + 32 * i, 4, b, lb[i]);
+        }
+      }
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < NQ; ++j) {
+      const int64_t q = row(wave_q() + 16 * j + (lane & 15));
+      if (q < 0) continue;
+      const int p = wave_out() + 4 * (lane >> 4);
+      Loaded l[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) l[i] = load(q, p + 16 * i, pn - p - 16 * i);
+#pragma unroll
+      for (int i = 0; i < N; ++i) use(q, p + 16 * i, pn - p - 16 * i, acc[i][j], l[i]);
+    }
+  }
+
+  // The first n of four elements; the others are 0.
+  template <typename U>
+  __device__ static __forceinline__ f32x4 load_quad(const U* at, int n) {
+    typedef U quad __attribute__((ext_vector_type(4)));
+    quad v = {};
+    if (n >= 4) {
+      __builtin_memcpy(&v, at, sizeof(v));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (i < n) v[i] = at[i];
+    }
+    return __builtin_convertvector(v, f32x4);
+  }
   // The first n of four outputs, rounded to nearest even in U.
   template <typename U>
   __device__ static __forceinline__ void store_quad(U* at, f32x4 f, int n) {

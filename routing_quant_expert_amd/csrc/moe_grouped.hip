@@ -14,106 +14,21 @@
 // on even sizes). The weight gradient of the same rows writes 1.07 GB in f32:
 // 546 to 555 us, 341 without its stores.
 //
-// The offsets stay on the device: the grid is an upper bound of the tiles (a
-// group adds at most one partial tile), every wave finds its tile from the
-// offsets by two wave-wide prefix sums, and workgroups past the last tile end
-// at once.
+// The offsets stay on the device (moe_groups.h).
 #include <hip/hip_runtime.h>
 
 #include "moe_gemm.h"
+#include "moe_groups.h"
 #include "moe_host.h"
 
 namespace moe {
 namespace {
 
-struct GroupedArgs {
-  const int32_t* offsets;
-  int32_t* status;
-  int groups, rows;
+struct GroupedArgs : Groups {
   int n, k;
   int f32;   // outputs in f32
   int64_t x_stride, y_stride, w_stride, w_group;
 };
-
-// Rows are cut at the edges 0, offsets[0..groups], rows: entry e = g + 1 is
-// group g, the first and last entries are the rows of no group. Edges are
-// clamped to [0, rows], so that no offsets lead outside the buffers.
-__device__ __forceinline__ int edge(const GroupedArgs& a, int e) {
-  if (e <= 0) return 0;
-  if (e > a.groups + 1) return a.rows;
-  return min(max(a.offsets[e - 1], 0), a.rows);
-}
-
-struct Tile {
-  int group;        // groups or -1: the rows of no group
-  int row, rows;    // first row and rows of the tile (0: no tile)
-  int p;            // tile along the output's columns
-};
-
-// The tile of this workgroup: `np` column tiles for every BQ rows of an entry.
-// Lane l sums the tiles of the entries U l .. U l + U - 1; the wave's prefix
-// sums give the lane, and the prefix sums of that lane's entries the entry.
-template <int BQ>
-__device__ __forceinline__ Tile find_tile(const GroupedArgs& a, int np) {
-  const int lane = threadIdx.x & 63, entries = a.groups + 2, U = (entries + 63) / 64;
-  auto tiles = [](int lo, int hi) { return hi > lo ? (hi - lo + BQ - 1) / BQ : 0; };
-  int sum = 0;
-  const int lo0 = edge(a, lane * U);
-  int lo = lo0;
-  for (int u = 0; u < U; ++u) {
-    const int e = lane * U + u;
-    if (e >= entries) break;
-    const int hi = edge(a, e + 1);
-    sum += tiles(lo, hi);
-    lo = hi;
-  }
-  const int incl = wave_scan(sum, lane);
-  const int64_t total = (int64_t)__builtin_amdgcn_readlane(incl, 63) * np;
-  const int64_t place = xcd_order(blockIdx.x, total);
-  if (place >= total) return {0, 0, 0, 0};
-  const int t = (int)(place / np);
-  const uint64_t lanes = __ballot(incl > t);
-  if (!lanes) return {0, 0, 0, 0};   // (counts of offsets that do not ascend may wrap)
-  const int sel = __builtin_ctzll(lanes);
-  // the sums of the entries before, and the entry's own tiles and rows
-  int s = 0, first = __builtin_amdgcn_readlane(incl - sum, sel), n_rt, glo, ghi;
-  if (U == 1) {   // (a lane has one entry: its edges are there)
-    n_rt = __builtin_amdgcn_readlane(sum, sel);
-    glo = __builtin_amdgcn_readlane(lo0, sel);
-    ghi = __builtin_amdgcn_readlane(lo, sel);
-  } else {
-    const int e = sel * U + lane;
-    const bool mine = lane < U && e < entries;
-    const int elo = mine ? edge(a, e) : 0, ehi = mine ? edge(a, e + 1) : 0;
-    const int cnt = tiles(elo, ehi);
-    const int incl2 = first + wave_scan(cnt, lane);
-    const uint64_t hits = __ballot(incl2 > t);
-    if (!hits) return {0, 0, 0, 0};
-    s = __builtin_ctzll(hits);
-    first = __builtin_amdgcn_readlane(incl2 - cnt, s);
-    n_rt = __builtin_amdgcn_readlane(cnt, s);
-    glo = __builtin_amdgcn_readlane(elo, s);
-    ghi = __builtin_amdgcn_readlane(ehi, s);
-  }
-  int rt, pt;
-  tile_at(place - (int64_t)first * np, n_rt, np, rt, pt);
-  if (rt < 0 || rt >= n_rt) return {0, 0, 0, 0};
-  return {sel * U + s - 1, glo + rt * BQ, min(BQ, ghi - (glo + rt * BQ)), pt};
-}
-
-// The first workgroup reports offsets that do not ascend or leave [0, rows].
-__device__ __forceinline__ void report(const GroupedArgs& a) {
-  if (!a.status || blockIdx.x) return;
-  bool bad = false;
-  for (int g = threadIdx.x; g < a.groups; g += blockDim.x) {
-    const int lo = a.offsets[g], hi = a.offsets[g + 1];
-    bad = bad || lo < 0 || hi < lo || hi > a.rows;
-  }
-  if (bad) atomicOr(a.status, MOE_STATUS_BAD_OFFSETS);
-}
-
-// No rows: nothing to write, but the offsets are looked at.
-__global__ __launch_bounds__(64) void k_grouped_offsets(GroupedArgs a) { report(a); }
 
 // Forward (WCOL false): in = x, out = y. Input gradient (WCOL true): in = dy, out = dx.
 template <typename T, bool WCOL, typename G>
@@ -236,28 +151,15 @@ int check_grouped(const moe_grouped* g, int64_t rows) {
 }
 
 GroupedArgs grouped_args(const moe_grouped& g, const int32_t* offsets, int64_t rows, int32_t* status) {
-  return {offsets, status, g.n_groups, (int)rows, g.n, g.k, g.out_type == MOE_TYPE_F32,
+  return {{offsets, status, g.n_groups, (int)rows}, g.n, g.k, g.out_type == MOE_TYPE_F32,
           g.x_stride, g.y_stride, g.w_stride, g.w_group_stride};
-}
-
-template <auto Kernel, typename G, typename... A>
-int launch(int64_t tiles, hipStream_t s, A... args) {
-  const int64_t blocks = tile_blocks(tiles, G::NT);
-  if (!blocks) return fail(MOE_EUNSUPPORTED, "grouped: too many tiles for one launch%s (%lld)", "", tiles);
-  return launch_tiles<Kernel>("grouped", dim3((unsigned)blocks), G::NT, G::kLds, s, args...);
-}
-
-// At most so many row tiles of q rows: a group adds at most one partial tile.
-int64_t row_tiles(const GroupedArgs& a, int q) {
-  const int64_t some = a.groups + 2 < a.rows ? a.groups + 2 : a.rows;   // entries that can have rows
-  return (a.rows + (q - 1) * some) / q;
 }
 
 template <typename T, bool WCOL, typename G>
 int launch_rows(const GroupedArgs& a, const void* in, const void* w, void* out, hipStream_t s) {
   const int width = WCOL ? a.k : a.n;
-  return launch<k_grouped<T, WCOL, G>, G>(row_tiles(a, G::kQ) * ((width + G::kP - 1) / G::kP), s, a, (const T*)in,
-                                          (const T*)w, out);
+  return launch_rows_of_tiles<k_grouped<T, WCOL, G>, G>("grouped", row_tiles(a, G::kQ) * ((width + G::kP - 1) / G::kP),
+                                                        s, a, (const T*)in, (const T*)w, out);
 }
 
 template <typename T, bool WCOL, bool DMA>
@@ -288,7 +190,7 @@ int launch_rows_as(const GroupedArgs& a, const void* in, const void* w, void* ou
 template <typename T, typename G>
 int launch_dw(const GroupedArgs& a, const void* dy, const void* x, void* dw, hipStream_t s) {
   const int64_t tiles = (int64_t)((a.k + G::kP - 1) / G::kP) * ((a.n + G::kQ - 1) / G::kQ) * a.groups;
-  return launch<k_grouped_dw<T, G>, G>(tiles, s, a, (const T*)dy, (const T*)x, dw);
+  return launch_rows_of_tiles<k_grouped_dw<T, G>, G>("grouped", tiles, s, a, (const T*)dy, (const T*)x, dw);
 }
 
 template <typename T, typename G>
@@ -340,9 +242,7 @@ int grouped(Way way, const moe_grouped* g, const void* in, const void* w, const 
     if (!status) return MOE_OK;
     if ((uintptr_t)offsets % 4 || (uintptr_t)status % 4)
       return fail(MOE_EINVAL, "grouped: a pointer is not aligned to its elements%s%lld");
-    k_grouped_offsets<<<dim3(1), dim3(64), 0, (hipStream_t)stream>>>(grouped_args(*g, offsets, rows, status));
-    const hipError_t e = hipGetLastError();
-    return e == hipSuccess ? MOE_OK : hip_fail(e, "grouped");
+    return launch_offsets("grouped", grouped_args(*g, offsets, rows, status), (hipStream_t)stream);
   }
   if ((rows && !in) || ((rows || way != kWeight) && !w) || !out)
     return fail(MOE_EINVAL, "grouped: operands and output must be non-NULL%s%lld");

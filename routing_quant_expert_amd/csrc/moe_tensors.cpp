@@ -1,6 +1,6 @@
 // The calls of the operators beside the layer on torch tensors (Python module
 // `_tensors`): every tensor is held against the call's description (moe_join,
-// moe_grouped, moe_adapters), then the entry point of include/moe.h is called.
+// moe_grouped, moe_adapters, moe_gated), then the entry point of include/moe.h is called.
 // Native because the host's part of a small call is all of it: a join_forward
 // of one row takes 3.6 us so, 4.6 through ctypes without the checks of its seven
 // tensors and 5.4 with them in Python.
@@ -13,6 +13,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/detail/CUDAHooksInterface.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdio>
@@ -32,6 +33,9 @@ struct {
   decltype(&::moe_grouped_backward_x) grouped_backward_x;
   decltype(&::moe_grouped_backward_w) grouped_backward_w;
   decltype(&::moe_adapter_project) adapter_project;
+  decltype(&::moe_gated_forward) gated_forward;
+  decltype(&::moe_gated_backward_h) gated_backward_h;
+  decltype(&::moe_gated_backward_x) gated_backward_x;
   decltype(&::moe_last_error) last_error;
 } entry;
 
@@ -319,6 +323,83 @@ int adapter_project(PyObject* const* a) {
   });
 }
 
+// The tensors of one call: on the current device, which is where the kernels are launched.
+class Tensors {
+  int device_ = -1;
+
+  void here(PyObject* o, const char* what) {
+    if (!THPVariable_Check(o)) return;
+    const at::Tensor& t = THPVariable_Unpack(o);
+    if (!t.is_cuda()) return;
+    if (device_ < 0) device_ = at::detail::getCUDAHooks().getCurrentDevice();
+    if (t.get_device() != device_) fail(what, "on another device than the current one");
+  }
+
+ public:
+  void* operator()(PyObject* o, const char* what, int type, const Extent& x) {
+    void* at = address(o, what, type, x);
+    here(o, what);
+    return at;
+  }
+};
+
+int gated_forward(PyObject* const* a) {
+  const Plan<moe_gated> g(a[0], "gated");
+  const int64_t rows = rows_of(a[1], "x");
+  const Extent w = {g->n_groups, g->w_group_stride, g->n, g->w_stride, g->k}, kept = matrix(rows, g->gate_stride, g->n);
+  Tensors of;
+  const void* x = of(a[1], "x", g->type, matrix(rows, g->x_stride, g->k));
+  const void* w_gate = of(a[2], "w_gate", g->type, w);
+  const void* w_up = of(a[3], "w_up", g->type, w);
+  const int32_t* offsets = (const int32_t*)of(a[4], "offsets", kIndex, vector((int64_t)g->n_groups + 1));
+  void* h = of(a[5], "h", g->type, matrix(rows, g->h_stride, g->n));
+  void* gate = of(a[6], "gate", g->type, kept);
+  void* up = of(a[7], "up", g->type, kept);
+  int32_t* status = (int32_t*)of(a[8], "status", kIndex, vector(1));
+  void* stream = stream_of(a[9]);
+  return without_gil([&] {
+    return entry.gated_forward(g.get(), x, w_gate, w_up, offsets, rows, h, gate, up, status, stream);
+  });
+}
+
+int gated_backward_h(PyObject* const* a) {
+  const Plan<moe_gated> g(a[0], "gated");
+  const int64_t rows = rows_of(a[1], "dy");
+  const Extent kept = matrix(rows, g->gate_stride, g->n);
+  Tensors of;
+  const void* dy = of(a[1], "dy", g->type, matrix(rows, g->y_stride, g->k));
+  const void* w_down = of(a[2], "w_down", g->type, {g->n_groups, g->down_group_stride, g->k, g->down_stride, g->n});
+  const void* gate = of(a[3], "gate", g->type, kept);
+  const void* up = of(a[4], "up", g->type, kept);
+  const int32_t* offsets = (const int32_t*)of(a[5], "offsets", kIndex, vector((int64_t)g->n_groups + 1));
+  void* dgate = of(a[6], "dgate", g->type, kept);
+  void* dup = of(a[7], "dup", g->type, kept);
+  void* h = of(a[8], "h", g->type, matrix(rows, g->h_stride, g->n));
+  int32_t* status = (int32_t*)of(a[9], "status", kIndex, vector(1));
+  void* stream = stream_of(a[10]);
+  return without_gil([&] {
+    return entry.gated_backward_h(g.get(), dy, w_down, gate, up, offsets, rows, dgate, dup, h, status, stream);
+  });
+}
+
+int gated_backward_x(PyObject* const* a) {
+  const Plan<moe_gated> g(a[0], "gated");
+  const int64_t rows = rows_of(a[1], "dgate");
+  const Extent w = {g->n_groups, g->w_group_stride, g->n, g->w_stride, g->k}, kept = matrix(rows, g->gate_stride, g->n);
+  Tensors of;
+  const void* dgate = of(a[1], "dgate", g->type, kept);
+  const void* dup = of(a[2], "dup", g->type, kept);
+  const void* w_gate = of(a[3], "w_gate", g->type, w);
+  const void* w_up = of(a[4], "w_up", g->type, w);
+  const int32_t* offsets = (const int32_t*)of(a[5], "offsets", kIndex, vector((int64_t)g->n_groups + 1));
+  void* dx = of(a[6], "dx", g->dx_type, matrix(rows, g->x_stride, g->k));
+  int32_t* status = (int32_t*)of(a[7], "status", kIndex, vector(1));
+  void* stream = stream_of(a[8]);
+  return without_gil([&] {
+    return entry.gated_backward_x(g.get(), dgate, dup, w_gate, w_up, offsets, rows, dx, status, stream);
+  });
+}
+
 // bind(MoeError, addresses of the entry points in the order of `entry`)
 PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
   constexpr int kEntries = sizeof(entry) / sizeof(void*);
@@ -346,6 +427,9 @@ PyMethodDef methods[] = {MOE_METHOD("bind", bind),
                          MOE_METHOD("grouped_backward_x", (function<7, grouped<kInput>>)),
                          MOE_METHOD("grouped_backward_w", (function<7, grouped<kWeight>>)),
                          MOE_METHOD("adapter_project", (function<8, adapter_project>)),
+                         MOE_METHOD("gated_forward", (function<10, gated_forward>)),
+                         MOE_METHOD("gated_backward_h", (function<11, gated_backward_h>)),
+                         MOE_METHOD("gated_backward_x", (function<9, gated_backward_x>)),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensors", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
