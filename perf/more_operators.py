@@ -223,6 +223,8 @@ def prepare(case, seed):
     s["case"] = case
     if own:
         s.update(_handles(case))
+        if case["op"] in ("mx", "mx gated"):
+            s["x"] = (s["x"][0].to(torch.uint8), s["x"][1])   # the library takes codes as bytes
     return s
 
 
