@@ -570,6 +570,64 @@ int moe_gated_backward_h(const moe_gated* g, const void* dy, const void* w_down,
 int moe_gated_backward_x(const moe_gated* g, const void* dgate, const void* dup, const void* w_gate, const void* w_up,
                          const int32_t* offsets, int64_t rows, void* dx, int32_t* status, void* stream);
 
+/* Microscaled 4-bit floats: a row of k elements is (k + 1) / 2 bytes of codes and
+ * (k + 31) / 32 bytes of scales. A code is a sign (8) and 0 .5 1 1.5 2 3 4 6
+ * (e2m1), the even element of a byte in its low half; a scale s of each 32
+ * elements of the row is 2^(s - 127) (e8m0), 255: the block is NaN.
+ *   quantise    t = the block's largest magnitude; scale 2^(floor(log2 t) - 2)
+ *               (MOE_MX_FLOOR) or the least power of two with t <= 6 of it
+ *               (MOE_MX_CEIL), 2^-127 at least; elements to the nearest, ties to even, at
+ *               most 6 (MOE_MX_FLOOR: of magnitudes up to 8). A block that holds
+ *               an infinity or NaN is NaN (its codes 0); the half byte past an odd k is 0.
+ *   dequantise  element * scale, rounded to the type
+ *   x  type [rows][k]   codes  bytes [rows][(k + 1) / 2]   scales  bytes [rows][(k + 31) / 32]
+ * Any k from 1 to MOE_MX_MAX_K, stride and alignment; rows may be 0, and is at
+ * most MOE_MX_MAX_ROWS; fewer than 2^32 blocks in a call. Outputs must not overlap inputs. */
+#define MOE_MX_FLOOR 0
+#define MOE_MX_CEIL 1
+#define MOE_MX_MAX_K (1 << 22)
+#define MOE_MX_MAX_ROWS 0x7fffffff
+typedef struct moe_mx_rows {
+  int32_t k;
+  int32_t type;          /* of x: MOE_TYPE_*                   */
+  int32_t scale;         /* MOE_MX_FLOOR or MOE_MX_CEIL        */
+  int64_t x_stride;      /* elements between rows of x, >= k   */
+  int64_t code_stride;   /* bytes between rows of codes        */
+  int64_t scale_stride;  /* bytes between rows of scales       */
+} moe_mx_rows;
+int moe_mx_quantise(const moe_mx_rows* p, const void* x, int64_t rows, void* codes, void* scales, void* stream);
+int moe_mx_dequantise(const moe_mx_rows* p, const void* codes, const void* scales, int64_t rows, void* x, void* stream);
+
+/* Products of operands in that format grouped by expert, rows and offsets as for
+ * the grouped products; f32 sums, one rounding:
+ *   forward  y[r] = W[g] x[r]
+ *   gated    h[r] = act(min(Wg[g] x[r], L)) * clamp(Wu[g] x[r], -L, L)
+ *   x, x_scale  [rows]   w, w_scale (of gate and up too)  [n_groups][n]   rows of the format over k
+ *   y, h  out_type [rows][n]
+ * Every output is written whole: rows of no group are 0. A NaN block makes the
+ * outputs that it enters NaN. rows may be 0, and is at most MOE_GROUPED_MAX_ROWS.
+ * Any n, k, stride and alignment; codes whose rows start 16-byte aligned with
+ * scales 4-byte aligned take the faster path. Outputs must not overlap inputs.
+ * The same call gives the same bits. status: MOE_STATUS_BAD_OFFSETS, may be NULL; outputs are unspecified then. */
+typedef struct moe_mx {
+  int32_t n_groups, n, k;
+  int32_t out_type;              /* MOE_TYPE_*                                 */
+  int32_t act;                   /* moe_mx_gated: MOE_ACT_*                    */
+  float limit;                   /* moe_mx_gated: finite, >= 0                 */
+  int64_t x_stride;              /* bytes between rows of x's codes            */
+  int64_t x_scale_stride;        /* and of its scales                          */
+  int64_t y_stride;              /* elements between rows of y and h, >= n     */
+  int64_t w_stride;              /* bytes between rows of w's codes            */
+  int64_t w_group_stride;        /* and from one group's to the next           */
+  int64_t w_scale_stride;        /* the same of its scales                     */
+  int64_t w_scale_group_stride;
+} moe_mx;
+int moe_mx_forward(const moe_mx* m, const void* x, const void* x_scale, const void* w, const void* w_scale,
+                   const int32_t* offsets, int64_t rows, void* y, int32_t* status, void* stream);
+int moe_mx_gated(const moe_mx* m, const void* x, const void* x_scale, const void* w_gate, const void* w_gate_scale,
+                 const void* w_up, const void* w_up_scale, const int32_t* offsets, int64_t rows, void* h, int32_t* status,
+                 void* stream);
+
 /* A shared projection with one low-rank adapter per token:
  *   out[t] = W x[t] + factor[a] B[a] (A[a] x[t]),  a = index[t]; a = -1: W x[t].
  * Products of 16-bit elements, f32 sums, one rounding at the end. factor A x is

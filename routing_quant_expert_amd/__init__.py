@@ -12,6 +12,7 @@ from .binding import (MOE_K_DOWN, MOE_K_DOWN2, MOE_K_GATEUP, MOE_K_GATEUP2, MOE_
                       workspace_bytes, workspace_init, workspace_layout)
 from .binding import (MOE_ADAPTER_MAX_ADAPTERS, MOE_ADAPTER_MAX_RANK, MOE_ADAPTER_MAX_TOKENS, MOE_GROUPED_MAX_GROUPS, MOE_GROUPED_MAX_ROWS, MOE_GROUPED_MAX_STRIDE, MOE_JOIN_MAX_DIM, MOE_STATUS_BAD_ADAPTER, MOE_STATUS_BAD_OFFSETS, MOE_TYPE_BF16, MOE_TYPE_F32,
                       MOE_TYPE_FP16, Adapters, Grouped, Join,
+                      MOE_MX_CEIL, MOE_MX_FLOOR, MOE_MX_MAX_K, MOE_MX_MAX_ROWS, Mx, MxRows, mx_dequantise, mx_forward, mx_gated, mx_quantise,
                       MOE_ACT_GELU, MOE_ACT_SILU, Gated, act_code, gated_backward_h, gated_backward_x, gated_forward,
                       adapter_project, adapter_workspace_bytes, grouped_backward_w, grouped_backward_x, grouped_forward, join_backward, join_forward, join_workspace_bytes, type_code)
 
@@ -28,4 +29,6 @@ __all__ = [
     "MOE_GROUPED_MAX_ROWS", "MOE_GROUPED_MAX_STRIDE", "Adapters", "adapter_project", "adapter_workspace_bytes", "MOE_ADAPTER_MAX_ADAPTERS",
     "MOE_ADAPTER_MAX_RANK", "MOE_ADAPTER_MAX_TOKENS",
     "Gated", "act_code", "gated_forward", "gated_backward_h", "gated_backward_x", "MOE_ACT_SILU", "MOE_ACT_GELU",
+    "MxRows", "mx_quantise", "mx_dequantise", "Mx", "mx_forward", "mx_gated", "MOE_MX_FLOOR", "MOE_MX_CEIL", "MOE_MX_MAX_K",
+    "MOE_MX_MAX_ROWS",
 ]

@@ -118,6 +118,10 @@ def lib():
         L.moe_gated_forward.argtypes = [_VP] * 5 + [ctypes.c_int64] + [_VP] * 5
         L.moe_gated_backward_h.argtypes = [_VP] * 6 + [ctypes.c_int64] + [_VP] * 5
         L.moe_gated_backward_x.argtypes = [_VP] * 6 + [ctypes.c_int64] + [_VP] * 3
+        L.moe_mx_quantise.argtypes = [_VP] * 2 + [ctypes.c_int64] + [_VP] * 3
+        L.moe_mx_dequantise.argtypes = [_VP] * 3 + [ctypes.c_int64] + [_VP] * 2
+        L.moe_mx_forward.argtypes = [_VP] * 6 + [ctypes.c_int64] + [_VP] * 3
+        L.moe_mx_gated.argtypes = [_VP] * 8 + [ctypes.c_int64] + [_VP] * 3
         L.moe_last_error.restype = ctypes.c_char_p
         _lib = L
     return _lib
@@ -350,6 +354,9 @@ MOE_GROUPED_MAX_GROUPS = 1024
 MOE_GROUPED_MAX_STRIDE = 1 << 22
 MOE_GROUPED_MAX_ROWS = 0x7fffff00
 MOE_ACT_SILU, MOE_ACT_GELU = 0, 1
+MOE_MX_FLOOR, MOE_MX_CEIL = 0, 1
+MOE_MX_MAX_K = 1 << 22
+MOE_MX_MAX_ROWS = 0x7fffffff
 MOE_ADAPTER_MAX_ADAPTERS = 1024
 MOE_ADAPTER_MAX_RANK = 1024
 MOE_ADAPTER_MAX_TOKENS = 1 << 20
@@ -387,7 +394,8 @@ def _tensors():
         native.bind(MoeError, *(ctypes.cast(f, _VP).value for f in (
             L.moe_join_forward, L.moe_join_backward, L.moe_grouped_forward, L.moe_grouped_backward_x,
             L.moe_grouped_backward_w, L.moe_adapter_project, L.moe_gated_forward, L.moe_gated_backward_h,
-            L.moe_gated_backward_x, L.moe_last_error)))
+            L.moe_gated_backward_x, L.moe_mx_quantise, L.moe_mx_dequantise, L.moe_mx_forward, L.moe_mx_gated,
+            L.moe_last_error)))
         _native = native
     return _native
 
@@ -503,6 +511,65 @@ def gated_backward_h(g: Gated, dy, w_down, gate, up, offsets, dgate, dup, h=None
 def gated_backward_x(g: Gated, dgate, dup, w_gate, w_up, offsets, dx, status=None, stream=None):
     """dx[r] = w_gate[group of r]^T @ dgate[r] + w_up[group of r]^T @ dup[r]."""
     _tensors().gated_backward_x(g, dgate, dup, w_gate, w_up, offsets, dx, status, _stream(stream))
+
+
+class MxRows(ctypes.Structure):
+    """moe_mx_rows: rows of k elements of dtype and their microscaled 4-bit form, codes [rows, (k + 1) // 2] and scales
+    [rows, (k + 31) // 32] bytes. scale "floor" or "ceil": which power of two the largest of 32 elements gives. Strides
+    (of x in elements, of the others in bytes) default to contiguous rows."""
+    _fields_ = [("k", ctypes.c_int32), ("type", ctypes.c_int32), ("scale", ctypes.c_int32), ("x_stride", ctypes.c_int64),
+                ("code_stride", ctypes.c_int64), ("scale_stride", ctypes.c_int64)]
+
+    def __init__(self, k: int, dtype, scale="floor", x_stride: int | None = None, code_stride: int | None = None,
+                 scale_stride: int | None = None):
+        rule = scale if isinstance(scale, int) else {"floor": MOE_MX_FLOOR, "ceil": MOE_MX_CEIL}.get(scale)
+        if rule is None:
+            raise MoeError(-1, f"scale must be floor or ceil (got {scale!r})")
+        super().__init__(k, type_code(dtype), rule, k if x_stride is None else x_stride,
+                         (k + 1) // 2 if code_stride is None else code_stride,
+                         (k + 31) // 32 if scale_stride is None else scale_stride)
+
+
+def mx_quantise(p: MxRows, x, codes, scales, stream=None):
+    """Rows of x to 4-bit codes and the scales of 32 elements each."""
+    _tensors().mx_quantise(p, x, codes, scales, _stream(stream))
+
+
+def mx_dequantise(p: MxRows, codes, scales, x, stream=None):
+    """The values that codes and scales stand for, rounded to x's type."""
+    _tensors().mx_dequantise(p, codes, scales, x, _stream(stream))
+
+
+class Mx(ctypes.Structure):
+    """moe_mx: products grouped by expert of rows and weights in microscaled 4-bit floats, out: the outputs' type; act and
+    limit: as Gated, for mx_gated. Strides (of the outputs in elements, of the others in bytes) default to contiguous rows
+    and weights."""
+    _fields_ = [("n_groups", ctypes.c_int32), ("n", ctypes.c_int32), ("k", ctypes.c_int32), ("out_type", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("limit", ctypes.c_float), ("x_stride", ctypes.c_int64),
+                ("x_scale_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64), ("w_stride", ctypes.c_int64),
+                ("w_group_stride", ctypes.c_int64), ("w_scale_stride", ctypes.c_int64),
+                ("w_scale_group_stride", ctypes.c_int64)]
+
+    def __init__(self, n_groups: int, n: int, k: int, out, act="silu", limit: float | None = None,
+                 x_stride: int | None = None, x_scale_stride: int | None = None, y_stride: int | None = None,
+                 w_stride: int | None = None, w_group_stride: int | None = None, w_scale_stride: int | None = None,
+                 w_scale_group_stride: int | None = None):
+        codes, blocks = (k + 1) // 2, (k + 31) // 32
+        ws, ss = codes if w_stride is None else w_stride, blocks if w_scale_stride is None else w_scale_stride
+        super().__init__(n_groups, n, k, type_code(out), act_code(act), limit or 0.0, codes if x_stride is None else x_stride,
+                         blocks if x_scale_stride is None else x_scale_stride, n if y_stride is None else y_stride, ws,
+                         n * ws if w_group_stride is None else w_group_stride, ss,
+                         n * ss if w_scale_group_stride is None else w_scale_group_stride)
+
+
+def mx_forward(m: Mx, x, x_scale, w, w_scale, offsets, y, status=None, stream=None):
+    """y[r] = w[group of r] @ x[r] of codes and scales (as mx_quantise makes them)."""
+    _tensors().mx_forward(m, x, x_scale, w, w_scale, offsets, y, status, _stream(stream))
+
+
+def mx_gated(m: Mx, x, x_scale, w_gate, w_gate_scale, w_up, w_up_scale, offsets, h, status=None, stream=None):
+    """h[r] = act(w_gate[group of r] @ x[r]) * (w_up[group of r] @ x[r]) of codes and scales."""
+    _tensors().mx_gated(m, x, x_scale, w_gate, w_gate_scale, w_up, w_up_scale, offsets, h, status, _stream(stream))
 
 
 class Adapters(ctypes.Structure):

@@ -28,22 +28,6 @@ struct GatedArgs : Groups {
   int64_t x_stride, h_stride, gate_stride, y_stride, w_stride, w_group, down_stride, down_group;
 };
 
-// The workgroup's tile in scalar registers (it is the same in every lane).
-template <typename G>
-__device__ __forceinline__ Tile my_tile(const Groups& a, int width) {
-  Tile t = find_tile<G::kQ>(a, (width + G::kP - 1) / G::kP);
-  t.group = __builtin_amdgcn_readfirstlane(t.group);
-  t.row = __builtin_amdgcn_readfirstlane(t.row);
-  t.rows = __builtin_amdgcn_readfirstlane(t.rows);
-  t.p = __builtin_amdgcn_readfirstlane(t.p);
-  return t;
-}
-
-template <typename T>
-__device__ __forceinline__ int64_t elements_between(const T* a, const T* b) {
-  return ((int64_t)(intptr_t)b - (int64_t)(intptr_t)a) / (int64_t)sizeof(T);
-}
-
 template <typename T, typename G>
 __global__ __launch_bounds__(G::NT, 2) void k_gated(GatedArgs a, const T* __restrict__ x, const T* __restrict__ wg,
                                                  const T* __restrict__ wu, T* __restrict__ h, T* __restrict__ gate,
@@ -60,13 +44,7 @@ __global__ __launch_bounds__(G::NT, 2) void k_gated(GatedArgs a, const T* __rest
   typename G::Acc acc = {};
   G::run(P, Q, none ? 0 : a.k, lds, acc);
   f32x4 g[G::NP / 2][G::NQ], u[G::NP / 2][G::NQ];
-#pragma unroll
-  for (int i = 0; i < G::NP / 2; ++i)
-#pragma unroll
-    for (int j = 0; j < G::NQ; ++j) {
-      g[i][j] = acc[2 * i][j];
-      u[i][j] = acc[2 * i + 1][j];
-    }
+  G::part(acc, g, u);
   auto row = [&](int q) { return q < t.rows ? q : -1; };
   if (gate) {
     G::store_to(g, gate + t.row * a.gate_stride + p0, a.gate_stride, pn, row);

@@ -236,25 +236,165 @@ __device__ __forceinline__ void wait_steps(int steps) {
   wait_vmcnt<N * MAX + MORE>();
 }
 
-// WP x WQ waves of BP/WP x BQ/WQ outputs each; ST slots of one step in LDS.
-// DMA: 16-byte aligned rows, brought into LDS directly; otherwise through registers, any alignment.
-template <typename T, bool PCOL, bool QCOL, int BP, int BQ, int WP, int WQ, int ST, bool DMA, bool GATHER = false,
-          Two TWO = kSingle>
-struct Gemm {
+// The sums of a workgroup's tile of BP x BQ outputs as its WP x WQ waves hold them (PAIRS: BP / 2 outputs, of two
+// matrices each), and their way to memory.
+template <int BP, int BQ, int WP, int WQ, bool PAIRS>
+struct TileOut {
   static constexpr int NT = 64 * WP * WQ;
-  typedef TileOf<T, PCOL, BP, NT, false, TWO == kRowPairs> PT;
-  typedef TileOf<T, QCOL, BQ, NT, GATHER> QT;
-  static constexpr int kSlots = DMA ? ST : 2;
-  static constexpr int kSlot = PT::kBytes + QT::kBytes;
-  static constexpr int kLds = kSlots * kSlot;
-  static constexpr int kP = TWO == kRowPairs ? BP / 2 : BP, kQ = BQ;   // outputs of a tile
+  static constexpr int kP = PAIRS ? BP / 2 : BP, kQ = BQ;   // outputs of a tile
   static constexpr int NP = BP / WP / 16, NQ = BQ / WQ / 16;
   typedef f32x4 Acc[NP][NQ];
   static constexpr int kStores = NP * NQ;   // store instructions of a wave's whole part of a tile
 
   __device__ static __forceinline__ int wave_p() { return (threadIdx.x >> 6) % WP * (BP / WP); }
   __device__ static __forceinline__ int wave_q() { return (threadIdx.x >> 6) / WP * (BQ / WQ); }
+  // The wave's first output column.
+  __device__ static __forceinline__ int wave_out() { return PAIRS ? wave_p() / 2 : wave_p(); }
+  // PAIRS: the sums of the first and of the second matrix.
+  template <int N>
+  __device__ static __forceinline__ void part(const Acc& acc, f32x4 (&first)[N][NQ], f32x4 (&second)[N][NQ]) {
+    static_assert(2 * N == NP);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int j = 0; j < NQ; ++j) {
+        first[i][j] = acc[2 * i][j];
+        second[i][j] = acc[2 * i + 1][j];
+      }
+  }
 
+  // Writes the tile's first `pn` outputs of each row at `out`, rows `ld` apart;
+  // row(q) is the place of tile row q (below 0: not stored).
+  template <int N, typename U, typename Row>
+  __device__ static __forceinline__ void store_to(const f32x4 (&acc)[N][NQ], U* out, int64_t ld, int pn, Row& row) {
+    if constexpr (N % 2 == 0) {
+      if (pn >= kP) return store_whole(acc, out, ld, row);
+    }
+    store_part(acc, out, ld, pn, row);
+  }
+  template <int N, typename U, typename Row>
+  __device__ static __forceinline__ void store_part(const f32x4 (&acc)[N][NQ], U* out, int64_t ld, int pn, Row& row) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int j = 0; j < NQ; ++j) {
+      const int64_t q = row(wave_q() + 16 * j + (lane & 15));
+      if (q < 0) continue;
+      const int p = wave_out() + 4 * (lane >> 4);
+#pragma unroll
+      for (int i = 0; i < N; ++i) store_quad(out + q * ld + p + 16 * i, acc[i][j], pn - p - 16 * i);
+    }
+  }
+  // Lanes q and q + 8 of 16 exchange a quad, so that a store writes 32
+  // neighbouring outputs of 8 rows instead of 16 of 16 rows.
+  template <int N, typename U, typename Row>
+  __device__ static __forceinline__ void store_whole(const f32x4 (&acc)[N][NQ], U* out, int64_t ld, Row& row) {
+    const int lane = threadIdx.x & 63, upper = lane >> 3 & 1;
+#pragma unroll
+    for (int j = 0; j < NQ; ++j) {
+      const int64_t qa = row(wave_q() + 16 * j + (lane & 7)), qb = row(wave_q() + 16 * j + 8 + (lane & 7));
+      U* const at = out + wave_out() + 16 * upper + 4 * (lane >> 4);
+#pragma unroll
+      for (int i = 0; i < N; i += 2) {
+        f32x4 a = acc[i][j], b = acc[i + 1][j], x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[e] = dpp_f32<kDppRor8>(upper ? a[e] : b[e]);
+          a[e] = upper ? x[e] : a[e];
+          b[e] = upper ? b[e] : x[e];
+        }
+        if (qa >= 0) store_quad(at + qa * ld + 16 * i, a, 4);
+        if (qb >= 0) store_quad(at + qb * ld + 16 * i, b, 4);
+      }
+    }
+  }
+
+  // The same places for a use of its own: load(q, p, n) at tile row q, output p and the n - 1 after it, for all of a
+  // row of sums before use(q, p, n, sums, loaded) of each. What a lane loads is what it is given to use.
+  template <int N, typename Row, typename Load, typename Use>
+  __device__ static __forceinline__ void each_quad(const f32x4 (&acc)[N][NQ], int pn, Row&& row, Load&& load, Use&& use) {
+    const int lane = threadIdx.x & 63, upper = lane >> 3 & 1;
+    typedef decltype(load((int64_t)0, 0, 0)) Loaded;
+    if (N % 2 == 0 && pn >= kP) {
+#pragma unroll
+      for (int j = 0; j < NQ; ++j) {
+        const int64_t qa = row(wave_q() + 16 * j + (lane & 7)), qb = row(wave_q() + 16 * j + 8 + (lane & 7));
+        const int p = wave_out() + 16 * upper + 4 * (lane >> 4);
+        Loaded la[N / 2], lb[N / 2];
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+          if (qa >= 0) la[i] = load(qa, p + 32 * i, 4);
+          if (qb >= 0) lb[i] = load(qb, p + 32 * i, 4);
+        }
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+          f32x4 a = acc[2 * i][j], b = acc[(2 * i + 1) % N][j], x;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[e] = dpp_f32<kDppRor8>(upper ? a[e] : b[e]);
+            a[e] = upper ? x[e] : a[e];
+            b[e] = upper ? b[e] : x[e];
+          }
+          if (qa >= 0) use(qa, p + 32 * i, 4, a, la[i]);
+          if (qb >= 0) use(qb, p + 32 * i, 4, b, lb[i]);
+        }
+      }
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < NQ; ++j) {
+      const int64_t q = row(wave_q() + 16 * j + (lane & 15));
+      if (q < 0) continue;
+      const int p = wave_out() + 4 * (lane >> 4);
+      Loaded l[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) l[i] = load(q, p + 16 * i, pn - p - 16 * i);
+#pragma unroll
+      for (int i = 0; i < N; ++i) use(q, p + 16 * i, pn - p - 16 * i, acc[i][j], l[i]);
+    }
+  }
+
+  // The first n of four elements; the others are 0.
+  template <typename U>
+  __device__ static __forceinline__ f32x4 load_quad(const U* at, int n) {
+    typedef U quad __attribute__((ext_vector_type(4)));
+    quad v = {};
+    if (n >= 4) {
+      __builtin_memcpy(&v, at, sizeof(v));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (i < n) v[i] = at[i];
+    }
+    return __builtin_convertvector(v, f32x4);
+  }
+  // The first n of four outputs, rounded to nearest even in U.
+  template <typename U>
+  __device__ static __forceinline__ void store_quad(U* at, f32x4 f, int n) {
+    typedef U quad __attribute__((ext_vector_type(4)));
+    const quad v = __builtin_convertvector(f, quad);
+    if (n >= 4) {
+      __builtin_memcpy(at, &v, sizeof(v));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (i < n) at[i] = v[i];
+    }
+  }
+};
+
+// WP x WQ waves of BP/WP x BQ/WQ outputs each; ST slots of one step in LDS.
+// DMA: 16-byte aligned rows, brought into LDS directly; otherwise through registers, any alignment.
+template <typename T, bool PCOL, bool QCOL, int BP, int BQ, int WP, int WQ, int ST, bool DMA, bool GATHER = false,
+          Two TWO = kSingle>
+struct Gemm : TileOut<BP, BQ, WP, WQ, TWO == kRowPairs> {
+  typedef TileOut<BP, BQ, WP, WQ, TWO == kRowPairs> Out;
+  using Out::NT, Out::NP, Out::NQ, Out::kStores, Out::wave_p, Out::wave_q;
+  typedef typename Out::Acc Acc;
+  typedef TileOf<T, PCOL, BP, NT, false, TWO == kRowPairs> PT;
+  typedef TileOf<T, QCOL, BQ, NT, GATHER> QT;
+  static constexpr int kSlots = DMA ? ST : 2;
+  static constexpr int kSlot = PT::kBytes + QT::kBytes;
+  static constexpr int kLds = kSlots * kSlot;
   // kRowPairs: the rows that this thread brings in are those of the first matrix or of the second (8 rows to 64 chunks).
   __device__ static __forceinline__ bool second_rows() { return threadIdx.x >> 7 & 1; }
 
@@ -583,129 +723,11 @@ struct Gemm {
     return more;
   }
 
-  // Writes the tile's first `pn` outputs of each row at `out` (type f32 or T),
-  // rows `ld` apart; row(q) is the place of tile row q (below 0: not stored).
+  // Writes the tile's outputs as f32 or T.
   template <int N, typename Row>
   __device__ static __forceinline__ void store(const f32x4 (&acc)[N][NQ], void* out, bool f32, int64_t ld, int pn, Row&& row) {
-    if (f32) store_to(acc, (float*)out, ld, pn, row);
-    else store_to(acc, (T*)out, ld, pn, row);
-  }
-  template <int N, typename U, typename Row>
-  __device__ static __forceinline__ void store_to(const f32x4 (&acc)[N][NQ], U* out, int64_t ld, int pn, Row& row) {
-    if constexpr (N % 2 == 0) {
-      if (pn >= kP) return store_whole(acc, out, ld, row);
-    }
-    store_part(acc, out, ld, pn, row);
-  }
-  // The wave's first output column.
-  __device__ static __forceinline__ int wave_out() { return TWO == kRowPairs ? wave_p() / 2 : wave_p(); }
-  template <int N, typename U, typename Row>
-  __device__ static __forceinline__ void store_part(const f32x4 (&acc)[N][NQ], U* out, int64_t ld, int pn, Row& row) {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int j = 0; j < NQ; ++j) {
-      const int64_t q = row(wave_q() + 16 * j + (lane & 15));
-      if (q < 0) continue;
-      const int p = wave_out() + 4 * (lane >> 4);
-#pragma unroll
-      for (int i = 0; i < N; ++i) store_quad(out + q * ld + p + 16 * i, acc[i][j], pn - p - 16 * i);
-    }
-  }
-  // Lanes q and q + 8 of 16 exchange a quad, so that a store writes 32
-  // neighbouring outputs of 8 rows instead of 16 of 16 rows.
-  template <int N, typename U, typename Row>
-  __device__ static __forceinline__ void store_whole(const f32x4 (&acc)[N][NQ], U* out, int64_t ld, Row& row) {
-    const int lane = threadIdx.x & 63, upper = lane >> 3 & 1;
-#pragma unroll
-    for (int j = 0; j < NQ; ++j) {
-      const int64_t qa = row(wave_q() + 16 * j + (lane & 7)), qb = row(wave_q() + 16 * j + 8 + (lane & 7));
-      U* const at = out + wave_out() + 16 * upper + 4 * (lane >> 4);
-#pragma unroll
-      for (int i = 0; i < N; i += 2) {
-        f32x4 a = acc[i][j], b = acc[i + 1][j], x;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[e] = dpp_f32<kDppRor8>(upper ? a[e] : b[e]);
-          a[e] = upper ? x[e] : a[e];
-          b[e] = upper ? b[e] : x[e];
-        }
-        if (qa >= 0) store_quad(at + qa * ld + 16 * i, a, 4);
-        if (qb >= 0) store_quad(at + qb * ld + 16 * i, b, 4);
-      }
-    }
-  }
-
-  // The same places for a use of its own: load(q, p, n) at tile row q, output p and the n - 1 after it, for all of a
-  // row of sums before use(q, p, n, sums, loaded) of each. What a lane loads is what it is given to use.
-  template <int N, typename Row, typename Load, typename Use>
-  __device__ static __forceinline__ void each_quad(const f32x4 (&acc)[N][NQ], int pn, Row&& row, Load&& load, Use&& use) {
-    const int lane = threadIdx.x & 63, upper = lane >> 3 & 1;
-    typedef decltype(load((int64_t)0, 0, 0)) Loaded;
-    if (N % 2 == 0 && pn >= kP) {
-#pragma unroll
-      for (int j = 0; j < NQ; ++j) {
-        const int64_t qa = row(wave_q() + 16 * j + (lane & 7)), qb = row(wave_q() + 16 * j + 8 + (lane & 7));
-        const int p = wave_out() + 16 * upper + 4 * (lane >> 4);
-        Loaded la[N / 2], lb[N / 2];
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i) {
-          if (qa >= 0) la[i] = load(qa, p + 32 * i, 4);
-          if (qb >= 0) lb[i] = load(qb, p + 32 * i, 4);
-        }
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i) {
-          f32x4 a = acc[2 * i][j], b = acc[(2 * i + 1) % N][j], x;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            x[e] = dpp_f32<kDppRor8>(upper ? a[e] : b[e]);
-            a[e] = upper ? x[e] : a[e];
-            b[e] = upper ? b[e] : x[e];
-          }
-          if (qa >= 0) use(qa, p + 32 * i, 4, a, la[i]);
-          if (qb >= 0) use(qb, p + 32 * i, 4, b, lb[i]);
-        }
-      }
-      return;
-    }
-#pragma unroll
-    for (int j = 0; j < NQ; ++j) {
-      const int64_t q = row(wave_q() + 16 * j + (lane & 15));
-      if (q < 0) continue;
-      const int p = wave_out() + 4 * (lane >> 4);
-      Loaded l[N];
-#pragma unroll
-      for (int i = 0; i < N; ++i) l[i] = load(q, p + 16 * i, pn - p - 16 * i);
-#pragma unroll
-      for (int i = 0; i < N; ++i) use(q, p + 16 * i, pn - p - 16 * i, acc[i][j], l[i]);
-    }
-  }
-
-  // The first n of four elements; the others are 0.
-  template <typename U>
-  __device__ static __forceinline__ f32x4 load_quad(const U* at, int n) {
-    typedef U quad __attribute__((ext_vector_type(4)));
-    quad v = {};
-    if (n >= 4) {
-      __builtin_memcpy(&v, at, sizeof(v));
-    } else {
-#pragma unroll
-      for (int i = 0; i < 3; ++i)
-        if (i < n) v[i] = at[i];
-    }
-    return __builtin_convertvector(v, f32x4);
-  }
-  // The first n of four outputs, rounded to nearest even in U.
-  template <typename U>
-  __device__ static __forceinline__ void store_quad(U* at, f32x4 f, int n) {
-    typedef U quad __attribute__((ext_vector_type(4)));
-    const quad v = __builtin_convertvector(f, quad);
-    if (n >= 4) {
-      __builtin_memcpy(at, &v, sizeof(v));
-    } else {
-#pragma unroll
-      for (int i = 0; i < 3; ++i)
-        if (i < n) at[i] = v[i];
-    }
+    if (f32) Out::store_to(acc, (float*)out, ld, pn, row);
+    else Out::store_to(acc, (T*)out, ld, pn, row);
   }
 };
 

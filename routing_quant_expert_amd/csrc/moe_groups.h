@@ -80,6 +80,23 @@ __device__ __forceinline__ Tile find_tile(const Groups& a, int np) {
   return {sel * U + s - 1, glo + rt * BQ, min(BQ, ghi - (glo + rt * BQ)), pt};
 }
 
+// The workgroup's tile in scalar registers (it is the same in every lane).
+template <typename G>
+__device__ __forceinline__ Tile my_tile(const Groups& a, int width) {
+  Tile t = find_tile<G::kQ>(a, (width + G::kP - 1) / G::kP);
+  t.group = __builtin_amdgcn_readfirstlane(t.group);
+  t.row = __builtin_amdgcn_readfirstlane(t.row);
+  t.rows = __builtin_amdgcn_readfirstlane(t.rows);
+  t.p = __builtin_amdgcn_readfirstlane(t.p);
+  return t;
+}
+
+// (Of operands that need not lie in one allocation.)
+template <typename T>
+__device__ __forceinline__ int64_t elements_between(const T* a, const T* b) {
+  return ((int64_t)(intptr_t)b - (int64_t)(intptr_t)a) / (int64_t)sizeof(T);
+}
+
 // The first workgroup reports offsets that do not ascend or leave [0, rows].
 __device__ __forceinline__ void report(const Groups& a) {
   if (!a.status || blockIdx.x) return;

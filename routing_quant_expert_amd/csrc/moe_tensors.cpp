@@ -1,6 +1,6 @@
 // The calls of the operators beside the layer on torch tensors (Python module
 // `_tensors`): every tensor is held against the call's description (moe_join,
-// moe_grouped, moe_adapters, moe_gated), then the entry point of include/moe.h is called.
+// moe_grouped, moe_adapters, moe_gated, moe_mx), then the entry point of include/moe.h is called.
 // Native because the host's part of a small call is all of it: a join_forward
 // of one row takes 3.6 us so, 4.6 through ctypes without the checks of its seven
 // tensors and 5.4 with them in Python.
@@ -36,6 +36,10 @@ struct {
   decltype(&::moe_gated_forward) gated_forward;
   decltype(&::moe_gated_backward_h) gated_backward_h;
   decltype(&::moe_gated_backward_x) gated_backward_x;
+  decltype(&::moe_mx_quantise) mx_quantise;
+  decltype(&::moe_mx_dequantise) mx_dequantise;
+  decltype(&::moe_mx_forward) mx_forward;
+  decltype(&::moe_mx_gated) mx_gated;
   decltype(&::moe_last_error) last_error;
 } entry;
 
@@ -80,6 +84,7 @@ Extent vector(int64_t n) { return {1, 0, 1, 0, n}; }
 Extent matrix(int64_t rows, int64_t stride, int64_t width) { return {1, 0, rows, stride, width}; }
 
 constexpr int kIndex = 16;   // 32-bit integers; otherwise MOE_TYPE_*
+constexpr int kCodes = 17, kScales = 18;   // bytes: pairs of 4-bit floats, powers of two
 
 // Elements of a tensor in the units of the description (bytes of `e`): sizes and strides of integers that stand for others' bits scale.
 struct View {
@@ -130,10 +135,14 @@ void* address(PyObject* o, const char* what, int type, const Extent& x) {
   if (type == kIndex) {
     if (s != at::kInt && s != at::kUInt32) fail(what, "must be int32");
   } else {
-    const at::ScalarType want = type == MOE_TYPE_BF16 ? at::kBFloat16 : type == MOE_TYPE_FP16 ? at::kHalf : at::kFloat;
+    const at::ScalarType want = type == MOE_TYPE_BF16   ? at::kBFloat16
+                                : type == MOE_TYPE_FP16 ? at::kHalf
+                                : type == kCodes        ? at::kFloat4_e2m1fn_x2
+                                : type == kScales       ? at::kFloat8_e8m0fnu
+                                                        : at::kFloat;
     if (s != want && !at::isIntegralType(s, true)) fail(what, "not of the described element type");
   }
-  const int64_t item = t.element_size(), e = type == MOE_TYPE_BF16 || type == MOE_TYPE_FP16 ? 2 : 4;
+  const int64_t item = t.element_size(), e = type == MOE_TYPE_BF16 || type == MOE_TYPE_FP16 ? 2 : type == kCodes || type == kScales ? 1 : 4;
   if (!x.empty()) {
     if (x.span() * e > (int64_t)t.storage().nbytes() - t.storage_offset() * item)
       fail(what, "smaller than what the call reads or writes there");
@@ -400,6 +409,55 @@ int gated_backward_x(PyObject* const* a) {
   });
 }
 
+int64_t code_bytes(int64_t k) { return (k + 1) / 2; }
+int64_t scale_bytes(int64_t k) { return (k + 31) / 32; }
+
+int mx_quantise(PyObject* const* a) {
+  const Plan<moe_mx_rows> p(a[0], "mx rows");
+  const int64_t rows = rows_of(a[1], "x");
+  Tensors of;
+  const void* x = of(a[1], "x", p->type, matrix(rows, p->x_stride, p->k));
+  void* codes = of(a[2], "codes", kCodes, matrix(rows, p->code_stride, code_bytes(p->k)));
+  void* scales = of(a[3], "scales", kScales, matrix(rows, p->scale_stride, scale_bytes(p->k)));
+  void* stream = stream_of(a[4]);
+  return without_gil([&] { return entry.mx_quantise(p.get(), x, rows, codes, scales, stream); });
+}
+
+int mx_dequantise(PyObject* const* a) {
+  const Plan<moe_mx_rows> p(a[0], "mx rows");
+  const int64_t rows = rows_of(a[1], "codes");
+  Tensors of;
+  const void* codes = of(a[1], "codes", kCodes, matrix(rows, p->code_stride, code_bytes(p->k)));
+  const void* scales = of(a[2], "scales", kScales, matrix(rows, p->scale_stride, scale_bytes(p->k)));
+  void* x = of(a[3], "x", p->type, matrix(rows, p->x_stride, p->k));
+  void* stream = stream_of(a[4]);
+  return without_gil([&] { return entry.mx_dequantise(p.get(), codes, scales, rows, x, stream); });
+}
+
+template <bool GATED>
+int mx_product(PyObject* const* a) {
+  const Plan<moe_mx> m(a[0], "mx");
+  const int64_t rows = rows_of(a[1], "x"), codes = code_bytes(m->k), blocks = scale_bytes(m->k);
+  const Extent w = {m->n_groups, m->w_group_stride, m->n, m->w_stride, codes};
+  const Extent ws = {m->n_groups, m->w_scale_group_stride, m->n, m->w_scale_stride, blocks};
+  Tensors of;
+  const void* x = of(a[1], "x", kCodes, matrix(rows, m->x_stride, codes));
+  const void* xs = of(a[2], "x_scale", kScales, matrix(rows, m->x_scale_stride, blocks));
+  const void* w1 = of(a[3], GATED ? "w_gate" : "w", kCodes, w);
+  const void* s1 = of(a[4], GATED ? "w_gate_scale" : "w_scale", kScales, ws);
+  const void* w2 = GATED ? of(a[5], "w_up", kCodes, w) : nullptr;
+  const void* s2 = GATED ? of(a[6], "w_up_scale", kScales, ws) : nullptr;
+  PyObject* const* b = a + (GATED ? 7 : 5);
+  const int32_t* offsets = (const int32_t*)of(b[0], "offsets", kIndex, vector((int64_t)m->n_groups + 1));
+  void* out = of(b[1], GATED ? "h" : "y", m->out_type, matrix(rows, m->y_stride, m->n));
+  int32_t* status = (int32_t*)of(b[2], "status", kIndex, vector(1));
+  void* stream = stream_of(b[3]);
+  return without_gil([&] {
+    return GATED ? entry.mx_gated(m.get(), x, xs, w1, s1, w2, s2, offsets, rows, out, status, stream)
+                 : entry.mx_forward(m.get(), x, xs, w1, s1, offsets, rows, out, status, stream);
+  });
+}
+
 // bind(MoeError, addresses of the entry points in the order of `entry`)
 PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
   constexpr int kEntries = sizeof(entry) / sizeof(void*);
@@ -430,6 +488,10 @@ PyMethodDef methods[] = {MOE_METHOD("bind", bind),
                          MOE_METHOD("gated_forward", (function<10, gated_forward>)),
                          MOE_METHOD("gated_backward_h", (function<11, gated_backward_h>)),
                          MOE_METHOD("gated_backward_x", (function<9, gated_backward_x>)),
+                         MOE_METHOD("mx_quantise", (function<5, mx_quantise>)),
+                         MOE_METHOD("mx_dequantise", (function<5, mx_dequantise>)),
+                         MOE_METHOD("mx_forward", (function<9, mx_product<false>>)),
+                         MOE_METHOD("mx_gated", (function<11, mx_product<true>>)),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensors", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
