@@ -229,9 +229,9 @@ struct MxTensors {
   void* out;
 };
 
-template <bool GATED, bool DMA, int BP, int BQ, int WP, int WQ, int ST>
+template <bool GATED, bool DMA, int BP, int BQ, int WP, int WQ, int ST, int STEPS>
 int launch_tile(const MxArgs& a, const MxTensors& v, hipStream_t s) {
-  typedef MxGemm<BP, BQ, WP, WQ, ST, DMA, GATED> G;
+  typedef MxGemm<BP, BQ, WP, WQ, ST, STEPS, DMA, GATED> G;
   auto u8 = [](const void* p) { return (const uint8_t*)p; };
   return launch_rows_of_tiles<k_mx<G, GATED>, G>("mx", row_tiles(a, G::kQ) * ((a.n + G::kP - 1) / G::kP), s, a, u8(v.x), u8(v.xs),
                                                  u8(v.w), u8(v.ws), u8(v.w2), u8(v.ws2), v.out);
@@ -241,12 +241,12 @@ template <bool GATED, bool DMA>
 int launch_mx(const MxArgs& a, const MxTensors& v, hipStream_t s) {
   const int64_t mean = a.rows / a.groups;
   const int wide = GATED ? 2 * a.n : a.n;   // columns of P
-  if (mean < 16 || row_tiles(a, 64) * ((wide + 127) / 128) < 96) return launch_tile<GATED, DMA, 128, 16, 4, 1, 4>(a, v, s);
-  if (mean < 64 || row_tiles(a, 128) * ((wide + 127) / 128) < 300) return launch_tile<GATED, DMA, 128, 64, 2, 2, 3>(a, v, s);
+  if (mean < 16 || row_tiles(a, 64) * ((wide + 127) / 128) < 96) return launch_tile<GATED, DMA, 128, 16, 4, 1, 4, 2>(a, v, s);
+  if (mean < 64 || row_tiles(a, 128) * ((wide + 127) / 128) < 300) return launch_tile<GATED, DMA, 128, 64, 2, 2, 3, 2>(a, v, s);
   if constexpr (DMA) {
-    if (row_tiles(a, 128) * ((wide + 255) / 256) >= 768 && a.k >= 4096) return launch_tile<GATED, DMA, 256, 128, 4, 2, 3>(a, v, s);
+    if (row_tiles(a, 128) * ((wide + 255) / 256) >= 768 && a.k >= 4096) return launch_tile<GATED, DMA, 256, 128, 4, 2, 3, 2>(a, v, s);
   }
-  return launch_tile<GATED, DMA, 128, 128, 2, 2, 2>(a, v, s);
+  return launch_tile<GATED, DMA, 128, 128, 2, 2, 2, 4>(a, v, s);
 }
 
 int check_mx(const moe_mx* m, int64_t rows, bool with_act) {

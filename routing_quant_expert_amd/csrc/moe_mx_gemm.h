@@ -9,6 +9,10 @@
 // depend on the order of the blocks: lane group q of 4 takes blocks 2 q and
 // 2 q + 1 of the step in its two products, whose scales then lie next to each
 // other (one 16-bit read; the instruction selects the byte).
+//
+// A step's scales are 8 bytes of every row, each in a cache line of its own: brought in step by step they cost as many
+// lines as the codes (12288 rows over 384 groups of 2048 x 4096, gated: 787 us, 643 without them). So they come for G
+// steps at once, into buffers of their own.
 #pragma once
 
 #include "moe_gemm.h"
@@ -56,17 +60,19 @@ __device__ __forceinline__ i32x4 bytes16(const uint8_t* p, int n, bool room) {
   return __builtin_bit_cast(i32x4, v);
 }
 
-template <int R, int NT, bool PAIRS>
+// R rows of NT threads' tile; scales for G steps at once.
+template <int R, int NT, bool PAIRS, int G>
 struct MxTile {
   static constexpr int kCodes = R * 128;
   static constexpr int kChunks = R * 8;
   static constexpr int kPer = kChunks >= NT ? kChunks / NT : 1;   // chunks a thread brings in
-  static constexpr int kWords = R * 2;                            // of 4 scales
-  static constexpr int kWordsThere = kWords < 64 ? 64 : kWords;   // (a wave brings in 64; those past the rows' repeat the last row's)
-  static constexpr int kBytes = kCodes + 4 * kWordsThere;
+  static constexpr int kRowWords = 2 * G;                         // of 4 scales
+  static constexpr int kWords = R * kRowWords;
+  static constexpr int kPerScales = kWords >= NT ? kWords / NT : 1;
+  static constexpr int kScales = 4 * kWords;
   static_assert(kChunks % NT == 0 || NT % kChunks == 0, "chunks over threads");
-  static_assert(kWordsThere <= NT && NT % kWordsThere == 0, "one word of scales a thread");
-  static_assert(!PAIRS || (NT % 256 == 0 && kChunks >= NT && kWords == NT), "a thread's chunks, and a wave's scales, are all of one matrix");
+  static_assert((kWords % NT == 0 || NT % kWords == 0) && kWords % 64 == 0, "words of scales over threads");
+  static_assert(!PAIRS || (NT % (64 * G) == 0 && NT % 256 == 0 && kChunks >= NT && kWords >= NT), "what a thread brings in is all of one matrix");
 
   __device__ static __forceinline__ int position(int k) { return kChunks < NT ? threadIdx.x % kChunks : threadIdx.x + NT * k; }
   __device__ static __forceinline__ int chunk(int i) { return i % 8 ^ (i / 8 & 7); }
@@ -74,56 +80,70 @@ struct MxTile {
   __device__ static __forceinline__ int own(const MxOperand& o, int row) {
     return min(PAIRS ? row / 32 * 16 + row % 16 : row, o.count - 1);
   }
-  // Scales of a pair lie apart by matrix: those of the first in the first half.
-  __device__ static __forceinline__ int scale_row(int row) { return PAIRS ? (row / 16 % 2) * (R / 2) + row / 32 * 16 + row % 16 : row; }
-  __device__ static __forceinline__ int word() { return threadIdx.x % kWordsThere; }
-  __device__ static __forceinline__ int word_row(const MxOperand& o) {
-    const int row = min(word() / 2, R - 1);
-    return min(PAIRS ? row % (R / 2) : row, o.count - 1);
-  }
+  // Word w of a row lies at word w ^ turned(row): 16 rows then spread over the banks.
+  __device__ static __forceinline__ int turned(int row) { return G == 4 ? row >> 1 & 4 : 0; }
+  __device__ static __forceinline__ int word(int k) { return kWords < NT ? threadIdx.x % kWords : threadIdx.x + NT * k; }
 
+  // Where a thread's rows start, the same in every lane of its wave (8 rows of chunks, 32 / G rows of scales to a wave).
   __device__ static __forceinline__ const uint8_t* codes(const MxOperand& o) {
     return o.codes + (PAIRS && (threadIdx.x >> 7 & 1) ? o.then : 0);
   }
   __device__ static __forceinline__ const uint8_t* scales(const MxOperand& o) {
-    return o.scales + (PAIRS && word() >= kWords / 2 ? o.scales_then : 0);
+    return o.scales + (PAIRS && (threadIdx.x / (32 * G) & 1) ? o.scales_then : 0);
   }
   struct Offsets {
-    uint32_t codes[kPer], scales;
+    uint32_t codes[kPer], scales[kPerScales];
   };
+  // Of scales: the first `words` of a row; those past them repeat the last one.
+  __device__ static __forceinline__ void scale_offsets(const MxOperand& o, int words, uint32_t (&off)[kPerScales]) {
+#pragma unroll
+    for (int k = 0; k < kPerScales; ++k) {
+      const int row = word(k) / kRowWords, w = word(k) % kRowWords ^ turned(row);
+      off[k] = (uint32_t)own(o, row) * (uint32_t)o.scale_ld + 4 * min(w, words - 1);
+    }
+  }
   __device__ static __forceinline__ void offsets(const MxOperand& o, Offsets& off) {
 #pragma unroll
     for (int k = 0; k < kPer; ++k) off.codes[k] = (uint32_t)own(o, position(k) / 8) * (uint32_t)o.ld + 16 * chunk(position(k));
-    off.scales = (uint32_t)word_row(o) * (uint32_t)o.scale_ld + 4 * (word() & 1);
+    scale_offsets(o, kRowWords, off.scales);
   }
 
-  // (As TileOf::dma; `codes` and `scales` are the same in every lane.)
+  // (As TileOf::dma; `at` is the same in every lane of a wave.)
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
-  __device__ static __forceinline__ void dma(const uint8_t* codes, const uint8_t* scales, const Offsets& off, uint32_t tile) {
+  __device__ static __forceinline__ void dma_codes(const uint8_t* at, const uint32_t (&off)[kPer], uint32_t tile) {
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t first = tile + 16 * 64 * (wave % (kChunks < NT ? kChunks / 64 : NT / 64));
 #pragma unroll
     for (int k = 0; k < kPer; ++k)
       asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
-                   : : "v"(off.codes[k]), "s"(codes), "s"(first + 16 * NT * k) : "memory", "m0");
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
-                 : : "v"(off.scales), "s"(scales), "s"(tile + kCodes + 4 * 64 * (wave % (kWordsThere / 64))) : "memory", "m0");
+                   : : "v"(off[k]), "s"(at), "s"(first + 16 * NT * k) : "memory", "m0");
+  }
+  __device__ static __forceinline__ void dma_scales(const uint8_t* at, const uint32_t (&off)[kPerScales], uint32_t buffer) {
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t first = buffer + 4 * 64 * (wave % (kWords < NT ? kWords / 64 : NT / 64));
+#pragma unroll
+    for (int k = 0; k < kPerScales; ++k)
+      asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
+                   : : "v"(off[k]), "s"(at), "s"(first + 4 * NT * k) : "memory", "m0");
   }
 #pragma clang diagnostic pop
 
-  // The same through registers at any alignment; `left` elements of each row are there (fewer than a step: zeros follow),
-  // `row_bytes` and `row_blocks` in a whole row.
+  // One step through registers at any alignment; `left` elements of each row are there (fewer than a step: zeros follow),
+  // room: the rows have 16 bytes of codes or more. Its scales take the words of a buffer's first step.
+  static constexpr int kStepWords = 2 * R;
+  static constexpr int kPerStep = kStepWords >= NT ? kStepWords / NT : 1;
   struct Stage {
     i32x4 codes[kPer];
-    uint32_t scales;
+    uint32_t scales[kPerStep];
   };
-  __device__ static __forceinline__ void load(const uint8_t* codes, const uint8_t* scales, const Offsets& off, int left,
-                                              bool room, Stage& g) {
+  __device__ static __forceinline__ int step_word(int k) { return kStepWords < NT ? threadIdx.x % kStepWords : threadIdx.x + NT * k; }
+  __device__ static __forceinline__ void load(const MxOperand& o, const uint32_t (&off)[kPer], int s, int left, bool room, Stage& g) {
+    const uint8_t* const from = codes(o) + 128 * (int64_t)s;
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       const int at = 16 * chunk(position(k));
-      g.codes[k] = bytes16(codes + off.codes[k], (left + 1) / 2 - at, room);
+      g.codes[k] = bytes16(from + off[k], (left + 1) / 2 - at, room);
       if (left & 1) {   // the half of the last byte past an odd row
         const int last = left / 2 - at;
 #pragma unroll
@@ -131,62 +151,78 @@ struct MxTile {
           if (last >= 4 * w && last < 4 * w + 4) g.codes[k][w] &= (16u << (8 * (last - 4 * w))) - 1;
       }
     }
-    const int n = (left + kMxBlock - 1) / kMxBlock - 4 * (word() & 1);   // scales there
-    uint32_t v = 0;
-    if (n >= 4) {
-      __builtin_memcpy(&v, scales + off.scales, 4);
-    } else {
 #pragma unroll
-      for (int i = 0; i < 3; ++i)
-        if (i < n) v |= (uint32_t)scales[off.scales + i] << (8 * i);
+    for (int k = 0; k < kPerStep; ++k) {
+      const int row = step_word(k) / 2, w = step_word(k) % 2;
+      const uint8_t* const p = o.scales + (PAIRS && (row / 16 & 1) ? o.scales_then : 0) + 8 * (int64_t)s +
+                               (uint32_t)own(o, row) * (uint32_t)o.scale_ld + 4 * w;
+      const int n = (left + kMxBlock - 1) / kMxBlock - 4 * w;   // scales there
+      uint32_t v = 0;
+      if (n >= 4) {
+        __builtin_memcpy(&v, p, 4);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+          if (i < n) v |= (uint32_t)p[i] << (8 * i);
+      }
+      g.scales[k] = v;
     }
-    g.scales = v;
   }
-  __device__ static __forceinline__ void store(const Stage& g, uint8_t* tile) {
+  __device__ static __forceinline__ void store(const Stage& g, uint8_t* tile, uint8_t* buffer) {
 #pragma unroll
     for (int k = 0; k < kPer; ++k) *reinterpret_cast<i32x4*>(tile + 16 * position(k)) = g.codes[k];
-    *reinterpret_cast<uint32_t*>(tile + kCodes + 4 * word()) = g.scales;
+#pragma unroll
+    for (int k = 0; k < kPerStep; ++k) {
+      const int row = step_word(k) / 2, w = step_word(k) % 2;
+      *reinterpret_cast<uint32_t*>(buffer + 4 * (kRowWords * row + (w ^ turned(row)))) = g.scales[k];
+    }
   }
 
-  // The lane's block and its two scales: row `own` + lane % 16, blocks 2 (lane / 16) + kk.
+  // The lane's block and its two scales: row `own` + lane % 16, blocks 2 (lane / 16) + kk of the step, which is step `in` of
+  // its buffer.
   __device__ static __forceinline__ i32x4 operand(const uint8_t* tile, int own, int kk, int lane) {
     const int row = own + (lane & 15);
     return *reinterpret_cast<const i32x4*>(tile + 128 * row + 16 * ((2 * (lane >> 4) + kk) ^ (row & 7)));
   }
-  __device__ static __forceinline__ int scale(const uint8_t* tile, int own, int lane) {
-    return *reinterpret_cast<const uint16_t*>(tile + kCodes + 8 * scale_row(own + (lane & 15)) + 2 * (lane >> 4));
+  __device__ static __forceinline__ int scale(const uint8_t* buffer, int own, int in, int lane) {
+    const int row = own + (lane & 15);
+    return *reinterpret_cast<const uint16_t*>(buffer + 4 * (kRowWords * row + ((2 * in + (lane >> 5)) ^ turned(row))) + 2 * (lane >> 4 & 1));
   }
 };
 
 // DMA: codes 16-byte and scales 4-byte aligned, brought into LDS directly; otherwise through registers, any alignment.
-template <int BP, int BQ, int WP, int WQ, int ST, bool DMA, bool PAIRS>
+template <int BP, int BQ, int WP, int WQ, int ST, int G, bool DMA, bool PAIRS>
 struct MxGemm : TileOut<BP, BQ, WP, WQ, PAIRS> {
   typedef TileOut<BP, BQ, WP, WQ, PAIRS> Out;
   using Out::NT, Out::NP, Out::NQ, Out::wave_p, Out::wave_q;
   typedef typename Out::Acc Acc;
-  typedef MxTile<BP, NT, PAIRS> PT;
-  typedef MxTile<BQ, NT, false> QT;
+  typedef MxTile<BP, NT, PAIRS, G> PT;
+  typedef MxTile<BQ, NT, false, G> QT;
   static constexpr int kSlots = DMA ? ST : 2;
-  static constexpr int kSlot = PT::kBytes + QT::kBytes;
-  static constexpr int kLds = kSlots * kSlot;
+  static constexpr int kSlot = PT::kCodes + QT::kCodes;
+  // A buffer takes the next G steps' scales together with the first of these steps' codes, when all waves are past the
+  // step ST before it: the buffer's last steps are then no later than that.
+  static constexpr int kBuffers = DMA ? (ST + G - 2) / G + 1 : 2;
+  static constexpr int kBuffer = PT::kScales + QT::kScales;
+  static constexpr int kLds = kSlots * kSlot + kBuffers * kBuffer;
 
   struct Half {
     i32x4 p[NP], q[NQ];
     int ps[NP], qs[NQ];
   };
-  // kk = 0: with the step's scales, which the second half takes from `first`.
+  // KK = 0: with the step's scales, step `in` of `buffer`; the second half takes them from `first`.
   template <int KK>
-  __device__ static __forceinline__ void read(const uint8_t* slot, Half& h, const Half* first = nullptr) {
+  __device__ static __forceinline__ void read(const uint8_t* slot, const uint8_t* buffer, int in, Half& h, const Half* first = nullptr) {
     const int lane = threadIdx.x & 63, p0 = wave_p(), q0 = wave_q();
 #pragma unroll
     for (int j = 0; j < NQ; ++j) {
-      h.q[j] = QT::operand(slot + PT::kBytes, q0 + 16 * j, KK, lane);
-      h.qs[j] = KK ? first->qs[j] : QT::scale(slot + PT::kBytes, q0 + 16 * j, lane);
+      h.q[j] = QT::operand(slot + PT::kCodes, q0 + 16 * j, KK, lane);
+      h.qs[j] = KK ? first->qs[j] : QT::scale(buffer + PT::kScales, q0 + 16 * j, in, lane);
     }
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       h.p[i] = PT::operand(slot, p0 + 16 * i, KK, lane);
-      h.ps[i] = KK ? first->ps[i] : PT::scale(slot, p0 + 16 * i, lane);
+      h.ps[i] = KK ? first->ps[i] : PT::scale(buffer, p0 + 16 * i, in, lane);
     }
   }
   template <int KK>
@@ -196,7 +232,7 @@ struct MxGemm : TileOut<BP, BQ, WP, WQ, PAIRS> {
 #pragma unroll
       for (int j = 0; j < NQ; ++j) acc[i][j] = mfma_mx<KK>(h.p[i], h.q[j], acc[i][j], h.ps[i], h.qs[j]);
   }
-  // Places `reads` LDS reads evenly among the first products of the half before.
+  // Places `READS` LDS reads evenly among the first products of the half before.
   template <int READS>
   __device__ static __forceinline__ void interleave() {
     constexpr int kProducts = NP * NQ, kEach = (2 * READS + kProducts - 1) / kProducts;
@@ -207,12 +243,19 @@ struct MxGemm : TileOut<BP, BQ, WP, WQ, PAIRS> {
     }
     __builtin_amdgcn_sched_barrier(0);
   }
-  __device__ static __forceinline__ void compute(const uint8_t* slot, Acc& acc) {
+  __device__ static __forceinline__ void compute(const uint8_t* slot, const uint8_t* buffer, Acc& acc) {
     Half h0, h1;
-    read<0>(slot, h0);
-    read<1>(slot, h1, &h0);
+    read<0>(slot, buffer, 0, h0);
+    read<1>(slot, buffer, 0, h1, &h0);
     multiply<0>(h0, acc);
     multiply<1>(h1, acc);
+  }
+
+  // Waits until nothing older than what steps first .. last (fewer than ST) brought in is in flight.
+  __device__ static __forceinline__ void wait_before(int first, int last) {
+    constexpr int kCodes = PT::kPer + QT::kPer, kScales = PT::kPerScales + QT::kPerScales;
+    if (last >= first && last / G * G >= first) wait_steps<kCodes, ST - 1, kScales>(last - first + 1);
+    else wait_steps<kCodes, ST - 1>(max(last - first + 1, 0));
   }
 
   // Adds the sum over the k elements of the rows. LDS is free for other use after a barrier.
@@ -222,78 +265,96 @@ struct MxGemm : TileOut<BP, BQ, WP, WQ, PAIRS> {
     PT::offsets(p, po);
     QT::offsets(q, qo);
     const bool room = k >= 32;
+    uint8_t *const end = lds + kSlots * kSlot, *const buffers = end, *const last = buffers + (kBuffers - 1) * kBuffer;
     struct Stage {
       typename PT::Stage p;
       typename QT::Stage q;
     };
     auto load = [&](int s, Stage& g) {
-      PT::load(PT::codes(p) + 128 * (int64_t)s, PT::scales(p) + 8 * (int64_t)s, po, k - s * kMxStep, room, g.p);
-      QT::load(QT::codes(q) + 128 * (int64_t)s, QT::scales(q) + 8 * (int64_t)s, qo, k - s * kMxStep, room, g.q);
+      PT::load(p, po.codes, s, k - s * kMxStep, room, g.p);
+      QT::load(q, qo.codes, s, k - s * kMxStep, room, g.q);
     };
-    auto store = [&](uint8_t* slot, const Stage& g) {
-      PT::store(g.p, slot);
-      QT::store(g.q, slot + PT::kBytes);
+    auto store = [&](const Stage& g, uint8_t* slot, uint8_t* buffer) {
+      PT::store(g.p, slot, buffer);
+      QT::store(g.q, slot + PT::kCodes, buffer + PT::kScales);
     };
     if constexpr (DMA) {
       const int nk = k / kMxStep;
-      constexpr int kPer = PT::kPer + QT::kPer + 2;
       const uint8_t *pc = uniform(PT::codes(p)), *ps = uniform(PT::scales(p)), *qc = uniform(q.codes), *qs = uniform(q.scales);
-      auto issue = [&](const uint8_t* slot) {
+      uint32_t put = lds_offset(buffers);   // the buffer of the next scales asked for
+      auto issue = [&](int s, const uint8_t* slot) {
+        if (s % G == 0) {
+          if (nk - s >= G) {
+            PT::dma_scales(ps, po.scales, put);
+            QT::dma_scales(qs, qo.scales, put + PT::kScales);
+          } else {
+            uint32_t pw[PT::kPerScales], qw[QT::kPerScales];
+            PT::scale_offsets(p, 2 * (nk - s), pw);
+            QT::scale_offsets(q, 2 * (nk - s), qw);
+            PT::dma_scales(ps, pw, put);
+            QT::dma_scales(qs, qw, put + PT::kScales);
+          }
+          ps += 8 * G;
+          qs += 8 * G;
+          put = put == lds_offset(last) ? lds_offset(buffers) : put + kBuffer;
+        }
         const uint32_t at = lds_offset(slot);
-        PT::dma(pc, ps, po, at);
-        QT::dma(qc, qs, qo, at + PT::kBytes);
+        PT::dma_codes(pc, po.codes, at);
+        QT::dma_codes(qc, qo.codes, at + PT::kCodes);
         pc += 128;
         qc += 128;
-        ps += 8;
-        qs += 8;
       };
-      uint8_t* const end = lds + kLds;
 #pragma unroll
       for (int s = 0; s < ST - 1; ++s)
-        if (s < nk) issue(lds + s * kSlot);
-      if (k % kMxStep) {   // the last, partial step first, in the slot that the ring needs last
+        if (s < nk) issue(s, lds + s * kSlot);
+      if (k % kMxStep) {   // the last, partial step first, in the slot and the buffer that the ring needs last
         Stage g;
         load(nk, g);
-        store(end - kSlot, g);
+        store(g, end - kSlot, last);
         lds_barrier();
-        compute(end - kSlot, acc);
+        compute(end - kSlot, last, acc);
         lds_barrier();
       }
       if (nk == 0) return;
-      if (ST - 1 < nk) issue(end - kSlot);
+      if (ST - 1 < nk) issue(ST - 1, end - kSlot);
       // (as Gemm::run)
       Half h0, h1;
-      wait_steps<kPer, ST - 1>(nk - 1);
+      wait_before(1, min(nk, ST) - 1);
       lds_barrier();
-      read<0>(lds, h0);
-      const uint8_t* get = lds;
+      const uint8_t *get = lds, *scales = buffers;
+      read<0>(get, scales, 0, h0);
       int s = 0;
+      auto next = [&] {   // to step s + 1
+        get = get + kSlot == end ? lds : get + kSlot;
+        if ((s + 1) % G == 0) scales = scales == last ? buffers : scales + kBuffer;
+      };
 #pragma unroll 1
       for (; s < nk - ST; ++s) {
-        read<1>(get, h1, &h0);
+        read<1>(get, scales, s % G, h1, &h0);
         multiply<0>(h0, acc);
         interleave<NP + NQ>();
-        wait_vmcnt<kPer * (ST - 2)>();   // step s + 1 is in; later ones may be in flight
-        lds_barrier();                   // for every wave; and all have read step s
-        issue(get);
-        get = get + kSlot == end ? lds : get + kSlot;
-        read<0>(get, h0);
+        if constexpr (ST == 2) wait_vmcnt<0>();
+        else wait_before(s + 2, s + ST - 1);   // step s + 1 is in; later ones may be in flight
+        lds_barrier();                         // for every wave; and all have read step s
+        issue(s + ST, get);
+        next();
+        read<0>(get, scales, (s + 1) % G, h0);
         multiply<1>(h1, acc);
         interleave<2 * (NP + NQ)>();
       }
 #pragma unroll 1
       for (; s < nk - 1; ++s) {
-        read<1>(get, h1, &h0);
+        read<1>(get, scales, s % G, h1, &h0);
         multiply<0>(h0, acc);
         interleave<NP + NQ>();
-        wait_steps<kPer, ST - 2>(nk - 2 - s);
+        wait_before(s + 2, min(nk, s + ST) - 1);
         lds_barrier();
-        get = get + kSlot == end ? lds : get + kSlot;
-        read<0>(get, h0);
+        next();
+        read<0>(get, scales, (s + 1) % G, h0);
         multiply<1>(h1, acc);
         interleave<2 * (NP + NQ)>();
       }
-      read<1>(get, h1, &h0);
+      read<1>(get, scales, s % G, h1, &h0);
       multiply<0>(h0, acc);
       multiply<1>(h1, acc);
     } else {
@@ -301,13 +362,13 @@ struct MxGemm : TileOut<BP, BQ, WP, WQ, PAIRS> {
       if (nk == 0) return;
       Stage g;
       load(0, g);
-      store(lds, g);
+      store(g, lds, buffers);
 #pragma unroll 1
       for (int s = 0; s < nk; ++s) {
         lds_barrier();   // step s is there, and all are done with step s - 1
         if (s + 1 < nk) load(s + 1, g);
-        compute(lds + (s & 1) * kSlot, acc);
-        if (s + 1 < nk) store(lds + (s + 1 & 1) * kSlot, g);
+        compute(lds + (s & 1) * kSlot, buffers + (s & 1) * kBuffer, acc);
+        if (s + 1 < nk) store(g, lds + (s + 1 & 1) * kSlot, buffers + (s + 1 & 1) * kBuffer);
       }
     }
   }
