@@ -27,7 +27,7 @@ FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-ffp-contract=
          "-Wall", "-Wno-unused-function", "-Wno-unused-variable", "-Wno-unused-command-line-argument"]
 SOURCES = ["moe_api.hip", "moe_route.hip", "moe_experts.hip", "moe_decode1.hip", "moe_prefill.hip",
            "moe_shared_pf.hip", "moe_cache.hip", "moe_score_table.hip", "moe_join.hip", "moe_grouped.hip", "moe_adapter.hip",
-           "moe_gated.hip", "moe_mx.hip"]
+           "moe_gated.hip", "moe_gated_hidden.hip", "moe_gated_input.hip", "moe_mx.hip"]
 # the prefill kernels consume MFMA results in VALU code: keep them in VGPRs (no accvgpr copies);
 # the single-token kernels' leading scalar arguments are preloaded into SGPRs at wave launch
 EXTRA = {"moe_prefill.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
@@ -52,7 +52,7 @@ def _tensors_command(out: str) -> list:
             "-o", out, "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
 
 
-def build(verbose: bool = False, jobs: int = 4) -> str:
+def build(verbose: bool = False, jobs: int = 6) -> str:
     os.makedirs(BUILD, exist_ok=True)
     objs = []
     cmds = []

@@ -2,9 +2,14 @@
 //   h = act(min(g, L)) * clamp(u, -L, L),  act(z) = z s(z),
 // s the logistic function of z (silu) or of 2 sqrt(2/pi) (z + 0.044715 z^3)
 // (gelu in its tanh form), and its gradient.
+//
+// It is the work of one wave for up to 256 outputs a lane, with nothing beside
+// it to hide it: an instruction more or less is 1024 cycles a tile there.
 #pragma once
 
 #include <hip/hip_runtime.h>
+
+#include <cmath>
 
 #include "../../include/moe.h"
 
@@ -15,47 +20,71 @@ struct Gate {
   float limit;   // infinity: none
 };
 
-// e^x for x <= 0: 2^t with t = x log2(e) rounded, and what the rounding left
-// to first order: about two steps of f32 off down to e^-87, then 0.
-__device__ __forceinline__ float exp_f32(float x) {
-  const float t = x * 0x1.715476p+0f;
-  const float left = __builtin_fmaf(x, 0x1.4ae0cp-26f, __builtin_fmaf(x, 0x1.715476p+0f, -t));
-  const float e = __builtin_amdgcn_exp2f(t);
-  return __builtin_fmaf(e, left * 0x1.62e43p-1f, e);
-}
-
-// act(z) and, with SLOPE, its derivative s + z s (1 - s) inner'. Past +-104 both
-// are their limits to f32 (which also keeps infinities from meeting zeros); NaN stays.
-template <bool SLOPE>
-__device__ __forceinline__ float activation(const Gate& a, float z, float& slope) {
-  z = z < -104.0f ? -104.0f : z;
-  const float y = z > 104.0f ? 104.0f : z;
-  float inner = y, by = 1.0f;
-  if (a.act == MOE_ACT_GELU) {
-    constexpr float c = 1.5957691216057308f;   // 2 sqrt(2/pi)
-    inner = c * __builtin_fmaf(0.044715f * y * y, y, y);
-    by = c * __builtin_fmaf(0.134145f * y, y, 1.0f);
+// act(z) and, with SLOPE, its derivative s + act(z) (1 - s) inner'(z). s is 1 / (1 + 2^t): t's rounding moves it by
+// |t| s (1 - s) 2^-24, which stays below 2^-25. At -infinity act and derivative are 0 (s is 0 below -104); at +infinity the
+// derivative is NaN (infinity times 0), and so is everything of NaN.
+template <int ACT, bool SLOPE>
+__device__ __forceinline__ float activation(float z, float& slope) {
+  constexpr float kLog2e = 1.4426950408889634f, kInner = 1.5957691216057308f, kCubic = 0.044715f;   // 2 sqrt(2/pi)
+  float t;
+  if (ACT == MOE_ACT_GELU) t = z * __builtin_fmaf(z * z, -kInner * kCubic * kLog2e, -kInner * kLog2e);
+  else t = z * -kLog2e;
+  const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(t));
+  const float y = __builtin_amdgcn_fmed3f(z, -104.0f, INFINITY);   // (NaN is in s)
+  const float v = y * s;
+  if (SLOPE) {
+    float by = 1.0f - s;
+    if (ACT == MOE_ACT_GELU) by *= __builtin_fmaf(y * y, 3.0f * kCubic * kInner, kInner);
+    slope = __builtin_fmaf(v, by, s);
   }
-  const float e = exp_f32(-__builtin_fabsf(inner)), high = __builtin_amdgcn_rcpf(1.0f + e), low = e * high;
-  const float s = inner < 0.0f ? low : high;
-  if (SLOPE) slope = __builtin_fmaf(y * s, (inner < 0.0f ? high : low) * by, s);
-  return z * s;
+  return v;
 }
 
-__device__ __forceinline__ float at_most(float v, float limit) { return v > limit ? limit : v; }
-__device__ __forceinline__ float clamped(float v, float limit) { return v > limit ? limit : v < -limit ? -limit : v; }
+// (Comparisons, not minima: NaN stays.)
+__device__ __forceinline__ float held(float v, bool over, float limit) { return over ? __builtin_copysignf(limit, v) : v; }
 
-__device__ __forceinline__ float gated(const Gate& a, float g, float u) {
+template <int ACT>
+__device__ __forceinline__ float gated(float g, float u, float limit) {
   float unused;
-  return activation<false>(a, at_most(g, a.limit), unused) * clamped(u, a.limit);
+  return activation<ACT, false>(held(g, g > limit, limit), unused) * held(u, __builtin_fabsf(u) > limit, limit);
 }
 // h again, and the gradients of g and u for that of h (the clamps' ends pass it).
-__device__ __forceinline__ float gated_back(const Gate& a, float g, float u, float dh, float& dg, float& du) {
+template <int ACT>
+__device__ __forceinline__ float gated_back(float g, float u, float dh, float limit, float& dg, float& du) {
+  const bool g_over = g > limit, u_over = __builtin_fabsf(u) > limit;
   float slope;
-  const float v = activation<true>(a, at_most(g, a.limit), slope), uc = clamped(u, a.limit);
-  dg = g > a.limit ? 0.0f : dh * uc * slope;
-  du = u > a.limit || u < -a.limit ? 0.0f : dh * v;
+  const float v = activation<ACT, true>(held(g, g_over, limit), slope), uc = held(u, u_over, limit);
+  dg = g_over ? 0.0f : dh * uc * slope;
+  du = u_over ? 0.0f : dh * v;
   return v * uc;
+}
+
+// The same for N neighbouring outputs (vectors of f32), the activation chosen once.
+template <typename V>
+__device__ __forceinline__ V gated_all(const Gate& a, V g, V u) {
+  constexpr int N = sizeof(V) / 4;
+  V h;
+  if (a.act == MOE_ACT_SILU) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) h[e] = gated<MOE_ACT_SILU>(g[e], u[e], a.limit);
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e) h[e] = gated<MOE_ACT_GELU>(g[e], u[e], a.limit);
+  }
+  return h;
+}
+template <int ACT, typename V>
+__device__ __forceinline__ V gated_back_all(V g, V u, V dh, float limit, V& dg, V& du) {
+  constexpr int N = sizeof(V) / 4;
+  V h;
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    float x, y;
+    h[e] = gated_back<ACT>(g[e], u[e], dh[e], limit, x, y);
+    dg[e] = x;
+    du[e] = y;
+  }
+  return h;
 }
 
 }  // namespace moe

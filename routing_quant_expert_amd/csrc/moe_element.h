@@ -34,6 +34,20 @@ using oct = typename oct_of<T>::type;
 template <typename V>
 __device__ __forceinline__ f32x8 to_f32(V v) { return __builtin_convertvector(v, f32x8); }
 
+// The same of bf16 by the bits: an instruction an element.
+__device__ __forceinline__ f32x8 unpacked(bf16x8_t v) {
+  uint32_t w[4];
+  __builtin_memcpy(w, &v, sizeof(w));
+  f32x8 f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __builtin_bit_cast(float, w[i] << 16);
+    f[2 * i + 1] = __builtin_bit_cast(float, w[i] & 0xffff0000u);
+  }
+  return f;
+}
+__device__ __forceinline__ f32x8 unpacked(fp16x8_t v) { return to_f32(v); }
+
 // Elements p[0..7] of which the first n are there (n >= 8: all) are loaded in
 // two steps: raw_oct asks for them, and placed_oct, where they are used, moves
 // them to their places and fills up with zeros. A load with a branch on its own

@@ -1,32 +1,11 @@
-// The experts' gated feed-forward on 16-bit weights (moe_gated_*), rows sorted
-// by group as for the grouped products:
-//
-//   forward     h[r] = act(Wg[e] x[r]) * (Wu[e] x[r])      P = 16 rows of Wg and 16 of Wu in turn, Q = x rows, sum over k
-//   backward_h  dh[r] = Wd[e]^T dy[r], never stored:       P = Wd columns, Q = dy rows, sum over k
-//               dgate, dup (and h again) from dh, gate, up
-//   backward_x  dx[r] = Wg[e]^T dgate[r] + Wu[e]^T dup[r]  P = Wg, then Wu columns, Q = dgate, then dup rows, two sums over n
-//
-// A lane of the forward tile holds the sums of the same outputs of both
-// projections, so that activation and product are its own work; the backward
-// pass applies their derivatives to dh while it is still in registers.
-#include <hip/hip_runtime.h>
-
+// The gated feed-forward's forward pass, and the entry points of all three calls (moe_gated.h).
+#include "moe_gated.h"
 #include <cmath>
 
-#include "moe_activation.h"
-#include "moe_gemm.h"
-#include "moe_groups.h"
 #include "moe_host.h"
 
 namespace moe {
 namespace {
-
-struct GatedArgs : Groups {
-  int n, k;
-  int f32;   // dx in f32
-  Gate gate;
-  int64_t x_stride, h_stride, gate_stride, y_stride, w_stride, w_group, down_stride, down_group;
-};
 
 template <typename T, typename G>
 __global__ __launch_bounds__(G::NT, 2) void k_gated(GatedArgs a, const T* __restrict__ x, const T* __restrict__ wg,
@@ -53,129 +32,68 @@ __global__ __launch_bounds__(G::NT, 2) void k_gated(GatedArgs a, const T* __rest
 #pragma unroll
   for (int i = 0; i < G::NP / 2; ++i)
 #pragma unroll
-    for (int j = 0; j < G::NQ; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) g[i][j][e] = gated(a.gate, g[i][j][e], u[i][j][e]);
+    for (int j = 0; j < G::NQ; ++j) g[i][j] = gated_all(a.gate, g[i][j], u[i][j]);
   G::store_to(g, h + t.row * a.h_stride + p0, a.h_stride, pn, row);
 }
 
-// (gate and dgate, and up and dup, may be the same memory.)
-template <typename T, typename G>
-__global__ __launch_bounds__(G::NT, 2) void k_gated_dh(GatedArgs a, const T* __restrict__ dy, const T* __restrict__ wd,
-                                                    const T* gate, const T* up, T* dgate, T* dup, T* __restrict__ h) {
+template <typename T, typename G, int ACT>
+__global__ __launch_bounds__(256, 1) void k_gated_wide(GatedArgs a, const T* __restrict__ x, const T* __restrict__ wg,
+                                                      const T* __restrict__ wu, T* __restrict__ h, T* __restrict__ gate,
+                                                      T* __restrict__ up) {
   extern __shared__ __align__(16) uint8_t lds[];
   report(a);
   const Tile t = my_tile<G>(a, a.n);
   if (t.rows <= 0) return;
   const bool none = t.group < 0 || t.group >= a.groups;
   const int p0 = t.p * G::kP, pn = a.n - p0;
-  const Operand<T> P = {wd + (none ? 0 : t.group) * a.down_group + p0, a.down_stride, pn, nullptr, a.n >= 8};
-  const Operand<T> Q = {dy + t.row * a.y_stride, a.y_stride, t.rows, nullptr, a.k >= 8};
-  typename G::Acc acc = {};
-  G::run(P, Q, none ? 0 : a.k, lds, acc);
-  const int64_t first = t.row * a.gate_stride + p0;
-  struct Kept {
-    f32x4 g, u;
-  };
-  G::each_quad(
-      acc, pn, [&](int q) { return q < t.rows ? q : -1; },
-      [&](int64_t q, int p, int n) -> Kept {
-        const int64_t at = first + q * a.gate_stride + p;
-        return {G::load_quad(gate + at, n), G::load_quad(up + at, n)};
-      },
-      [&](int64_t q, int p, int n, f32x4 dh, const Kept& kept) {
-        f32x4 dg, du, v;
+  const Operand<T> P = {(G::second_rows() ? wu : wg) + (none ? 0 : t.group) * a.w_group + p0 * a.w_stride, a.w_stride,
+                        min(G::kP, pn), nullptr, true};
+  const Operand<T> Q = {x + t.row * a.x_stride, a.x_stride, t.rows, nullptr, true};
+  by_rows(t.rows, [&](auto parts) {
+    constexpr int NQ = parts;
+    f32x4 acc[8][NQ] = {};
+    if (!none) G::run(P, Q, a.k, lds, acc, [] {});
+    f32x4 g[4][NQ], u[4][NQ];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x, y;
-          v[e] = gated_back(a.gate, kept.g[e], kept.u[e], dh[e], x, y);
-          // rows of no group have no gradients, whatever is kept there
-          dg[e] = none ? 0.0f : x;
-          du[e] = none ? 0.0f : y;
-          v[e] = none ? 0.0f : v[e];
-        }
-        const int64_t at = first + q * a.gate_stride + p;
-        G::store_quad(dgate + at, dg, n);
-        G::store_quad(dup + at, du, n);
-        if (h) G::store_quad(h + (t.row + q) * a.h_stride + p0 + p, v, n);
-      });
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < NQ; ++j) {
+        g[i][j] = acc[2 * i][j];
+        u[i][j] = acc[2 * i + 1][j];
+      }
+    if (gate) {
+      G::store(g, gate + t.row * a.gate_stride + p0, a.gate_stride, pn, t.rows);
+      G::store(u, up + t.row * a.gate_stride + p0, a.gate_stride, pn, t.rows);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < NQ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) g[i][j][e] = gated<ACT>(g[i][j][e], u[i][j][e], a.gate.limit);
+    G::store(g, h + t.row * a.h_stride + p0, a.h_stride, pn, t.rows);
+  });
 }
 
-template <typename T, typename G>
-__global__ __launch_bounds__(G::NT, 2) void k_gated_dx(GatedArgs a, const T* __restrict__ dgate, const T* __restrict__ dup,
-                                                    const T* __restrict__ wg, const T* __restrict__ wu,
-                                                    void* __restrict__ dx) {
-  extern __shared__ __align__(16) uint8_t lds[];
-  report(a);
-  const Tile t = my_tile<G>(a, a.k);
-  if (t.rows <= 0) return;
-  const bool none = t.group < 0 || t.group >= a.groups;
-  const int p0 = t.p * G::kP, pn = a.k - p0;
-  const Operand<T> P = {wg + (none ? 0 : t.group) * a.w_group + p0, a.w_stride, pn, nullptr, a.k >= 8,
-                        elements_between(wg, wu)};
-  const Operand<T> Q = {dgate + t.row * a.gate_stride, a.gate_stride, t.rows, nullptr, a.n >= 8,
-                        elements_between(dgate, dup)};
-  typename G::Acc acc = {};
-  G::run(P, Q, none ? 0 : a.n, lds, acc);
-  uint8_t* o = (uint8_t*)dx + (t.row * a.x_stride + p0) * (a.f32 ? 4 : 2);
-  G::store(acc, o, a.f32, a.x_stride, pn, [&](int q) { return q < t.rows ? q : -1; });
-}
-
-enum Way { kForward, kHidden, kInput };
-
-// What a call was given, in the order of its entry point.
-struct Tensors {
-  const void *in, *in2;   // x; dy; dgate and dup
-  const void *w, *w2;     // w_gate and w_up; w_down
-  const void *gate, *up;  // kept by the forward pass
-  void *out, *out2, *h;   // h (gate and up kept as out and out2); dgate and dup, h; dx
+struct Kernels {
+  template <typename T, typename G>
+  static int narrow(int64_t tiles, const GatedArgs& a, const GatedTensors& v, hipStream_t s) {
+    return launch_rows_of_tiles<k_gated<T, G>, G>("gated", tiles, s, a, (const T*)v.in, (const T*)v.w, (const T*)v.w2, (T*)v.h,
+                                                  (T*)v.out, (T*)v.out2);
+  }
+  template <typename T, typename G>
+  static int wide(int64_t tiles, const GatedArgs& a, const GatedTensors& v, hipStream_t s) {
+    return a.gate.act == MOE_ACT_SILU ? wide_with<T, G, MOE_ACT_SILU>(tiles, a, v, s) : wide_with<T, G, MOE_ACT_GELU>(tiles, a, v, s);
+  }
+  template <typename T, typename G, int ACT>
+  static int wide_with(int64_t tiles, const GatedArgs& a, const GatedTensors& v, hipStream_t s) {
+    return launch_rows_of_tiles<k_gated_wide<T, G, ACT>, G>("gated", tiles, s, a, (const T*)v.in, (const T*)v.w, (const T*)v.w2,
+                                                            (T*)v.h, (T*)v.out, (T*)v.out2);
+  }
 };
 
-template <Way W, typename T, bool DMA, int BP, int BQ, int WP, int WQ, int ST>
-int launch_tile(const GatedArgs& a, const Tensors& v, hipStream_t s) {
-  typedef Gemm<T, W != kForward, false, BP, BQ, WP, WQ, ST, DMA, false,
-               W == kForward ? kRowPairs : W == kInput ? kTwoSums : kSingle> G;
-  const int width = W == kInput ? a.k : a.n;
-  const int64_t tiles = row_tiles(a, G::kQ) * ((width + G::kP - 1) / G::kP);
-  if constexpr (W == kForward)
-    return launch_rows_of_tiles<k_gated<T, G>, G>("gated", tiles, s, a, (const T*)v.in, (const T*)v.w, (const T*)v.w2,
-                                                  (T*)v.h, (T*)v.out, (T*)v.out2);
-  else if constexpr (W == kHidden)
-    return launch_rows_of_tiles<k_gated_dh<T, G>, G>("gated", tiles, s, a, (const T*)v.in, (const T*)v.w,
-                                                     (const T*)v.gate, (const T*)v.up, (T*)v.out, (T*)v.out2, (T*)v.h);
-  else
-    return launch_rows_of_tiles<k_gated_dx<T, G>, G>("gated", tiles, s, a, (const T*)v.in, (const T*)v.in2,
-                                                     (const T*)v.w, (const T*)v.w2, v.out);
-}
 
-template <Way W, typename T, bool DMA>
-int launch_rows(const GatedArgs& a, const Tensors& v, hipStream_t s) {
-  const int64_t mean = a.rows / a.groups;
-  const int width = W == kInput ? a.k : a.n, wide = W == kForward ? 2 * width : width;   // columns of P
-  if (mean < 16 || row_tiles(a, 64) * ((wide + 127) / 128) < 96) return launch_tile<W, T, DMA, 128, 16, 4, 1, 4>(a, v, s);
-  if (mean < 64 || row_tiles(a, 128) * ((wide + 127) / 128) < 300)
-    return launch_tile<W, T, DMA, 128, 64, 2, 2, 3>(a, v, s);
-  if constexpr (DMA) {
-    if (row_tiles(a, 128) * ((wide + 255) / 256) >= 768 && (W == kInput ? a.n : a.k) >= 1024)
-      return launch_tile<W, T, DMA, 256, 128, 4, 2, 3>(a, v, s);
-  }
-  return launch_tile<W, T, DMA, 128, 128, 2, 2, 2>(a, v, s);
-}
-
-template <Way W, typename T>
-int launch_way(const GatedArgs& a, const Tensors& v, hipStream_t s) {
-  bool aligned;
-  if (W == kForward)
-    aligned = rows16(v.in, a.x_stride) && rows16(v.w, a.w_stride) && rows16(v.w2, a.w_stride) && a.w_group % 8 == 0;
-  else if (W == kHidden)
-    aligned = rows16(v.in, a.y_stride) && rows16(v.w, a.down_stride) && a.down_group % 8 == 0 && a.n % 8 == 0;
-  else
-    aligned = rows16(v.in, a.gate_stride) && rows16(v.in2, a.gate_stride) && rows16(v.w, a.w_stride) &&
-              rows16(v.w2, a.w_stride) && a.w_group % 8 == 0 && a.k % 8 == 0;
-  return aligned ? launch_rows<W, T, true>(a, v, s) : launch_rows<W, T, false>(a, v, s);
-}
-
-int check_gated(const moe_gated* g, int64_t rows, Way way) {
+int check_gated(const moe_gated* g, int64_t rows, GatedWay way) {
   if (!g) return fail(MOE_EINVAL, "gated is NULL%s%lld");
   if (g->type != MOE_TYPE_BF16 && g->type != MOE_TYPE_FP16)
     return fail(MOE_EINVAL, "gated: type must be MOE_TYPE_BF16 or MOE_TYPE_FP16%s (%lld)", "", g->type);
@@ -206,8 +124,8 @@ int check_gated(const moe_gated* g, int64_t rows, Way way) {
   return MOE_OK;
 }
 
-template <Way W>
-int gated_call(const moe_gated* g, const Tensors& v, const int32_t* offsets, int64_t rows, int32_t* status, void* stream) {
+template <GatedWay W>
+int gated_call(const moe_gated* g, const GatedTensors& v, const int32_t* offsets, int64_t rows, int32_t* status, void* stream) {
   if (int r = check_gated(g, rows, W)) return r;
   if (!offsets) return fail(MOE_EINVAL, "gated: offsets must be non-NULL%s%lld");
   if ((uintptr_t)offsets % 4 || (uintptr_t)status % 4)
@@ -237,10 +155,17 @@ int gated_call(const moe_gated* g, const Tensors& v, const int32_t* offsets, int
                            (uintptr_t)v.up | (uintptr_t)v.out | (uintptr_t)v.out2 | (uintptr_t)v.h;
   if (halves % 2 || (W == kInput && a.f32 && (uintptr_t)v.out % 4))
     return fail(MOE_EINVAL, "gated: a pointer is not aligned to its elements%s%lld");
-  return g->type == MOE_TYPE_BF16 ? launch_way<W, bf16_t>(a, v, s) : launch_way<W, fp16_t>(a, v, s);
+  return W == kForward  ? gated_forward(a, v, g->type, s)
+         : W == kHidden ? gated_hidden(a, v, g->type, s)
+                        : gated_input(a, v, g->type, s);
 }
 
 }  // namespace
+
+int gated_forward(const GatedArgs& a, const GatedTensors& v, int type, hipStream_t s) {
+  return launch_gated<kForward, Kernels>(a, v, type, s);
+}
+
 }  // namespace moe
 
 using namespace moe;

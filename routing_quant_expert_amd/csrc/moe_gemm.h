@@ -132,6 +132,13 @@ struct TileOf {
     }
   }
 
+  // The k-th chunk alone.
+  __device__ static __forceinline__ void dma_one(const T* at, Off off, uint32_t tile, int k) {
+    static_assert(!GATHER && kChunks >= NT);
+    const uint32_t first = tile + 16 * 64 * __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+                 : : "v"(2 * off), "s"(at), "s"(first + 16 * NT * k) : "memory", "m0");
+  }
 #pragma clang diagnostic pop
 
   // COL: a last step of `left` r: the rows past it repeat the last one, until clear() zeroes them in LDS.
@@ -308,56 +315,62 @@ struct TileOut {
     }
   }
 
-  // The same places for a use of its own: load(q, p, n) at tile row q, output p and the n - 1 after it, for all of a
-  // row of sums before use(q, p, n, sums, loaded) of each. What a lane loads is what it is given to use.
-  template <int N, typename Row, typename Load, typename Use>
-  __device__ static __forceinline__ void each_quad(const f32x4 (&acc)[N][NQ], int pn, Row&& row, Load&& load, Use&& use) {
+  // The same places for a use of its own: use(q, p, n, sums, loaded) at tile row q, output p and the n - 1 after it, with
+  // what load(q, p, n) gave there. All is loaded before the first use: a wait for a load is for the stores before it too.
+  template <int N, typename L, typename Row, typename Load>
+  __device__ static __forceinline__ void load_quads(L (&l)[N][NQ], int pn, Row&& row, Load&& load) {
+    const int lane = threadIdx.x & 63;
+    const bool whole = N % 2 == 0 && pn >= kP;
+#pragma unroll
+    for (int j = 0; j < NQ; ++j)
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int p = wave_out() + 4 * (lane >> 4) + (whole ? 16 * (lane >> 3 & 1) + 32 * (i / 2) : 16 * i);
+        const int64_t q = row(wave_q() + 16 * j + (whole ? 8 * (i % 2) + (lane & 7) : lane & 15));
+        if (q >= 0) l[i][j] = load(q, p, whole ? 4 : pn - p);
+      }
+  }
+  template <int N, typename L, typename Row, typename Use>
+  __device__ static __forceinline__ void use_quads(const f32x4 (&acc)[N][NQ], const L (&l)[N][NQ], int pn, Row&& row, Use&& use) {
     const int lane = threadIdx.x & 63, upper = lane >> 3 & 1;
-    typedef decltype(load((int64_t)0, 0, 0)) Loaded;
     if (N % 2 == 0 && pn >= kP) {
+      const int p = wave_out() + 16 * upper + 4 * (lane >> 4);
 #pragma unroll
       for (int j = 0; j < NQ; ++j) {
         const int64_t qa = row(wave_q() + 16 * j + (lane & 7)), qb = row(wave_q() + 16 * j + 8 + (lane & 7));
-        const int p = wave_out() + 16 * upper + 4 * (lane >> 4);
-        Loaded la[N / 2], lb[N / 2];
 #pragma unroll
-        for (int i = 0; i < N / 2; ++i) {
-          if (qa >= 0) la[i] = load(qa, p + 32 * i, 4);
-          if (qb >= 0) lb[i] = load(qb, p + 32 * i, 4);
-        }
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i) {
-          f32x4 a = acc[2 * i][j], b = acc[(2 * i + 1) % N][j], x;
+        for (int i = 0; i + 1 < N; i += 2) {
+          f32x4 a = acc[i][j], b = acc[i + 1][j], x;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             x[e] = dpp_f32<kDppRor8>(upper ? a[e] : b[e]);
             a[e] = upper ? x[e] : a[e];
             b[e] = upper ? b[e] : x[e];
           }
-          if (qa >= 0) use(qa, p + 32 * i, 4, a, la[i]);
-          if (qb >= 0) use(qb, p + 32 * i, 4, b, lb[i]);
+          if (qa >= 0) use(qa, p + 16 * i, 4, a, l[i][j]);
+          if (qb >= 0) use(qb, p + 16 * i, 4, b, l[i + 1][j]);
         }
       }
       return;
     }
+    const int p = wave_out() + 4 * (lane >> 4);
 #pragma unroll
     for (int j = 0; j < NQ; ++j) {
       const int64_t q = row(wave_q() + 16 * j + (lane & 15));
       if (q < 0) continue;
-      const int p = wave_out() + 4 * (lane >> 4);
-      Loaded l[N];
 #pragma unroll
-      for (int i = 0; i < N; ++i) l[i] = load(q, p + 16 * i, pn - p - 16 * i);
-#pragma unroll
-      for (int i = 0; i < N; ++i) use(q, p + 16 * i, pn - p - 16 * i, acc[i][j], l[i]);
+      for (int i = 0; i < N; ++i) use(q, p + 16 * i, pn - p - 16 * i, acc[i][j], l[i][j]);
     }
   }
 
   // The first n of four elements; the others are 0.
   template <typename U>
-  __device__ static __forceinline__ f32x4 load_quad(const U* at, int n) {
-    typedef U quad __attribute__((ext_vector_type(4)));
-    quad v = {};
+  struct Quad {
+    typedef U type __attribute__((ext_vector_type(4)));
+  };
+  template <typename U>
+  __device__ static __forceinline__ typename Quad<U>::type load_quad(const U* at, int n) {
+    typename Quad<U>::type v = {};
     if (n >= 4) {
       __builtin_memcpy(&v, at, sizeof(v));
     } else {
@@ -365,7 +378,7 @@ struct TileOut {
       for (int i = 0; i < 3; ++i)
         if (i < n) v[i] = at[i];
     }
-    return __builtin_convertvector(v, f32x4);
+    return v;
   }
   // The first n of four outputs, rounded to nearest even in U.
   template <typename U>
@@ -454,8 +467,13 @@ struct Gemm : TileOut<BP, BQ, WP, WQ, TWO == kRowPairs> {
   }
 
   // Adds the sum over r < red (kTwoSums: both sums, each over r < red). LDS is free for other use after a barrier.
+  // last() is called once nothing more of the sum is asked for, before its last products where that helps.
+  struct Nothing {
+    __device__ __forceinline__ void operator()() const {}
+  };
+  template <typename Last = Nothing>
   __device__ static __forceinline__ void run(const Operand<T>& p, const Operand<T>& q, int red, uint8_t* lds,
-                                             Acc& acc) {
+                                             Acc& acc, Last&& last = Last()) {
     const int64_t ps = PT::step_stride(p), qs = QT::step_stride(q);
     typename PT::Off po[PT::kPer];
     typename QT::Off qo[QT::kPer];
@@ -496,7 +514,7 @@ struct Gemm : TileOut<BP, BQ, WP, WQ, TWO == kRowPairs> {
         compute(put, acc);
         lds_barrier();
       }
-      if (nk == 0) return;
+      if (nk == 0) return last();
       if (ST - 1 < nk) issue(end - kSlot);
       // The operands of one half step are read while the products of the half
       // before run; a slot is free, and filled with the step ST later, as soon as every wave has read its second half.
@@ -533,6 +551,7 @@ struct Gemm : TileOut<BP, BQ, WP, WQ, TWO == kRowPairs> {
       }
       read(get, 1, h1);
       multiply(h0, acc);
+      last();   // (with the first half's registers)
       multiply(h1, acc);
     } else {
       const int each = (red + kStep - 1) / kStep, nk = TWO == kTwoSums ? 2 * each : each;
@@ -558,7 +577,7 @@ struct Gemm : TileOut<BP, BQ, WP, WQ, TWO == kRowPairs> {
         PT::store(p, left(s), g.p, slot);
         QT::store(q, left(s), g.q, slot + PT::kBytes);
       };
-      if (nk == 0) return;
+      if (nk == 0) return last();
       if constexpr (PT::kPer + QT::kPer <= 6) {   // two steps on their way, where the registers hold them
         Stage g0, g1;
         load(0, g0);
@@ -589,6 +608,7 @@ struct Gemm : TileOut<BP, BQ, WP, WQ, TWO == kRowPairs> {
           if (s + 1 < nk) store(s + 1, g);
         }
       }
+      last();
     }
   }
 

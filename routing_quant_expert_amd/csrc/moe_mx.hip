@@ -215,9 +215,7 @@ __global__ __launch_bounds__(G::NT, 2) void k_mx(MxArgs a, const uint8_t* __rest
 #pragma unroll
     for (int i = 0; i < G::NP / 2; ++i)
 #pragma unroll
-      for (int j = 0; j < G::NQ; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) g[i][j][e] = gated(a.gate, g[i][j][e], u[i][j][e]);
+      for (int j = 0; j < G::NQ; ++j) g[i][j] = gated_all(a.gate, g[i][j], u[i][j]);
     store(g);
   } else {
     store(acc);
