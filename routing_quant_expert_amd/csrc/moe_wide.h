@@ -23,20 +23,22 @@
 
 namespace moe {
 
-// How the loads and reads of a step lie among its products, in groups of two products.
+// How the loads and reads of a step lie among its products, in groups of two products (32 cycles, in which LDS gives each
+// wave one operand). Evenly spread: 16384 rows over 4 groups of 2048 x 4096, gated, 430 us with two reads a group and the
+// loads in half of the step, 411 with one and the loads in two thirds of it.
 template <int NQ, int LOADS>
 struct WideOrder {
-  static constexpr int kGroups = 4 * NQ;                           // of a half step
-  static constexpr int kReads = 8 + NQ;                            // operands of a half step, two to a group
-  static constexpr int kFree = (kReads + 1) / 2 + NQ;              // all reads of the step are back: the barrier
-  static constexpr int kWindow = 2 * (kGroups - kFree);            // the loads' groups, half of them in each half step
+  static constexpr int kGroups = 4 * NQ;                                            // of a half step
+  static constexpr int kReads = 8 + NQ;                                             // operands of a half step
+  static constexpr int kEach = kReads > kGroups / 2 + 2 ? 2 : 1;                    // reads in a group
+  static constexpr int kFree = kReads + 2 < kGroups ? kReads + 2 : kGroups - 1;     // the step's reads are back: the barrier
+  static constexpr int kWindow = 2 * kGroups - kFree - kGroups / 5;                 // groups of the loads
   static constexpr int at(int load) { return kFree + load * kWindow / LOADS; }
-  static constexpr int first() {                                   // loads in the first half step
+  static constexpr int first() {                                                    // loads in the first half step
     int n = 0;
     while (n < LOADS && at(n) < kGroups) ++n;
     return n;
   }
-  static_assert(kFree < kGroups);
 };
 
 // The sums of a wide tile: wave w has outputs 128 (w % 2) on, and of every 32 rows the 16 from 16 (w / 2).
@@ -156,7 +158,7 @@ struct WideGemm : WideOut<TWO == kRowPairs> {
 #pragma unroll
       for (int g = 0; g < O::kGroups; ++g) {
 #pragma unroll
-        for (int n = 2 * g; n < 2 * g + 2; ++n)
+        for (int n = O::kEach * g; n < O::kEach * (g + 1); ++n)
           if (n < O::kReads) read(get, 1, n, h1);
         if (LOAD && g == O::kFree) lds_barrier();   // all have read the step
         multiply(h0, 2 * g, acc);
@@ -178,7 +180,7 @@ struct WideGemm : WideOut<TWO == kRowPairs> {
       for (int g = 0; g < O::kGroups; ++g) {
         if (NEXT) {
 #pragma unroll
-          for (int n = 2 * g; n < 2 * g + 2; ++n)
+          for (int n = O::kEach * g; n < O::kEach * (g + 1); ++n)
             if (n < O::kReads) read(then, 0, n, h0);
         }
         multiply(h1, 2 * g, acc);
