@@ -222,6 +222,46 @@ __global__ __launch_bounds__(G::NT, 2) void k_mx(MxArgs a, const uint8_t* __rest
   }
 }
 
+// The same in wide tiles.
+template <typename G, bool GATED, int ACT>
+__global__ __launch_bounds__(256, 1) void k_mx_wide(MxArgs a, const uint8_t* __restrict__ x, const uint8_t* __restrict__ xs,
+                                                   const uint8_t* __restrict__ w, const uint8_t* __restrict__ ws,
+                                                   const uint8_t* __restrict__ w2, const uint8_t* __restrict__ ws2,
+                                                   void* __restrict__ out) {
+  extern __shared__ __align__(16) uint8_t lds[];
+  report(a);
+  const Tile t = my_tile<G>(a, a.n);
+  if (t.rows <= 0) return;
+  const bool none = t.group < 0 || t.group >= a.groups;
+  const int p0 = t.p * G::kP, pn = a.n - p0;
+  const int64_t at = (none ? 0 : t.group) * a.w_group + p0 * a.w_stride;
+  const int64_t at_scale = (none ? 0 : t.group) * a.w_scale_group + p0 * a.w_scale;
+  const MxOperand P = {w + at, ws + at_scale, a.w_stride, a.w_scale, min(G::kP, pn), GATED ? elements_between(w, w2) : 0,
+                       GATED ? elements_between(ws, ws2) : 0};
+  const MxOperand Q = {x + t.row * a.x_stride, xs + t.row * a.x_scale, a.x_stride, a.x_scale, t.rows};
+  by_rows(t.rows, [&](auto parts) {
+    constexpr int NQ = parts, N = GATED ? 4 : 8;
+    f32x4 acc[8][NQ] = {};
+    if (!none) G::run(P, Q, a.k, lds, acc);
+    f32x4 sums[N][NQ];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int j = 0; j < NQ; ++j) {
+        if constexpr (GATED) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sums[i][j][e] = gated<ACT>(acc[2 * i][j][e], acc[2 * i + 1][j][e], a.gate.limit);
+        } else {
+          sums[i][j] = acc[i][j];
+        }
+      }
+    const int64_t to = t.row * a.y_stride + p0;
+    if (a.out_type == MOE_TYPE_F32) G::store(sums, (float*)out + to, a.y_stride, pn, t.rows);
+    else if (a.out_type == MOE_TYPE_BF16) G::store(sums, (bf16_t*)out + to, a.y_stride, pn, t.rows);
+    else G::store(sums, (fp16_t*)out + to, a.y_stride, pn, t.rows);
+  });
+}
+
 struct MxTensors {
   const void *x, *xs, *w, *ws, *w2, *ws2;
   void* out;
@@ -235,6 +275,20 @@ int launch_tile(const MxArgs& a, const MxTensors& v, hipStream_t s) {
                                                  u8(v.w), u8(v.ws), u8(v.w2), u8(v.ws2), v.out);
 }
 
+template <bool GATED>
+int launch_wide(const MxArgs& a, const MxTensors& v, hipStream_t s) {
+  typedef WideMx<GATED> G;
+  const int64_t tiles = row_tiles(a, G::kQ) * ((a.n + G::kP - 1) / G::kP);
+  auto with = [&](auto act) {
+    constexpr int ACT = act;
+    auto u8 = [](const void* p) { return (const uint8_t*)p; };
+    return launch_rows_of_tiles<k_mx_wide<G, GATED, ACT>, G>("mx", tiles, s, a, u8(v.x), u8(v.xs), u8(v.w), u8(v.ws), u8(v.w2),
+                                                             u8(v.ws2), v.out);
+  };
+  return GATED && a.gate.act == MOE_ACT_GELU ? with(std::integral_constant<int, GATED ? MOE_ACT_GELU : MOE_ACT_SILU>())
+                                             : with(std::integral_constant<int, MOE_ACT_SILU>());
+}
+
 template <bool GATED, bool DMA>
 int launch_mx(const MxArgs& a, const MxTensors& v, hipStream_t s) {
   const int64_t mean = a.rows / a.groups;
@@ -242,7 +296,8 @@ int launch_mx(const MxArgs& a, const MxTensors& v, hipStream_t s) {
   if (mean < 16 || row_tiles(a, 64) * ((wide + 127) / 128) < 96) return launch_tile<GATED, DMA, 128, 16, 4, 1, 4, 2>(a, v, s);
   if (mean < 64 || row_tiles(a, 128) * ((wide + 127) / 128) < 300) return launch_tile<GATED, DMA, 128, 64, 2, 2, 3, 2>(a, v, s);
   if constexpr (DMA) {
-    if (row_tiles(a, 128) * ((wide + 255) / 256) >= 768 && a.k >= 4096) return launch_tile<GATED, DMA, 256, 128, 4, 2, 3, 2>(a, v, s);
+    if (row_tiles(a, 128) * ((wide + 255) / 256) >= 768 && a.k >= 1024 && a.k % WideMx<GATED>::kGroup == 0)
+      return launch_wide<GATED>(a, v, s);
   }
   return launch_tile<GATED, DMA, 128, 128, 2, 2, 2, 4>(a, v, s);
 }

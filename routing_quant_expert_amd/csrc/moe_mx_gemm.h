@@ -15,7 +15,7 @@
 // steps at once, into buffers of their own.
 #pragma once
 
-#include "moe_gemm.h"
+#include "moe_wide.h"
 
 namespace moe {
 
@@ -126,6 +126,23 @@ struct MxTile {
     for (int k = 0; k < kPerScales; ++k)
       asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
                    : : "v"(off[k]), "s"(at), "s"(first + 4 * NT * k) : "memory", "m0");
+  }
+  // The thread's k-th word of scales, for any k.
+  __device__ static __forceinline__ uint32_t word_offset(const MxOperand& o, int k) {
+    static_assert(G == 4 && NT == 256);   // 32 rows to k
+    const int row = threadIdx.x / 8, first = PAIRS ? row % 16 : row;
+    return (uint32_t)min(first + (PAIRS ? 16 : 32) * k, o.count - 1) * (uint32_t)o.scale_ld + 4 * (threadIdx.x % 8 ^ turned(row));
+  }
+  // One chunk, and one word of scales, alone.
+  __device__ static __forceinline__ void dma_code(const uint8_t* at, uint32_t off, uint32_t tile, int k) {
+    const uint32_t first = tile + 16 * 64 * __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+                 : : "v"(off), "s"(at), "s"(first + 16 * NT * k) : "memory", "m0");
+  }
+  __device__ static __forceinline__ void dma_scale(const uint8_t* at, uint32_t off, uint32_t buffer, int k) {
+    const uint32_t first = buffer + 4 * 64 * __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
+                 : : "v"(off), "s"(at), "s"(first + 4 * NT * k) : "memory", "m0");
   }
 #pragma clang diagnostic pop
 
@@ -371,6 +388,157 @@ struct MxGemm : TileOut<BP, BQ, WP, WQ, PAIRS> {
         if (s + 1 < nk) store(g, lds + (s + 1 & 1) * kSlot, buffers + (s + 1 & 1) * kBuffer);
       }
     }
+  }
+};
+
+// The same in wide tiles (moe_wide.h): rows of whole groups of four steps (k a multiple of 1024), 16-byte aligned codes and
+// 4-byte aligned scales. The scales of four steps come in quarters, one beside the codes of each step, during the four
+// steps that end one before they are needed: a buffer's last step has then been read by all.
+template <bool PAIRS>
+struct WideMx : WideOut<PAIRS> {
+  typedef MxTile<256, 256, PAIRS, 4> PT;
+  typedef MxTile<256, 256, false, 4> QT;
+  typedef WideOut<PAIRS> Out;
+  static constexpr int kSlot = PT::kCodes + QT::kCodes;
+  static constexpr int kBuffer = PT::kScales + QT::kScales;
+  static constexpr int kLds = 2 * kSlot + 2 * kBuffer;   // all of a CU's
+  static constexpr int kGroup = 4 * kMxStep;
+
+  template <int NQ>
+  struct Half {
+    i32x4 p[8], q[NQ];
+    int ps[8], qs[NQ];
+  };
+  // Read number n of a half step: the rows' operands, then P's; in the first half with their scales.
+  template <int KK, int NQ>
+  __device__ static __forceinline__ void read(const uint8_t* slot, const uint8_t* buffer, int in, int n, Half<NQ>& h, const Half<NQ>* first) {
+    const int lane = threadIdx.x & 63;
+    if (n < NQ) {
+      const int own = 32 * n + 16 * (Out::wave() / 2);
+      h.q[n] = QT::operand(slot + PT::kCodes, own, KK, lane);
+      h.qs[n] = KK ? first->qs[n] : QT::scale(buffer + PT::kScales, own, in, lane);
+    } else {
+      const int i = n - NQ, own = Out::wave_p() + 16 * i;
+      h.p[i] = PT::operand(slot, own, KK, lane);
+      h.ps[i] = KK ? first->ps[i] : PT::scale(buffer, own, in, lane);
+    }
+  }
+  template <int KK, int NQ>
+  __device__ static __forceinline__ void multiply(const Half<NQ>& h, int n, f32x4 (&acc)[8][NQ]) {
+    const int i = n / NQ, j = n % NQ;
+    acc[i][j] = mfma_mx<KK>(h.p[i], h.q[j], acc[i][j], h.ps[i], h.qs[j]);
+  }
+
+  template <int NQ>
+  __device__ static __forceinline__ void run(const MxOperand& p, const MxOperand& q, int k, uint8_t* lds, f32x4 (&acc)[8][NQ]) {
+    // a step's loads: 8 + NQ of codes, and of a quarter of scales two of P's and NQ / 4 of the rows' (NQ = 6: two, NQ = 2: one,
+    // of which some repeat the last)
+    constexpr int kScaleQ = (NQ + 3) / 4, kLoads = 8 + NQ + 2 + kScaleQ;
+    typedef WideOrder<NQ, kLoads> O;
+    const int nk = k / kMxStep, groups = nk / 4;
+    typename PT::Offsets po;
+    typename QT::Offsets qo;
+    PT::offsets(p, po);
+    QT::offsets(q, qo);
+    const uint8_t *pc = uniform(PT::codes(p)), *qc = uniform(q.codes), *ps = uniform(PT::scales(p)), *qs = uniform(q.scales);
+    uint8_t* const buffers = lds + 2 * kSlot;
+    // Number n of a step's loads, codes into `at`; the scales are quarter `part` of a buffer at `to`.
+    auto load = [&](int n, uint32_t at, uint32_t to, int part) {
+      if (n < 8) {
+        PT::dma_code(pc, po.codes[n], at, n);
+      } else if (n < 8 + NQ) {
+        QT::dma_code(qc, qo.codes[n - 8], at + PT::kCodes, n - 8);
+      } else if (n < 8 + NQ + 2) {
+        const int w = 2 * part + n - 8 - NQ;
+        PT::dma_scale(ps, PT::word_offset(p, w), to, w);
+      } else {
+        const int w = min(kScaleQ * part + n - 8 - NQ - 2, NQ - 1);
+        QT::dma_scale(qs, QT::word_offset(q, w), to + PT::kScales, w);
+      }
+    };
+    auto loaded = [&] {
+      pc += 128;
+      qc += 128;
+    };
+    // group 0's scales, then the codes of steps 0 and 1 with the first quarter of group 1's scales
+#pragma unroll
+    for (int n = 0; n < 8; ++n) PT::dma_scale(ps, PT::word_offset(p, n), lds_offset(buffers), n);
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) QT::dma_scale(qs, QT::word_offset(q, n), lds_offset(buffers) + PT::kScales, n);
+    if (groups > 1) {
+      ps += 32;
+      qs += 32;
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+#pragma unroll
+      for (int n = 0; n < 8 + NQ; ++n) load(n, lds_offset(lds) + s * kSlot, 0, 0);
+      loaded();
+    }
+#pragma unroll
+    for (int n = 8 + NQ; n < kLoads; ++n) load(n, 0, lds_offset(buffers) + kBuffer, 0);
+    Half<NQ> h0, h1;
+    wait_vmcnt<kLoads>();
+    lds_barrier();
+    const uint8_t *get = lds, *then = lds + kSlot;
+    const uint8_t *scales = buffers;
+#pragma unroll
+    for (int n = 0; n < O::kReads; ++n) read<0>(get, scales, 0, n, h0, (const Half<NQ>*)nullptr);
+    // Step s; with LOAD the codes of step s + 2, and the scales that step s + 1's quarter stands for, are asked for.
+    auto step = [&](int s, auto LOAD, auto NEXT) {
+      const uint32_t at = lds_offset(get);
+      const int part = (s + 1) & 3;
+      if (LOAD && part == 0) {   // the next group's, or the last one's again
+        const bool more = (s + 1) / 4 + 1 < groups;
+        ps += more ? 32 : 0;
+        qs += more ? 32 : 0;
+      }
+      const uint32_t to = lds_offset(buffers) + ((((s + 1) >> 2) + 1) & 1) * kBuffer;
+#pragma unroll
+      for (int g = 0; g < O::kGroups; ++g) {
+#pragma unroll
+        for (int n = O::kEach * g; n < O::kEach * (g + 1); ++n)
+          if (n < O::kReads) read<1>(get, scales, 0, n, h1, &h0);
+        if (LOAD && g == O::kFree) lds_barrier();   // all have read the step
+        multiply<0>(h0, 2 * g, acc);
+        multiply<0>(h0, 2 * g + 1, acc);
+        if (LOAD) {
+#pragma unroll
+          for (int n = 0; n < kLoads; ++n)
+            if (O::at(n) == g) load(n, at, to, part);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (NEXT) {   // the next step is there, for every wave
+        wait_vmcnt<LOAD ? O::first() : 0>();
+        lds_barrier();
+        if (part == 0) scales = scales == buffers ? buffers + kBuffer : buffers;
+      }
+#pragma unroll
+      for (int g = 0; g < O::kGroups; ++g) {
+        if (NEXT) {
+#pragma unroll
+          for (int n = O::kEach * g; n < O::kEach * (g + 1); ++n)
+            if (n < O::kReads) read<0>(then, scales, part, n, h0, (const Half<NQ>*)nullptr);
+        }
+        multiply<1>(h1, 2 * g, acc);
+        multiply<1>(h1, 2 * g + 1, acc);
+        if (LOAD) {
+#pragma unroll
+          for (int n = 0; n < kLoads; ++n)
+            if (O::at(n) == O::kGroups + g) load(n, at, to, part);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (LOAD) loaded();
+      const uint8_t* const was = get;
+      get = then;
+      then = was;
+    };
+#pragma unroll 1
+    for (int s = 0; s < nk - 2; ++s) step(s, std::true_type(), std::true_type());
+    step(nk - 2, std::false_type(), std::true_type());
+    step(nk - 1, std::false_type(), std::false_type());
   }
 };
 
