@@ -24,14 +24,15 @@ constexpr int kMxBlock = 32;   // elements of a scale
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 
-// C += A B of the lane's 32 elements each; byte KK of the scales.
-template <int KK>
+// C += A B of the lane's 32 elements each; bytes SA and SB of the scales.
+template <int SA, int SB>
 __device__ __forceinline__ f32x4 mfma_mx(i32x4 a, i32x4 b, f32x4 c, int sa, int sb) {
   constexpr int kFp4 = 4;
   const i32x8 a8 = __builtin_shufflevector(a, a, 0, 1, 2, 3, -1, -1, -1, -1);
   const i32x8 b8 = __builtin_shufflevector(b, b, 0, 1, 2, 3, -1, -1, -1, -1);
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b8, c, kFp4, kFp4, KK, sa, KK, sb);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b8, c, kFp4, kFp4, SA, sa, SB, sb);
 }
 
 // The rows of a tile: `count` of them, codes `ld` and scales `scale_ld` bytes apart. Of a pair of matrices (as kRowPairs)
@@ -247,7 +248,7 @@ struct MxGemm : TileOut<BP, BQ, WP, WQ, PAIRS> {
 #pragma unroll
     for (int i = 0; i < NP; ++i)
 #pragma unroll
-      for (int j = 0; j < NQ; ++j) acc[i][j] = mfma_mx<KK>(h.p[i], h.q[j], acc[i][j], h.ps[i], h.qs[j]);
+      for (int j = 0; j < NQ; ++j) acc[i][j] = mfma_mx<KK, KK>(h.p[i], h.q[j], acc[i][j], h.ps[i], h.qs[j]);
   }
   // Places `READS` LDS reads evenly among the first products of the half before.
   template <int READS>
@@ -404,29 +405,52 @@ struct WideMx : WideOut<PAIRS> {
   static constexpr int kLds = 2 * kSlot + 2 * kBuffer;   // all of a CU's
   static constexpr int kGroup = 4 * kMxStep;
 
+  // Two operands' scales of a step share a register: bytes 2 (i % 2) + kk.
   template <int NQ>
   struct Half {
     i32x4 p[8], q[NQ];
-    int ps[8], qs[NQ];
+    u16x2 ps[4], qs[NQ / 2];
   };
-  // Read number n of a half step: the rows' operands, then P's; in the first half with their scales.
+  // Where a lane's operands lie in a slot and its scales in a buffer: the rows' n-th 4096 n bytes (scales: 1024 n) after `q`,
+  // P's i-th 2048 i (512 i) after `p`; the scales of the buffer's step `in` are at the place with 8 in XORed to it.
+  struct Places {
+    uint32_t p[2], q[2], ps, qs;
+    __device__ __forceinline__ Places() {
+      const int lane = threadIdx.x & 63, row = lane & 15;
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) {
+        const uint32_t at = 128 * row + 16 * ((2 * (lane >> 4) + kk) ^ (row & 7));
+        q[kk] = PT::kCodes + 128 * 16 * (Out::wave() / 2) + at;
+        p[kk] = 128 * Out::wave_p() + at;
+      }
+      const uint32_t at = 32 * row + 4 * (lane >> 5 ^ PT::turned(row)) + 2 * (lane >> 4 & 1);
+      qs = PT::kScales + 32 * 16 * (Out::wave() / 2) + at;
+      ps = 32 * Out::wave_p() + at;
+    }
+  };
+  // Read number n of half step KK of a slot: the rows' operands, then P's; in the first half with their scales, which the
+  // second half takes from `first`.
   template <int KK, int NQ>
-  __device__ static __forceinline__ void read(const uint8_t* slot, const uint8_t* buffer, int in, int n, Half<NQ>& h, const Half<NQ>* first) {
-    const int lane = threadIdx.x & 63;
+  __device__ static __forceinline__ void read(uint32_t slot, uint32_t ps, uint32_t qs, const Places& places, int n, Half<NQ>& h,
+                                              const Half<NQ>* first) {
+    typedef unsigned short u16;
     if (n < NQ) {
-      const int own = 32 * n + 16 * (Out::wave() / 2);
-      h.q[n] = QT::operand(slot + PT::kCodes, own, KK, lane);
-      h.qs[n] = KK ? first->qs[n] : QT::scale(buffer + PT::kScales, own, in, lane);
+      h.q[n] = lds_at<i32x4>(slot + places.q[KK] + 4096 * n);
+      if (!KK) h.qs[n / 2][n % 2] = lds_at<u16>(qs + 1024 * n);
+      else if (n % 2) h.qs[n / 2] = first->qs[n / 2];
     } else {
-      const int i = n - NQ, own = Out::wave_p() + 16 * i;
-      h.p[i] = PT::operand(slot, own, KK, lane);
-      h.ps[i] = KK ? first->ps[i] : PT::scale(buffer, own, in, lane);
+      const int i = n - NQ;
+      h.p[i] = lds_at<i32x4>(slot + places.p[KK] + 2048 * i);
+      if (!KK) h.ps[i / 2][i % 2] = lds_at<u16>(ps + 512 * i);
+      else if (i % 2) h.ps[i / 2] = first->ps[i / 2];
     }
   }
   template <int KK, int NQ>
   __device__ static __forceinline__ void multiply(const Half<NQ>& h, int n, f32x4 (&acc)[8][NQ]) {
-    const int i = n / NQ, j = n % NQ;
-    acc[i][j] = mfma_mx<KK>(h.p[i], h.q[j], acc[i][j], h.ps[i], h.qs[j]);
+    const int i = n / NQ, j = n % NQ, a = __builtin_bit_cast(int, h.ps[i / 2]), b = __builtin_bit_cast(int, h.qs[j / 2]);
+    f32x4& c = acc[i][j];
+    if (i % 2) c = j % 2 ? mfma_mx<2 + KK, 2 + KK>(h.p[i], h.q[j], c, a, b) : mfma_mx<2 + KK, KK>(h.p[i], h.q[j], c, a, b);
+    else c = j % 2 ? mfma_mx<KK, 2 + KK>(h.p[i], h.q[j], c, a, b) : mfma_mx<KK, KK>(h.p[i], h.q[j], c, a, b);
   }
 
   template <int NQ>
@@ -480,13 +504,13 @@ struct WideMx : WideOut<PAIRS> {
     Half<NQ> h0, h1;
     wait_vmcnt<kLoads>();
     lds_barrier();
-    const uint8_t *get = lds, *then = lds + kSlot;
-    const uint8_t *scales = buffers;
+    uint32_t get = lds_offset(lds), then = get + kSlot, scales = lds_offset(buffers);
+    const Places places;
 #pragma unroll
-    for (int n = 0; n < O::kReads; ++n) read<0>(get, scales, 0, n, h0, (const Half<NQ>*)nullptr);
+    for (int n = 0; n < O::kReads; ++n) read<0>(get, scales + places.ps, scales + places.qs, places, n, h0, (const Half<NQ>*)nullptr);
     // Step s; with LOAD the codes of step s + 2, and the scales that step s + 1's quarter stands for, are asked for.
     auto step = [&](int s, auto LOAD, auto NEXT) {
-      const uint32_t at = lds_offset(get);
+      const uint32_t at = get;
       const int part = (s + 1) & 3;
       if (LOAD && part == 0) {   // the next group's, or the last one's again
         const bool more = (s + 1) / 4 + 1 < groups;
@@ -498,7 +522,7 @@ struct WideMx : WideOut<PAIRS> {
       for (int g = 0; g < O::kGroups; ++g) {
 #pragma unroll
         for (int n = O::kEach * g; n < O::kEach * (g + 1); ++n)
-          if (n < O::kReads) read<1>(get, scales, 0, n, h1, &h0);
+          if (n < O::kReads) read<1>(get, 0, 0, places, n, h1, &h0);
         if (LOAD && g == O::kFree) lds_barrier();   // all have read the step
         multiply<0>(h0, 2 * g, acc);
         multiply<0>(h0, 2 * g + 1, acc);
@@ -512,14 +536,15 @@ struct WideMx : WideOut<PAIRS> {
       if (NEXT) {   // the next step is there, for every wave
         wait_vmcnt<LOAD ? O::first() : 0>();
         lds_barrier();
-        if (part == 0) scales = scales == buffers ? buffers + kBuffer : buffers;
+        if (part == 0) scales = scales == lds_offset(buffers) ? scales + kBuffer : lds_offset(buffers);
       }
+      const uint32_t ps_at = scales + (places.ps ^ 8 * part), qs_at = scales + (places.qs ^ 8 * part);
 #pragma unroll
       for (int g = 0; g < O::kGroups; ++g) {
         if (NEXT) {
 #pragma unroll
           for (int n = O::kEach * g; n < O::kEach * (g + 1); ++n)
-            if (n < O::kReads) read<0>(then, scales, part, n, h0, (const Half<NQ>*)nullptr);
+            if (n < O::kReads) read<0>(then, ps_at, qs_at, places, n, h0, (const Half<NQ>*)nullptr);
         }
         multiply<1>(h1, 2 * g, acc);
         multiply<1>(h1, 2 * g + 1, acc);
@@ -531,10 +556,11 @@ struct WideMx : WideOut<PAIRS> {
         __builtin_amdgcn_sched_barrier(0);
       }
       if (LOAD) loaded();
-      const uint8_t* const was = get;
+      const uint32_t was = get;
       get = then;
       then = was;
     };
+    own_registers(acc);
 #pragma unroll 1
     for (int s = 0; s < nk - 2; ++s) step(s, std::true_type(), std::true_type());
     step(nk - 2, std::false_type(), std::true_type());

@@ -85,6 +85,20 @@ struct WideOut {
   }
 };
 
+// Every sum in registers of its own before the loop: zeroed ones would share theirs, and be moved apart in every step.
+template <int NQ>
+__device__ __forceinline__ void own_registers(f32x4 (&acc)[8][NQ]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < NQ; ++j) asm volatile("" : "+a"(acc[i][j]));
+}
+
+template <typename V>
+__device__ __forceinline__ V lds_at(uint32_t offset) {
+  return *(const __attribute__((address_space(3))) V*)offset;
+}
+
 // Whole steps of rows that start 16-byte aligned (columns: widths that are multiples of 8). DMA only.
 template <typename T, bool PCOL, Two TWO>
 struct WideGemm : WideOut<TWO == kRowPairs> {
@@ -100,12 +114,43 @@ struct WideGemm : WideOut<TWO == kRowPairs> {
   struct Half {
     oct<T> p[8], q[NQ];
   };
-  // Read number n of a half step: the rows' operands, then P's.
+  // Where a lane's operands lie in a slot (TileOf::operand): the rows' n-th 4096 n bytes after `q` of its half step, P's i-th
+  // 2048 i after `p` of its half step, or of columns 16384 kk after its own `p`. A wave issues one instruction in 4 cycles,
+  // 512 in a step's products, so an address for every read would cost.
+  struct Places {
+    uint32_t p[PCOL ? 8 : 2], q[2];
+    __device__ __forceinline__ Places() {
+      const int lane = threadIdx.x & 63, row = lane & 15, chunk = lane >> 4;
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) {
+        const uint32_t at = 128 * row + 16 * ((4 * kk + chunk) ^ QT::swizzle(row));
+        q[kk] = PT::kBytes + 128 * 16 * (Out::wave() / 2) + at;
+        if (!PCOL) p[kk] = 128 * Out::wave_p() + at;
+      }
+      if constexpr (PCOL) {
+        const int r = 8 * chunk + (row >> 2), col = Out::wave_p() + 4 * (lane & 3);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int own = col + 16 * i;
+          p[i] = 16 * (r * PT::kRowChunks + ((own >> 3) ^ PT::swizzle(r))) + 2 * (own & 7);
+        }
+      }
+    }
+  };
+  // Read number n of half step kk of a slot: the rows' operands, then P's.
   template <int NQ>
-  __device__ static __forceinline__ void read(const uint8_t* slot, int kk, int n, Half<NQ>& h) {
-    const int lane = threadIdx.x & 63;
-    if (n < NQ) h.q[n] = QT::operand(slot + PT::kBytes, 32 * n + 16 * (Out::wave() / 2), kk, lane);
-    else h.p[n - NQ] = PT::operand(slot, Out::wave_p() + 16 * (n - NQ), kk, lane);
+  __device__ static __forceinline__ void read(uint32_t slot, const Places& places, int kk, int n, Half<NQ>& h) {
+    if (n < NQ) {
+      h.q[n] = lds_at<oct<T>>(slot + places.q[kk] + 4096 * n);
+    } else if constexpr (!PCOL) {
+      h.p[n - NQ] = lds_at<oct<T>>(slot + places.p[kk] + 2048 * (n - NQ));
+    } else {
+      const uint32_t at = slot + places.p[n - NQ] + 32 * 16 * PT::kRowChunks * kk;
+      struct { s16x4 lo, hi; } v;
+      v.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_tr_t)at);
+      v.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_tr_t)(at + 4 * 16 * PT::kRowChunks));
+      h.p[n - NQ] = __builtin_bit_cast(oct<T>, v);
+    }
   }
   template <int NQ>
   __device__ static __forceinline__ void multiply(const Half<NQ>& h, int n, f32x4 (&acc)[8][NQ]) {
@@ -149,17 +194,18 @@ struct WideGemm : WideOut<TWO == kRowPairs> {
     Half<NQ> h0, h1;
     wait_vmcnt<8 + NQ>();
     lds_barrier();
+    uint32_t get = lds_offset(lds), then = get + kSlot;
+    const Places places;
 #pragma unroll
-    for (int n = 0; n < O::kReads; ++n) read(lds, 0, n, h0);
-    const uint8_t *get = lds, *then = lds + kSlot;
+    for (int n = 0; n < O::kReads; ++n) read(get, places, 0, n, h0);
     // The two half steps of a step. LOAD: the step after next follows; NEXT: the next one does.
     auto step = [&](auto LOAD, auto NEXT) {
-      const uint32_t at = lds_offset(get);
+      const uint32_t at = get;
 #pragma unroll
       for (int g = 0; g < O::kGroups; ++g) {
 #pragma unroll
         for (int n = O::kEach * g; n < O::kEach * (g + 1); ++n)
-          if (n < O::kReads) read(get, 1, n, h1);
+          if (n < O::kReads) read(get, places, 1, n, h1);
         if (LOAD && g == O::kFree) lds_barrier();   // all have read the step
         multiply(h0, 2 * g, acc);
         multiply(h0, 2 * g + 1, acc);
@@ -181,7 +227,7 @@ struct WideGemm : WideOut<TWO == kRowPairs> {
         if (NEXT) {
 #pragma unroll
           for (int n = O::kEach * g; n < O::kEach * (g + 1); ++n)
-            if (n < O::kReads) read(then, 0, n, h0);
+            if (n < O::kReads) read(then, places, 0, n, h0);
         }
         multiply(h1, 2 * g, acc);
         multiply(h1, 2 * g + 1, acc);
@@ -193,10 +239,11 @@ struct WideGemm : WideOut<TWO == kRowPairs> {
         __builtin_amdgcn_sched_barrier(0);
       }
       if (LOAD) loaded();
-      const uint8_t* const was = get;
+      const uint32_t was = get;
       get = then;
       then = was;
     };
+    own_registers(acc);
 #pragma unroll 1
     for (int s = 0; s < nk - 2; ++s) step(std::true_type(), std::true_type());
     step(std::false_type(), std::true_type());
