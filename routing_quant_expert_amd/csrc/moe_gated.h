@@ -53,22 +53,40 @@ int launch_gated_tile(const GatedArgs& a, const GatedTensors& v, hipStream_t s) 
   return K::template narrow<T, G>(row_tiles(a, G::kQ) * ((width + G::kP - 1) / G::kP), a, v, s);
 }
 
+// Which tiles. The times are of bf16 at n = 2048, k = 4096, rows as `rows of groups` (a power law of 0.4), in us.
+// Few tiles (up to two of 64 columns for a CU): the smallest, for more workgroups. 1 of 1: forward 12.3 against 15.1 in
+// tiles of 128 columns, hidden 12.8 (16.7), input 12.6 (16.8); past it those read the rows less often: hidden of 100 of 8 37.4 (28.8).
+// Unaligned rows wait longer for each load: up to three. 1000 rows of 13, 257 and 515 wide: 13.6 (17.1).
+// Tall tiles for few rows: under 6 a group 172.7 at 64 of 32 against 173.7 with 64 rows, 192.3 (176.5) at 250 of 32; and where
+// tiles of 64 rows would be few: hidden of 256 of 1 19.7 (29.5).
+// Wide tiles (moe_wide.h) where the sum is long: a round of 256 of them takes about three halves of one of 512 tiles of 128 x 128,
+// so where 3 times its rounds are no more than twice theirs. Forward of 16384 of 32 530 (597), 2048 of 4 85 (123), but
+// 2048 of 1 88 (67). From 768 tiles on, what counts is the weights' reading, which they do in longer rows: 96 groups of 128 rows 723 (774),
+// input 644 (776). The backward pass, whose weights' rows lie across the sum, gains by that with few rows too, if most of the
+// CUs have a tile: input of 64 of 32 165 (186), 32 of 8 60 (50). The forward pass does not under 24 rows: 4000 of 384 2198 (2194).
+// At a sum of 1024 little is left of it: forward of 16384 of 16, n = 1024, 106 (115), n = 512 66 (56).
 template <GatedWay W, typename K, typename T, bool DMA>
 int launch_gated_rows(const GatedArgs& a, const GatedTensors& v, hipStream_t s) {
   const int64_t mean = a.rows / a.groups;
   const int width = W == kInput ? a.k : a.n, wide = W == kForward ? 2 * width : width;   // columns of P
-  if (mean < 16 || row_tiles(a, 64) * ((wide + 127) / 128) < 96)
-    return launch_gated_tile<W, K, T, DMA, 128, 16, 4, 1, 4>(a, v, s);
-  if (mean < 64 || row_tiles(a, 128) * ((wide + 127) / 128) < 300)
-    return launch_gated_tile<W, K, T, DMA, 128, 64, 2, 2, 3>(a, v, s);
+  auto columns = [&](int p) { return (wide + p - 1) / p; };
+  constexpr int kFewRows = W == kForward ? 32 : 16;   // (of 16 rows a wave would have no row of both projections)
+  if (row_tiles(a, kFewRows) * columns(64) <= (DMA ? 480 : 768)) {
+    if constexpr (W == kForward) return launch_gated_tile<W, K, T, DMA, 64, 32, 2, 2, 4>(a, v, s);
+    else return launch_gated_tile<W, K, T, DMA, 64, 16, 4, 1, 4>(a, v, s);
+  }
   if constexpr (DMA) {
     const int red = W == kInput ? a.n : a.k;
-    if (row_tiles(a, 128) * ((wide + 255) / 256) >= 768 && red >= 1024) {
+    const int64_t tiles = likely_row_tiles(a, 256) * columns(256), small = likely_row_tiles(a, 128) * columns(128);
+    const bool pays = mean < 64 ? W != kForward ? tiles >= 128 : mean >= 24 && tiles >= 768
+                                : tiles >= 768 || 3 * rounds(a, tiles, 256) <= 2 * rounds(a, small, 512);
+    if (pays && red >= 1024 && red % kStep == 0) {
       typedef WideGemm<T, W != kForward, W == kForward ? kRowPairs : W == kInput ? kTwoSums : kSingle> G;
-      if (red % kStep == 0) return K::template wide<T, G>(row_tiles(a, G::kQ) * ((width + G::kP - 1) / G::kP), a, v, s);
-      return launch_gated_tile<W, K, T, DMA, 256, 128, 4, 2, 3>(a, v, s);
+      return K::template wide<T, G>(row_tiles(a, G::kQ) * ((width + G::kP - 1) / G::kP), a, v, s);
     }
   }
+  if (mean < 6 || row_tiles(a, 64) * columns(128) <= 160) return launch_gated_tile<W, K, T, DMA, 128, 16, 4, 1, 4>(a, v, s);
+  if (mean < 64 || row_tiles(a, 128) * columns(128) < 300) return launch_gated_tile<W, K, T, DMA, 128, 64, 2, 2, 3>(a, v, s);
   return launch_gated_tile<W, K, T, DMA, 128, 128, 2, 2, 2>(a, v, s);
 }
 

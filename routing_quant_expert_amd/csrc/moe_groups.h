@@ -130,4 +130,14 @@ inline int64_t row_tiles(const Groups& a, int q) {
   return (a.rows + (q - 1) * some) / q;
 }
 
+// About so many: half a partial tile a group. (What a launch rule compares; the grid is the bound.)
+inline int64_t likely_row_tiles(const Groups& a, int q) {
+  return a.groups == 1 ? (a.rows + q - 1) / q : a.rows / q + (a.groups < a.rows ? a.groups : a.rows) / 2;
+}
+
+// Rounds of `tiles` workgroups of which `at_once` run at a time. (The tiles of several groups are guessed: on a tie there is one more.)
+inline int64_t rounds(const Groups& a, int64_t tiles, int at_once) {
+  return a.groups == 1 ? (tiles + at_once - 1) / at_once : tiles / at_once + 1;
+}
+
 }  // namespace moe

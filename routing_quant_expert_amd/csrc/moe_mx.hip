@@ -289,16 +289,30 @@ int launch_wide(const MxArgs& a, const MxTensors& v, hipStream_t s) {
                                              : with(std::integral_constant<int, MOE_ACT_SILU>());
 }
 
+// Which tiles, by the same reckoning as the 16-bit products' (moe_gated.h). The times are at n = 2048, k = 4096, in us.
+// Few rows: plain in tiles of 64 x 16, 48 of 384 39.2 against 42.6 in 128 x 16 and 44.1 in 128 x 64, 1 of 1 7.1 (8.9, 11.4), up to
+// some thousand tiles: 128 of 64 58 (51 in 128 x 16); gated in 64 x 32 while the tiles are few, 1 of 1 8.1 (9.5 in 128 x 16), then in 128 x 16: 48 of 384 75.7 (82.4).
+// Wide tiles from a sum of 2048 on: 12288 rows of 64 groups plain 112 (130), gated 190 (238), 12288 of 384 gated 682 (721 in 128 x 64);
+// but 4096 of 384 640 (607), 8192 of 16 plain 66 (60), and with k = 1024 16384 of 16, n = 1024, 30.4 (26.6).
 template <bool GATED, bool DMA>
 int launch_mx(const MxArgs& a, const MxTensors& v, hipStream_t s) {
   const int64_t mean = a.rows / a.groups;
   const int wide = GATED ? 2 * a.n : a.n;   // columns of P
-  if (mean < 16 || row_tiles(a, 64) * ((wide + 127) / 128) < 96) return launch_tile<GATED, DMA, 128, 16, 4, 1, 4, 2>(a, v, s);
-  if (mean < 64 || row_tiles(a, 128) * ((wide + 127) / 128) < 300) return launch_tile<GATED, DMA, 128, 64, 2, 2, 3, 2>(a, v, s);
-  if constexpr (DMA) {
-    if (row_tiles(a, 128) * ((wide + 255) / 256) >= 768 && a.k >= 1024 && a.k % WideMx<GATED>::kGroup == 0)
-      return launch_wide<GATED>(a, v, s);
+  auto columns = [&](int p) { return (wide + p - 1) / p; };
+  if constexpr (GATED) {
+    if (row_tiles(a, 32) * columns(64) <= 1024) return launch_tile<GATED, DMA, 64, 32, 2, 2, 3, 4>(a, v, s);
+    if (mean < 6) return launch_tile<GATED, DMA, 128, 16, 4, 1, 4, 2>(a, v, s);
+  } else {
+    const bool small = row_tiles(a, 64) * columns(128) <= 192;
+    if (small || (mean < 6 && row_tiles(a, 16) * columns(64) <= 2048)) return launch_tile<GATED, DMA, 64, 16, 4, 1, 4, 2>(a, v, s);
+    if (mean < 6) return launch_tile<GATED, DMA, 128, 16, 4, 1, 4, 2>(a, v, s);
   }
+  if constexpr (DMA) {
+    const int64_t tiles = likely_row_tiles(a, 256) * columns(256), small = likely_row_tiles(a, 128) * columns(128);
+    const bool pays = tiles >= 768 ? mean >= 24 : mean >= 64 && 3 * rounds(a, tiles, 256) < 2 * rounds(a, small, 512);
+    if (pays && a.k >= 2048 && a.k % WideMx<GATED>::kGroup == 0) return launch_wide<GATED>(a, v, s);
+  }
+  if (mean < 64 || row_tiles(a, 128) * columns(128) < 256) return launch_tile<GATED, DMA, 128, 64, 2, 2, 3, 2>(a, v, s);
   return launch_tile<GATED, DMA, 128, 128, 2, 2, 2, 4>(a, v, s);
 }
 
