@@ -425,7 +425,9 @@ int moe_read_probe(const void* buf, uint64_t bytes, uint32_t* sink, int32_t bloc
 /* ---- Operators beside the layer -------------------------------------------
  * What joins the layer to the rest of a model: the norms, gate and residual
  * scale around a block (moe_join_*), products grouped by expert on 16-bit
- * weights with their gradients (moe_grouped_*), and the low-rank adapters of
+ * weights with their gradients (moe_grouped_*), the gated feed-forward on them
+ * with its gradients (moe_gated_*), rows in microscaled 4-bit floats and the
+ * products of such operands (moe_mx_*), and the low-rank adapters of
  * many requests beside a shared projection (moe_adapter_project). They follow
  * the conventions above (device pointers, `stream`, error codes, nothing
  * allocated, nothing kept) with their own shapes and these element types: */

