@@ -8,6 +8,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "moe_activation.h"
 #include "moe_groups.h"
@@ -19,7 +20,8 @@ namespace {
 
 // ---- rows ------------------------------------------------------------------------
 // A thread takes 8 neighbouring elements, four threads a block of 32, and each
-// thread kChunksEach such chunks at once: bound by HBM (65536 x 4096 bf16 there and back in 256 us, 5.3 TB/s).
+// thread kChunksEach such chunks at once: bound by HBM (65536 x 4096 bf16 there and back in 252 us, 5.4 TB/s;
+// with 2 chunks 266, with 8 261).
 constexpr int kRowThreads = 256, kChunksEach = 4;
 
 struct RowArgs {
@@ -62,49 +64,94 @@ __device__ __forceinline__ uint32_t max_of_four(uint32_t v) {
   return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kDppXor2, 0xf, 0xf, true));
 }
 
+// The largest magnitude of 8 elements, as an f32's bits: they order like the values, infinities and NaN above all. (So do
+// those of the 16-bit types, two at a time.)
 template <typename T>
-__global__ __launch_bounds__(kRowThreads) void k_mx_quantise(RowArgs a, const T* __restrict__ x, uint8_t* __restrict__ codes,
-                                                           uint8_t* __restrict__ scales) {
-  const Chunks chunks(a);
-  const bool room = a.k >= 8;
-  oct<T> raw[kChunksEach];
+__device__ __forceinline__ uint32_t top_of(oct<T> v) {
+  if constexpr (sizeof(T) == 2) {
+    typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+    uint32_t w[4];
+    __builtin_memcpy(w, &v, sizeof(w));
+    u16x2 m[4];
 #pragma unroll
-  for (int u = 0; u < kChunksEach; ++u) {
-    const Chunk c = chunks(a, u);
-    raw[u] = raw_oct(x + c.row * a.x_stride + c.at, c.n, room);
-  }
-#pragma unroll
-  for (int u = 0; u < kChunksEach; ++u) {
-    const Chunk c = chunks(a, u);
-    const f32x8 v = to_f32(placed_oct<T>(raw[u], c.n, room));
-    uint32_t top = 0;   // the largest magnitude's bits: they order like the values, infinities and NaN above all
+    for (int i = 0; i < 4; ++i) m[i] = __builtin_bit_cast(u16x2, w[i] & 0x7fff7fffu);
+    m[0] = __builtin_elementwise_max(__builtin_elementwise_max(m[0], m[1]), __builtin_elementwise_max(m[2], m[3]));
+    const unsigned short lo = m[0][0], hi = m[0][1], top = lo > hi ? lo : hi;
+    if constexpr (std::is_same_v<T, bf16_t>) return (uint32_t)top << 16;
+    else return __builtin_bit_cast(uint32_t, (float)__builtin_bit_cast(fp16_t, top));
+  } else {
+    uint32_t top = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float one = v[e];   // (a bit cast of the vector's element itself takes the first one's bits)
       top = max(top, __builtin_bit_cast(uint32_t, one) & 0x7fffffffu);
     }
-    top = max_of_four(top);
+    return top;
+  }
+}
+
+// 8 elements divided by `by`, a power of two, to codes (rounds to nearest even, 6 at most).
+template <typename T>
+__device__ __forceinline__ uint32_t codes_of(oct<T> v, float by) {
+  uint32_t q = 0;
+  if constexpr (sizeof(T) == 4) {
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[0], v[1], by, 0);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[2], v[3], by, 1);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[4], v[5], by, 2);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[6], v[7], by, 3);
+  } else {
+    typedef T pair __attribute__((ext_vector_type(2)));
+    pair p[4];
+    __builtin_memcpy(p, &v, sizeof(p));
+    if constexpr (std::is_same_v<T, bf16_t>) {
+      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, p[0], by, 0);
+      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, p[1], by, 1);
+      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, p[2], by, 2);
+      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, p[3], by, 3);
+    } else {
+      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(q, p[0], by, 0);
+      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(q, p[1], by, 1);
+      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(q, p[2], by, 2);
+      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(q, p[3], by, 3);
+    }
+  }
+  return q;
+}
+
+// WHOLE: k is a multiple of 8, a chunk all there or not at all. (65536 x 4096 bf16 148 us; 158 with the elements made f32
+// first and every chunk's end looked at.)
+template <typename T, bool WHOLE>
+__global__ __launch_bounds__(kRowThreads) void k_mx_quantise(RowArgs a, const T* __restrict__ x, uint8_t* __restrict__ codes,
+                                                           uint8_t* __restrict__ scales) {
+  const Chunks chunks(a);
+  const bool room = WHOLE || a.k >= 8;
+  oct<T> raw[kChunksEach];
+  Chunk c[kChunksEach];
+#pragma unroll
+  for (int u = 0; u < kChunksEach; ++u) {
+    c[u] = chunks(a, u);
+    raw[u] = raw_oct(x + c[u].row * a.x_stride + c[u].at, WHOLE && c[u].n > 0 ? 8 : c[u].n, room);
+  }
+#pragma unroll
+  for (int u = 0; u < kChunksEach; ++u) {
+    const oct<T> v = WHOLE ? raw[u] : placed_oct<T>(raw[u], c[u].n, room);   // (zeros where nothing is there)
+    const uint32_t top = max_of_four(top_of<T>(v));
     // (past 1.5 times its power of two, t is more than 6 of the scale that floor gives; below 2^-125 the scale is 2^-127)
     int scale = max((int)(top >> 23) - 2 + (a.ceil && (top & 0x7fffffu) > 0x400000u ? 1 : 0), 0);
-    uint32_t q = 0;
+    uint32_t q = codes_of<T>(v, __builtin_bit_cast(float, scale ? (uint32_t)scale << 23 : 0x00400000u));
     if (top >= 0x7f800000u) {   // an infinity or NaN: the block is NaN
       scale = 255;
-    } else {
-      const float by = __builtin_bit_cast(float, scale ? (uint32_t)scale << 23 : 0x00400000u);
-      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[0], v[1], by, 0);   // (rounds to nearest even, 6 at most)
-      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[2], v[3], by, 1);
-      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[4], v[5], by, 2);
-      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[6], v[7], by, 3);
+      q = 0;
     }
-    uint8_t* const to = codes + c.row * a.code_stride + c.at / 2;
-    if (c.n >= 8) {
+    uint8_t* const to = codes + c[u].row * a.code_stride + c[u].at / 2;
+    if (WHOLE ? c[u].n > 0 : c[u].n >= 8) {
       __builtin_memcpy(to, &q, 4);
-    } else {
+    } else if (!WHOLE) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (2 * i < c.n) to[i] = (uint8_t)(q >> (8 * i));
+        if (2 * i < c[u].n) to[i] = (uint8_t)(q >> (8 * i));
     }
-    if (c.n > 0 && c.at % kMxBlock == 0) scales[c.row * a.scale_stride + c.at / kMxBlock] = (uint8_t)scale;
+    if (c[u].n > 0 && c[u].at % kMxBlock == 0) scales[c[u].row * a.scale_stride + c[u].at / kMxBlock] = (uint8_t)scale;
   }
 }
 
@@ -384,9 +431,14 @@ int moe_mx_quantise(const moe_mx_rows* p, const void* x, int64_t rows, void* cod
   return row_call(p, x, codes, scales, rows, [&](const RowArgs& a, unsigned blocks) {
     const hipStream_t s = (hipStream_t)stream;
     uint8_t *c = (uint8_t*)codes, *e = (uint8_t*)scales;
-    if (p->type == MOE_TYPE_BF16) k_mx_quantise<<<blocks, kRowThreads, 0, s>>>(a, (const bf16_t*)x, c, e);
-    else if (p->type == MOE_TYPE_FP16) k_mx_quantise<<<blocks, kRowThreads, 0, s>>>(a, (const fp16_t*)x, c, e);
-    else k_mx_quantise<<<blocks, kRowThreads, 0, s>>>(a, (const float*)x, c, e);
+    auto with = [&](auto whole, const auto* from) {
+      typedef std::remove_const_t<std::remove_pointer_t<decltype(from)>> T;
+      k_mx_quantise<T, whole><<<blocks, kRowThreads, 0, s>>>(a, from, c, e);
+    };
+    auto of = [&](const auto* from) { p->k % 8 ? with(std::false_type(), from) : with(std::true_type(), from); };
+    if (p->type == MOE_TYPE_BF16) of((const bf16_t*)x);
+    else if (p->type == MOE_TYPE_FP16) of((const fp16_t*)x);
+    else of((const float*)x);
   });
 }
 
