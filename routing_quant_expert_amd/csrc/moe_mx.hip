@@ -314,9 +314,9 @@ struct MxTensors {
   void* out;
 };
 
-template <bool GATED, bool DMA, int BP, int BQ, int WP, int WQ, int ST, int STEPS>
+template <bool GATED, bool DMA, int BP, int BQ, int WP, int WQ, int ST, int STEPS, bool ONCE = false>
 int launch_tile(const MxArgs& a, const MxTensors& v, hipStream_t s) {
-  typedef MxGemm<BP, BQ, WP, WQ, ST, STEPS, DMA, GATED> G;
+  typedef MxGemm<BP, BQ, WP, WQ, ST, STEPS, DMA, GATED, ONCE> G;
   auto u8 = [](const void* p) { return (const uint8_t*)p; };
   return launch_rows_of_tiles<k_mx<G, GATED>, G>("mx", row_tiles(a, G::kQ) * ((a.n + G::kP - 1) / G::kP), s, a, u8(v.x), u8(v.xs),
                                                  u8(v.w), u8(v.ws), u8(v.w2), u8(v.ws2), v.out);
@@ -337,8 +337,10 @@ int launch_wide(const MxArgs& a, const MxTensors& v, hipStream_t s) {
 }
 
 // Which tiles, by the same reckoning as the 16-bit products' (moe_gated.h). The times are at n = 2048, k = 4096, in us.
-// Few rows: plain in tiles of 64 x 16, 48 of 384 39.2 against 42.6 in 128 x 16 and 44.1 in 128 x 64, 1 of 1 7.1 (8.9, 11.4), up to
-// some thousand tiles: 128 of 64 58 (51 in 128 x 16); gated in 64 x 32 while the tiles are few, 1 of 1 8.1 (9.5 in 128 x 16), then in 128 x 16: 48 of 384 75.7 (82.4).
+// Few tiles: plain in 64 x 16, 32 of 8 8.6 against 12.2 in 128 x 64, 1 of 1 7.1 (11.4); gated in 64 x 32, 1 of 1 8.1 (11.9).
+// More of them, but few rows a group: 128 x 32, whose codes of the weights are read once, gated 48 of 384 70.3 (74.0; 78.0 with
+// loads that stay in the caches), 2000 of 384 518 (581; 562), 4000 of 384 550 (608; 585), plain 280 (314; 305); but plain
+// 500 of 32, of fewer tiles, 31 (26), and 12288 of 384 gated 777 (711; 741).
 // Wide tiles from a sum of 2048 on: 12288 rows of 64 groups plain 112 (130), gated 190 (238), 12288 of 384 gated 682 (721 in 128 x 64);
 // but 4096 of 384 640 (607), 8192 of 16 plain 66 (60), and with k = 1024 16384 of 16, n = 1024, 30.4 (26.6).
 template <bool GATED, bool DMA>
@@ -348,11 +350,11 @@ int launch_mx(const MxArgs& a, const MxTensors& v, hipStream_t s) {
   auto columns = [&](int p) { return (wide + p - 1) / p; };
   if constexpr (GATED) {
     if (row_tiles(a, 32) * columns(64) <= 1024) return launch_tile<GATED, DMA, 64, 32, 2, 2, 3, 4>(a, v, s);
-    if (mean < 6) return launch_tile<GATED, DMA, 128, 16, 4, 1, 4, 2>(a, v, s);
+    if (mean < 24) return launch_tile<GATED, DMA, 128, 32, 4, 1, 3, 4, true>(a, v, s);
   } else {
-    const bool small = row_tiles(a, 64) * columns(128) <= 192;
-    if (small || (mean < 6 && row_tiles(a, 16) * columns(64) <= 2048)) return launch_tile<GATED, DMA, 64, 16, 4, 1, 4, 2>(a, v, s);
-    if (mean < 6) return launch_tile<GATED, DMA, 128, 16, 4, 1, 4, 2>(a, v, s);
+    if (mean < 24 && row_tiles(a, 32) * columns(128) > (mean < 6 ? 512 : 1024))
+      return launch_tile<GATED, DMA, 128, 32, 4, 1, 3, 4, true>(a, v, s);
+    if (mean < 6 || row_tiles(a, 64) * columns(128) <= 192) return launch_tile<GATED, DMA, 64, 16, 4, 1, 4, 2>(a, v, s);
   }
   if constexpr (DMA) {
     const int64_t tiles = likely_row_tiles(a, 256) * columns(256), small = likely_row_tiles(a, 128) * columns(128);

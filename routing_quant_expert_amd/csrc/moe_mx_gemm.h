@@ -109,16 +109,23 @@ struct MxTile {
     scale_offsets(o, kRowWords, off.scales);
   }
 
-  // (As TileOf::dma; `at` is the same in every lane of a wave.)
+  // (As TileOf::dma; `at` is the same in every lane of a wave.) ONCE: nothing else reads these codes, and they are the first
+  // to leave the caches: a line of scales, which is read in pieces of 4 steps, then stays until its last piece.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
+  template <bool ONCE>
   __device__ static __forceinline__ void dma_codes(const uint8_t* at, const uint32_t (&off)[kPer], uint32_t tile) {
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t first = tile + 16 * 64 * (wave % (kChunks < NT ? kChunks / 64 : NT / 64));
 #pragma unroll
-    for (int k = 0; k < kPer; ++k)
-      asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
-                   : : "v"(off[k]), "s"(at), "s"(first + 16 * NT * k) : "memory", "m0");
+    for (int k = 0; k < kPer; ++k) {
+      if constexpr (ONCE)
+        asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1 nt"
+                     : : "v"(off[k]), "s"(at), "s"(first + 16 * NT * k) : "memory", "m0");
+      else
+        asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+                     : : "v"(off[k]), "s"(at), "s"(first + 16 * NT * k) : "memory", "m0");
+    }
   }
   __device__ static __forceinline__ void dma_scales(const uint8_t* at, const uint32_t (&off)[kPerScales], uint32_t buffer) {
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -209,7 +216,8 @@ struct MxTile {
 };
 
 // DMA: codes 16-byte and scales 4-byte aligned, brought into LDS directly; otherwise through registers, any alignment.
-template <int BP, int BQ, int WP, int WQ, int ST, int G, bool DMA, bool PAIRS>
+// ONCE: hardly any group has rows for a second tile, which would read its weights again.
+template <int BP, int BQ, int WP, int WQ, int ST, int G, bool DMA, bool PAIRS, bool ONCE = false>
 struct MxGemm : TileOut<BP, BQ, WP, WQ, PAIRS> {
   typedef TileOut<BP, BQ, WP, WQ, PAIRS> Out;
   using Out::NT, Out::NP, Out::NQ, Out::wave_p, Out::wave_q;
@@ -317,8 +325,8 @@ struct MxGemm : TileOut<BP, BQ, WP, WQ, PAIRS> {
           put = put == lds_offset(last) ? lds_offset(buffers) : put + kBuffer;
         }
         const uint32_t at = lds_offset(slot);
-        PT::dma_codes(pc, po.codes, at);
-        QT::dma_codes(qc, qo.codes, at + PT::kCodes);
+        PT::template dma_codes<ONCE>(pc, po.codes, at);
+        QT::template dma_codes<false>(qc, qo.codes, at + PT::kCodes);
         pc += 128;
         qc += 128;
       };
