@@ -59,28 +59,32 @@ int launch_gated_tile(const GatedArgs& a, const GatedTensors& v, hipStream_t s) 
 // Unaligned rows wait longer for each load: up to three. 1000 rows of 13, 257 and 515 wide: 13.6 (17.1).
 // Tall tiles for few rows: under 6 a group 172.7 at 64 of 32 against 173.7 with 64 rows, 192.3 (176.5) at 250 of 32; and where
 // tiles of 64 rows would be few: hidden of 256 of 1 19.7 (29.5).
-// Wide tiles (moe_wide.h) where the sum is long: a round of 256 of them takes about three halves of one of 512 tiles of 128 x 128,
-// so where 3 times its rounds are no more than twice theirs. Forward of 16384 of 32 530 (597), 2048 of 4 85 (123), but
-// 2048 of 1 88 (67). From 768 tiles on, what counts is the weights' reading, which they do in longer rows: 96 groups of 128 rows 723 (774),
-// input 644 (776). The backward pass, whose weights' rows lie across the sum, gains by that with few rows too, if most of the
-// CUs have a tile: input of 64 of 32 165 (186), 32 of 8 60 (50). The forward pass does not under 24 rows: 4000 of 384 2198 (2194).
-// At a sum of 1024 little is left of it: forward of 16384 of 16, n = 1024, 106 (115), n = 512 66 (56).
+// Wide tiles (moe_wide.h): a round of 256 of them takes about three halves of one of 512 tiles of 128 x 128, so where 3 times
+// its rounds are less than twice theirs. Forward of 16384 of 32 530 (597), of k = 512 134 (161), 2048 of 4 87 (123), but 2048
+// of 1 88 (67). Where both are equal a round has just begun, and the larger tiles are the better ones for the hidden rows and
+// long sums: 4096 of 4 171 (182), hidden 8192 of 32 236 (263), but 8000 of 8 with n = 1024, k = 2048 106 (95). From 768
+// tiles on, what counts is the weights' reading, which they do in longer rows: 12288 of 96 723 (774), input 644 (776). The
+// backward pass, whose weights' rows lie across the sum, gains by that with few rows too, if most of the CUs have a
+// tile: input of 64 of 32 165 (181), 32 of 8 60 (50). The forward pass does not under 24 rows: 4000 of 384 2198 (2194).
+// At 4 steps they are still ahead: forward of 16384 of 32, n = 4096, k = 256, 211 (238); shorter sums are not tried.
 template <GatedWay W, typename K, typename T, bool DMA>
 int launch_gated_rows(const GatedArgs& a, const GatedTensors& v, hipStream_t s) {
   const int64_t mean = a.rows / a.groups;
   const int width = W == kInput ? a.k : a.n, wide = W == kForward ? 2 * width : width;   // columns of P
   auto columns = [&](int p) { return (wide + p - 1) / p; };
   constexpr int kFewRows = W == kForward ? 32 : 16;   // (of 16 rows a wave would have no row of both projections)
-  if (row_tiles(a, kFewRows) * columns(64) <= (DMA ? 480 : 768)) {
+  if (row_tiles(a, kFewRows) * columns(64) < (DMA ? 480 : 768)) {
     if constexpr (W == kForward) return launch_gated_tile<W, K, T, DMA, 64, 32, 2, 2, 4>(a, v, s);
     else return launch_gated_tile<W, K, T, DMA, 64, 16, 4, 1, 4>(a, v, s);
   }
   if constexpr (DMA) {
     const int red = W == kInput ? a.n : a.k;
     const int64_t tiles = likely_row_tiles(a, 256) * columns(256), small = likely_row_tiles(a, 128) * columns(128);
+    const int64_t ours = 3 * rounds(a, tiles, 256), theirs = 2 * rounds(a, small, 512);
+    const bool close = W == kHidden || (W == kInput ? 2 : 1) * (int64_t)red >= 4096;
     const bool pays = mean < 64 ? W != kForward ? tiles >= 128 : mean >= 24 && tiles >= 768
-                                : tiles >= 768 || 3 * rounds(a, tiles, 256) <= 2 * rounds(a, small, 512);
-    if (pays && red >= 1024 && red % kStep == 0) {
+                                : tiles >= 768 || ours < theirs || (ours == theirs && close);
+    if (pays && red >= 4 * kStep && red % kStep == 0) {
       typedef WideGemm<T, W != kForward, W == kForward ? kRowPairs : W == kInput ? kTwoSums : kSingle> G;
       return K::template wide<T, G>(row_tiles(a, G::kQ) * ((width + G::kP - 1) / G::kP), a, v, s);
     }

@@ -341,8 +341,9 @@ int launch_wide(const MxArgs& a, const MxTensors& v, hipStream_t s) {
 // More of them, but few rows a group: 128 x 32, whose codes of the weights are read once, gated 48 of 384 70.3 (74.0; 78.0 with
 // loads that stay in the caches), 2000 of 384 518 (581; 562), 4000 of 384 550 (608; 585), plain 280 (314; 305); but plain
 // 500 of 32, of fewer tiles, 31 (26), and 12288 of 384 gated 777 (711; 741).
-// Wide tiles from a sum of 2048 on: 12288 rows of 64 groups plain 112 (130), gated 190 (238), 12288 of 384 gated 682 (721 in 128 x 64);
-// but 4096 of 384 640 (607), 8192 of 16 plain 66 (60), and with k = 1024 16384 of 16, n = 1024, 30.4 (26.6).
+// Wide tiles: 12288 rows of 64 groups plain 112 (130), gated 190 (238), 12288 of 384 gated 682 (711 in 128 x 64); but 4000 of 384
+// 640 (607), 8192 of 16 plain 67 (63). With few of them from a sum of 2048 on, 8000 of 8, n = 4096, 64 (67); at k = 1024
+// 16384 of 16, n = 1024, 30.4 (26.6), but 16384 of 32, n = 4096, 86 (104).
 template <bool GATED, bool DMA>
 int launch_mx(const MxArgs& a, const MxTensors& v, hipStream_t s) {
   const int64_t mean = a.rows / a.groups;
@@ -359,7 +360,7 @@ int launch_mx(const MxArgs& a, const MxTensors& v, hipStream_t s) {
   if constexpr (DMA) {
     const int64_t tiles = likely_row_tiles(a, 256) * columns(256), small = likely_row_tiles(a, 128) * columns(128);
     const bool pays = tiles >= 768 ? mean >= 24 : mean >= 64 && 3 * rounds(a, tiles, 256) < 2 * rounds(a, small, 512);
-    if (pays && a.k >= 2048 && a.k % WideMx<GATED>::kGroup == 0) return launch_wide<GATED>(a, v, s);
+    if (pays && (tiles >= 768 || a.k >= 2048) && a.k % WideMx<GATED>::kGroup == 0) return launch_wide<GATED>(a, v, s);
   }
   if (mean < 64 || row_tiles(a, 128) * columns(128) < 256) return launch_tile<GATED, DMA, 128, 64, 2, 2, 3, 2>(a, v, s);
   return launch_tile<GATED, DMA, 128, 128, 2, 2, 2, 4>(a, v, s);

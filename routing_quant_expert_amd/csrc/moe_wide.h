@@ -116,7 +116,7 @@ struct WideGemm : WideOut<TWO == kRowPairs> {
   };
   // Where a lane's operands lie in a slot (TileOf::operand): the rows' n-th 4096 n bytes after `q` of its half step, P's i-th
   // 2048 i after `p` of its half step, or of columns 16384 kk after its own `p`. A wave issues one instruction in 4 cycles,
-  // 512 in a step's products, so an address for every read would cost.
+  // 512 in a step's products, so an address for every read costs (16384 rows over 4 groups, gated: 411 us, 402 so).
   struct Places {
     uint32_t p[PCOL ? 8 : 2], q[2];
     __device__ __forceinline__ Places() {
