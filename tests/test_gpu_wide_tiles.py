@@ -30,6 +30,19 @@ def test_edges_in_4_bits(of_two, out, act):
                      limit=1.0), of_two)
 
 
+@pytest.mark.parametrize("way", gated.WAYS)
+@pytest.mark.parametrize("terms", [256, 320])
+def test_short_sums(way, terms):
+    """The shortest sums that these tiles take: the pipeline's start and end with hardly a step between them."""
+    n, k = (terms, 2568) if way == "input" else (1288 if way == "forward" else 2568, terms)
+    gated.CHECKS[way](gated.make(EDGES, n, k, BF16, seed=30, before=5, after=7))
+
+
+@PLAIN_GATED
+def test_one_group_of_scales_in_4_bits(of_two):
+    mx.check(mx.make(EDGES, 1288 if of_two else 2568, 1024, seed=30, before=5, after=7), of_two)
+
+
 @pytest.mark.parametrize("way", ["hidden", "input"])
 def test_few_rows_of_many_groups(way):
     sizes = [0, 1, 2, 5] * 75
