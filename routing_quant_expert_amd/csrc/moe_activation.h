@@ -23,7 +23,8 @@ struct Gate {
 
 // act(z) and, with SLOPE, its derivative s + act(z) (1 - s) inner'(z). s is 1 / (1 + 2^t): t's rounding moves it by
 // |t| s (1 - s) 2^-24, which stays below 2^-25. At -infinity act and derivative are 0 (s is 0 below -104); at +infinity the
-// derivative is NaN (infinity times 0), and so is everything of NaN.
+// derivative is NaN (infinity times 0), and so is everything of NaN. Gelu's inner'(z) is taken of z held to +-104, past which
+// 1 - s is 0: the square of a finite z may leave f32, and infinity times 0 is no slope of 1.
 template <int ACT, bool SLOPE>
 __device__ __forceinline__ float activation(float z, float& slope) {
   constexpr float kLog2e = 1.4426950408889634f, kInner = 1.5957691216057308f, kCubic = 0.044715f;   // 2 sqrt(2/pi)
@@ -35,7 +36,10 @@ __device__ __forceinline__ float activation(float z, float& slope) {
   const float v = y * s;
   if (SLOPE) {
     float by = 1.0f - s;
-    if (ACT == MOE_ACT_GELU) by *= __builtin_fmaf(y * y, 3.0f * kCubic * kInner, kInner);
+    if (ACT == MOE_ACT_GELU) {
+      const float w = __builtin_amdgcn_fmed3f(z, -104.0f, 104.0f);
+      by *= __builtin_fmaf(w * w, 3.0f * kCubic * kInner, kInner);
+    }
     slope = __builtin_fmaf(v, by, s);
   }
   return v;
