@@ -547,7 +547,8 @@ int moe_grouped_backward_w(const moe_grouped* g, const void* dy, const void* x, 
  * written whole: rows of no group are 0. rows may be 0, and is at most MOE_GROUPED_MAX_ROWS. Any n, k >= 1,
  * stride and element alignment; rows whose start is 16-byte aligned (and, in the
  * backward calls, widths that are multiples of 8) take the faster path. A call looks
- * only at the strides of its own tensors. The same call gives the same bits.
+ * only at the strides of its own tensors: the forward call without gate and up not at
+ * gate_stride; backward_h at h_stride also where h is NULL. The same call gives the same bits.
  * status: MOE_STATUS_BAD_OFFSETS, may be NULL; outputs are unspecified then. */
 typedef struct moe_gated {
   int32_t n_groups, n, k;

@@ -96,7 +96,8 @@ struct Kernels {
 };
 
 
-int check_gated(const moe_gated* g, int64_t rows, GatedWay way) {
+// kept: the call has gate and up (the forward pass may go without).
+int check_gated(const moe_gated* g, int64_t rows, GatedWay way, bool kept) {
   if (!g) return fail(MOE_EINVAL, "gated is NULL%s%lld");
   if (g->type != MOE_TYPE_BF16 && g->type != MOE_TYPE_FP16)
     return fail(MOE_EINVAL, "gated: type must be MOE_TYPE_BF16 or MOE_TYPE_FP16%s (%lld)", "", g->type);
@@ -110,15 +111,15 @@ int check_gated(const moe_gated* g, int64_t rows, GatedWay way) {
     return fail(MOE_EUNSUPPORTED, "gated: n_groups above MOE_GROUPED_MAX_GROUPS%s (%lld)", "", g->n_groups);
   if (g->n < 1 || g->k < 1) return fail(MOE_EINVAL, "gated: n and k must be >= 1%s%lld");
   // only the strides that this call uses
-  const bool x = way != kHidden, h = way != kInput, gate = true, y = way == kHidden, w = way != kHidden;
-  if ((x && g->x_stride < g->k) || (h && g->h_stride < g->n) || (gate && g->gate_stride < g->n) ||
+  const bool x = way != kHidden, h = way != kInput, y = way == kHidden, w = way != kHidden;
+  if ((x && g->x_stride < g->k) || (h && g->h_stride < g->n) || (kept && g->gate_stride < g->n) ||
       (y && g->y_stride < g->k) || (w && g->w_stride < g->k) || (!w && g->down_stride < g->n))
     return fail(MOE_EINVAL, "gated: a row stride is below its row%s%lld");
   if (w ? g->w_group_stride < (int64_t)(g->n - 1) * g->w_stride + g->k
         : g->down_group_stride < (int64_t)(g->k - 1) * g->down_stride + g->n)
     return fail(MOE_EINVAL, "gated: a group stride is below one weight%s%lld");
   const int64_t most = MOE_GROUPED_MAX_STRIDE;
-  if ((x && g->x_stride > most) || (h && g->h_stride > most) || g->gate_stride > most || (y && g->y_stride > most) ||
+  if ((x && g->x_stride > most) || (h && g->h_stride > most) || (kept && g->gate_stride > most) || (y && g->y_stride > most) ||
       (w ? g->w_stride : g->down_stride) > most)
     return fail(MOE_EUNSUPPORTED, "gated: a row stride above MOE_GROUPED_MAX_STRIDE%s%lld");
   if (rows < 0) return fail(MOE_EINVAL, "gated: rows must be >= 0%s (%lld)", "", rows);
@@ -129,7 +130,7 @@ int check_gated(const moe_gated* g, int64_t rows, GatedWay way) {
 
 template <GatedWay W>
 int gated_call(const moe_gated* g, const GatedTensors& v, const int32_t* offsets, int64_t rows, int32_t* status, void* stream) {
-  if (int r = check_gated(g, rows, W)) return r;
+  if (int r = check_gated(g, rows, W, W != kForward || v.out || v.out2)) return r;
   if (!offsets) return fail(MOE_EINVAL, "gated: offsets must be non-NULL%s%lld");
   if ((uintptr_t)offsets % 4 || (uintptr_t)status % 4)
     return fail(MOE_EINVAL, "gated: a pointer is not aligned to its elements%s%lld");
