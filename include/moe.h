@@ -546,7 +546,8 @@ int moe_grouped_backward_w(const moe_grouped* g, const void* dy, const void* x, 
  * place; other outputs must not overlap inputs or one another. Every output is
  * written whole: rows of no group are 0. rows may be 0, and is at most MOE_GROUPED_MAX_ROWS. Any n, k >= 1,
  * stride and element alignment; rows whose start is 16-byte aligned (and, in the
- * backward calls, widths that are multiples of 8) take the faster path. A call looks
+ * backward calls, widths that are multiples of 8) take the faster path, calls of many rows a
+ * yet faster one if k (backward_x: n) is a multiple of 64, 256 or more. A call looks
  * only at the strides of its own tensors: the forward call without gate and up not at
  * gate_stride; backward_h at h_stride also where h is NULL. The same call gives the same bits.
  * status: MOE_STATUS_BAD_OFFSETS, may be NULL; outputs are unspecified then. */
@@ -610,7 +611,8 @@ int moe_mx_dequantise(const moe_mx_rows* p, const void* codes, const void* scale
  * Every output is written whole: rows of no group are 0. A NaN block makes the
  * outputs that it enters NaN. rows may be 0, and is at most MOE_GROUPED_MAX_ROWS.
  * Any n, k, stride and alignment; codes whose rows start 16-byte aligned with
- * scales 4-byte aligned take the faster path. Outputs must not overlap inputs.
+ * scales 4-byte aligned take the faster path, calls of many rows a yet faster one if
+ * k is a multiple of 1024. Outputs must not overlap inputs.
  * The same call gives the same bits. status: MOE_STATUS_BAD_OFFSETS, may be NULL; outputs are unspecified then. */
 typedef struct moe_mx {
   int32_t n_groups, n, k;

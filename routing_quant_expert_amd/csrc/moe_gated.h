@@ -54,11 +54,20 @@ int launch_gated_tile(const GatedArgs& a, const GatedTensors& v, hipStream_t s) 
 }
 
 // Which tiles. The times are of bf16 at n = 2048, k = 4096, rows as `rows of groups` (a power law of 0.4), in us.
-// Few tiles (up to two of 64 columns for a CU): the smallest, for more workgroups. 1 of 1: forward 12.3 against 15.1 in
-// tiles of 128 columns, hidden 12.8 (16.7), input 12.6 (16.8); past it those read the rows less often: hidden of 100 of 8 37.4 (28.8).
-// Unaligned rows wait longer for each load: up to three. 1000 rows of 13, 257 and 515 wide: 13.6 (17.1).
-// Tall tiles for few rows: under 6 a group 172.7 at 64 of 32 against 173.7 with 64 rows, 192.3 (176.5) at 250 of 32; and where
-// tiles of 64 rows would be few: hidden of 256 of 1 19.7 (29.5).
+// The counts of tiles and rows below are points among the sizes that were timed, a little off the chip's own 256 and 512 where
+// the times cross there; the crossings differ by way and width, and no single point has the faster side at all of them.
+// Few tiles (480 of 64 columns, about two for a CU): the smallest, for more workgroups. 1 of 1: forward 12.3 against 15.1 in
+// tiles of 128 columns, hidden 12.8 (16.7), input 12.6 (16.8); past it those read the rows less often: hidden of 100 of 8 37.4
+// (28.8). Around it: 100 of 8, n = 1024, k = 2048, forward (384 tiles) 12.3 (13.3), input (480) 17.5 (14.5); hidden of 128 of 1
+// (320) 13.9 (18.1), 224 of 1 (512) 20.2 (19.9); but 192 of 1 forward (512) still 19.4 (27.0), hidden (448) already 23.1 (18.8).
+// Unaligned rows wait longer for each load: up to 768. bf16, 257 and 515 wide: hidden of 1000 of 13 (380) 12.5 (15.6), input (684)
+// 13.7 (16.8), of 1600 (1026) 15.9 (19.3), of 2400 (1476) 20.9 (17.2, 64 rows); 515 and 1001 wide, input of 1500 of 32 (2000) 38.3 (34.5).
+// Tall tiles for few rows: under 6 a group forward of 64 of 32 171.7 against 171.7 with 64 rows, 192 of 32 174.2 (175.2), 256 of 32
+// 190.5 (176.5); and where tiles of 64 rows would be few, up to 160: hidden of 256 of 1 (96) 19.7 (29.9), input of 128 of 1 (128)
+// 17.7 (25.4), but hidden of 512 of 1 (160) 33.5 (30.2), 640 of 1 (192) 42.8 (30.7).
+// Tiles of 64 rows for middling groups (under 64 rows) and up to 300 tiles of 128 rows: hidden of 1024 of 1 (160) 32.5 against 51.1
+// with 128 rows, 2048 of 1 (288) 52.6 (54.8), 2304 of 1 (320) 71.3 (66.5); input of 1024 of 1 (320) 44.7 (43.6); forward of 400 of 8,
+// n = 1024, k = 2048, 15.8 (26.0), but 1536 of 32 204.9 (198.1).
 // Wide tiles (moe_wide.h): a round of 256 of them takes about three halves of one of 512 tiles of 128 x 128, so where 3 times
 // its rounds are less than twice theirs. Forward of 16384 of 32 530 (597), of k = 512 134 (161), 2048 of 4 87 (123), but 2048
 // of 1 88 (67). Where both are equal a round has just begun, and the larger tiles are the better ones for the hidden rows and

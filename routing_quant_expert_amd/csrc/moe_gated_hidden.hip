@@ -1,7 +1,8 @@
 // The gated feed-forward's gradients of gate and up (moe_gated.h).
 //
 // The sums are half of the forward pass's, and every output takes two loads and three stores beside them, at the same time
-// in all workgroups: 16384 rows of 32 groups of 2048 x 4096 in 354 us, about 41 of each round of tiles without a product.
+// in all workgroups: 16384 rows of 32 groups of 2048 x 4096 in 354 us, about 41 of each round of tiles without a product, and
+// 632 tiles, 2.47 rounds of the 256 CUs that take 3.
 #include "moe_gated.h"
 
 namespace moe {
@@ -46,6 +47,8 @@ __global__ __launch_bounds__(G::NT, 2) void k_gated_dh(GatedArgs a, const T* __r
   });
 }
 
+// (All registers are taken: 2 values a lane in bf16 and 5 in fp16 go to scratch memory before the loop over the sum and come back
+// where the outputs are made. No wait for a tile's loads stands between.)
 template <typename T, typename G, int ACT>
 __global__ __launch_bounds__(256, 1) void k_gated_dh_wide(GatedArgs a, const T* __restrict__ dy, const T* __restrict__ wd,
                                                          const T* gate, const T* up, T* dgate, T* dup, T* __restrict__ h) {

@@ -337,12 +337,20 @@ int launch_wide(const MxArgs& a, const MxTensors& v, hipStream_t s) {
 }
 
 // Which tiles, by the same reckoning as the 16-bit products' (moe_gated.h). The times are at n = 2048, k = 4096, in us.
+// The counts of tiles are points among the sizes that were timed; where the times cross differs by width.
 // Few tiles: plain in 64 x 16, 32 of 8 8.6 against 12.2 in 128 x 64, 1 of 1 7.1 (11.4); gated in 64 x 32, 1 of 1 8.1 (11.9).
+// Plain up to 192 tiles of 128 x 64: 256 of 1 (96) 9.1 (11.8), 1024 of 1, 1001 and 1003 wide (144), 11.4 (11.7), 600 of 32, 515 and
+// 1001 wide (210), 8.7 (11.0); but 512 of 1 (160) 15.8 (11.9), 640 of 1 (192) 18.5 (12.6). Gated up to 1024 of its own: 400 of 8,
+// n = 1024, k = 2048 (704), 8.5 (8.9), 384 of 1 (896) 13.0 (12.8), 512 of 1 (1152) 17.7 (13.2).
 // More of them, but few rows a group: 128 x 32, whose codes of the weights are read once, gated 48 of 384 70.3 (74.0; 78.0 with
 // loads that stay in the caches), 2000 of 384 518 (581; 562), 4000 of 384 550 (608; 585), plain 280 (314; 305); but plain
-// 500 of 32, of fewer tiles, 31 (26), and 12288 of 384 gated 777 (711; 741).
+// 500 of 32, of fewer tiles, 31 (26), and 12288 of 384 gated 777 (711; 741). Plain from 512 tiles on for under 6 rows a group: 64 of
+// 32 (544) 23.1 in them, 26.5 in 64 x 16, 32 of 32 (512) 19.2 (16.6); from 1024 for more rows, where 128 x 64 comes near: 400 of 60
+// (1152) 44.0 (50.5), 1000 of 64 (1520) 54.3 (55.1), 384 of 32 (704) 23.9 (25.8).
 // Wide tiles: 12288 rows of 64 groups plain 112 (130), gated 190 (238), 12288 of 384 gated 682 (711 in 128 x 64); but 4000 of 384
-// 640 (607), 8192 of 16 plain 67 (63). With few of them from a sum of 2048 on, 8000 of 8, n = 4096, 64 (67); at k = 1024
+// 640 (607), 8192 of 16 plain 67 (63). They take sums of whole groups of 1024: 16384 of 32, n = 4096, k = 2048 118 (142), but
+// k = 2560 167 in 128 x 128, k = 1536 122. 128 x 64 or 128 x 128: under 256 tiles of 128 x 128, plain 1024 of 1 (160) 13.0 (17.1),
+// 1536 of 1 (224) 18.7 (17.4), 2048 of 1 (288) 19.7 (18.1), gated 512 of 1 (192) 13.2 (17.2), 768 of 1 (256) 18.4 (17.5). With few of them from a sum of 2048 on, 8000 of 8, n = 4096, 64 (67); at k = 1024
 // 16384 of 16, n = 1024, 30.4 (26.6), but 16384 of 32, n = 4096, 86 (104).
 template <bool GATED, bool DMA>
 int launch_mx(const MxArgs& a, const MxTensors& v, hipStream_t s) {

@@ -1,5 +1,7 @@
-// The tile product of moe_gemm.h for many rows and long sums: 256 x (up to) 256
-// outputs, one workgroup of four waves a CU.
+// The tile product of moe_gemm.h for aligned rows and sums of whole steps (four
+// and more): 256 x (up to) 256 outputs, one workgroup of four waves a CU. For
+// many rows, and where weights are read across the sum for few rows of many
+// groups too, in longer pieces of a row (launch_gated_rows, launch_mx).
 //
 // A wave holds 128 x 128 sums in accumulation registers, so that an LDS read
 // feeds eight products where 64 x 64 sums make it four: 64 x 64 take the LDS
